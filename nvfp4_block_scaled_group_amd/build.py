@@ -2,8 +2,9 @@
 
     python -m nvfp4_block_scaled_group_amd.build
 
-Compiles ``csrc/*.hip`` with hipcc for gfx950 and links a plain shared library
-exporting the C ABI of ``include/nvfp4_group.h``; also builds
+Compiles ``csrc/*.hip`` and ``csrc/moe/*.hip`` with hipcc for gfx950 and links
+a plain shared library exporting the C ABI of ``include/nvfp4_group.h`` and
+``include/moe_ops.h``; also builds
 ``probe/libhbmprobe.so`` (the benchmark's memory-ceiling kernels, not part
 of that ABI).  The library's dependency on
 the HIP runtime is recorded as ``libamdhip64.so`` (the name PyTorch's ROCm
@@ -13,6 +14,7 @@ on its own it finds ROCm's runtime through its RUNPATH.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import importlib.util
 import os
@@ -53,14 +55,17 @@ def _hip_runtime_dir() -> str:
 def build(verbose: bool = False) -> str:
     hipcc = shutil.which("hipcc") or os.path.join(ROCM, "bin", "hipcc")
     os.makedirs(BUILD_DIR, exist_ok=True)
-    objs = []
-    for src in sorted(glob.glob(os.path.join(CSRC, "*.hip"))):
-        obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
+    sources = sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + sorted(glob.glob(os.path.join(CSRC, "moe", "*.hip")))
+    objs = [os.path.join(BUILD_DIR, os.path.basename(src) + ".o") for src in sources]
+
+    def compile_one(src: str, obj: str) -> None:
         cmd = [hipcc, *HIPCC_FLAGS, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
-        objs.append(obj)
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+        list(pool.map(compile_one, sources, objs))
     tmp = LIB + ".tmp"
     link = ["g++", "-shared", "-o", tmp, *objs, f"-L{_hip_runtime_dir()}", "-lamdhip64",
             f"-Wl,-rpath,{os.path.join(ROCM, 'lib')}", "-Wl,--no-undefined"]

@@ -1,0 +1,486 @@
+// moe_glu.hip -- the experts' gated feed-forward block on row-scaled NVFP4
+// operands: gate and up projection, activation and product in one kernel, and
+// its backward pass, behind the C ABI of include/moe_ops.h.
+//
+//   forward   g = Xa Wg^T, u = Xa Wu^T, h = act(g) * u
+//   backward  dh = dY Wd,  du = dh * act(g),  dg = dh * u * act'(g)
+//
+// Both are NT products of two NVFP4 operands stored along the contraction
+// index.  A line's factor A / 2688 leaves the sum, and value(code) * value(S)
+// (at most 6 significant bits, 2^-10 .. 2688) is exact in fp16, so the fp32
+// MFMA sum of exact products is the only rounding before the epilogue, which
+// stays in fp32 up to its one rounding to bf16.
+//
+// Work-group: 128 packed rows x 256 weight lines, 4 waves in a 2 x 2 grid of
+// 64 x 128 (2 x 4 MFMA tiles of 32 x 32), two work-groups on a CU.  In the
+// forward pass the 256 lines are 128 gate lines and the 128 up lines of the
+// same columns, laid out in LDS so that each wave holds g and u of the same
+// elements in the same lane (its first two MFMA columns are gate lines, the
+// other two the matching up lines): the activation and the product need no
+// exchange, and neither g nor u goes through memory.
+#include <algorithm>
+
+#include "moe_common.hpp"
+
+namespace {
+
+using namespace moe;
+
+typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kWavesN = 2;
+constexpr int kWM = 2, kWN = 4;   // 32 x 32 MFMA tiles of a wave (rows, lines)
+constexpr int kBM = 128;          // rows of a work-group: the expert granule
+constexpr int kBN = 256;          // weight lines of a work-group
+constexpr int kBK = 128;          // contraction step
+constexpr int kGroupRows = 8;     // row tiles that sweep the column tiles together
+
+// One operand: the lines of a tile, `valid` of which exist (others read 0).
+struct Lines {
+  const uint8_t* data;   // line pitch L/2 bytes
+  const uint8_t* scale;  // line pitch L/16 bytes
+  uint32_t valid;
+};
+
+// LDS: codes of one step, 64 bytes a line, A then B (two stages in separate
+// arrays, so that reads of one need not wait for copies into the other);
+// scales of four steps at a time, 32 bytes a line, double-buffered.
+constexpr uint32_t kRowBytes = kBK / 2, kRowScales = kBK / 16;
+constexpr uint32_t kStB = kBM * kRowBytes, kStageBytes = kStB + kBN * kRowBytes;  // 24 KB
+constexpr uint32_t kScSteps = 4, kScLine = kScSteps * kRowScales;
+constexpr uint32_t kScB = kBM * kScLine, kScBlockBytes = kScB + kBN * kScLine;    // 12 KB
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// 16-byte granule q of a line sits at slot q ^ (line / 4 % 4), so that a
+// fragment read of 32 consecutive lines spreads over the banks.
+__device__ __forceinline__ uint32_t swz(uint32_t line, uint32_t q) { return q ^ ((line >> 2) & 3u); }
+
+// s_waitcnt for at most n outstanding vector-memory operations.
+constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
+__device__ __forceinline__ h2_t scales_h2(uint32_t two_codes) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two_codes, 1.0f, false);
+}
+
+// Eight codes times value(S) as fp16 (exact).
+__device__ __forceinline__ h8_t decode8(uint32_t w, _Float16 S) {
+  const h2_t ss = {S, S};
+  const h2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * ss;
+  const h2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * ss;
+  const h2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * ss;
+  const h2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * ss;
+  return h8_t{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+__device__ __forceinline__ rsrc_t lines_rsrc(const uint8_t* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uni(reinterpret_cast<int64_t>(p))), 0, bytes,
+                                           0x00020000);
+}
+
+// acc[im][in] += A lines x B lines^T over the contraction length L (a multiple
+// of kBK).  PAIR: B's 256 LDS lines are four blocks of 64: lines 0-63 of B0
+// (gate), 0-63 of B1 (up), 64-127 of B0, 64-127 of B1; otherwise 256 lines of
+// B0.  Each step waits for its own copies, passes one barrier, issues the
+// copies of the next step into the other stage and multiplies meanwhile.
+// Contraction order: word 8h + s of a line's 64-byte chunk feeds sub-step s of
+// lane half h, in A and B alike, so a lane reads its eight sub-steps' words
+// with two 16-byte LDS reads.
+template <bool PAIR>
+__device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const Lines& B1, uint32_t L,
+                                         f32x16 (&acc)[kWM][kWN], uint8_t* lds0, uint8_t* lds1, uint8_t* lsc) {
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const uint32_t dpitch = uni(L / 2), spitch = uni(L / 16);
+  const uint32_t av = uni(A.valid), b0v = uni(B0.valid), b1v = uni(B1.valid);
+  const rsrc_t ad = lines_rsrc(A.data, av * dpitch), as = lines_rsrc(A.scale, av * spitch);
+  const rsrc_t b0d = lines_rsrc(B0.data, b0v * dpitch), b0s = lines_rsrc(B0.scale, b0v * spitch);
+  const rsrc_t b1d = PAIR ? lines_rsrc(B1.data, b1v * dpitch) : b0d;
+  // a wave's scale copies come from one of the two operands (32 lines a wave)
+  const bool up = PAIR && uni((uint32_t)wave) >= 2;
+  const rsrc_t bs = up ? lines_rsrc(B1.scale, b1v * spitch) : b0s;
+  const uint32_t nk = L / kBK;
+  if (nk == 0) return;
+
+  // Codes of a step: 64 lines a copy, lane g moves slot g % 4 of line g / 4.
+  const uint32_t cl = tid >> 2, cq = tid & 3;
+  auto issue = [&](uint32_t ks, uint8_t* base) {
+    const uint32_t sd = ks * kRowBytes;
+#pragma unroll
+    for (int c = 0; c < kBM / 64; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ad, (lds_ptr_t)(base + 16 * (c * kThreads + wave * 64)), 16,
+                                               (64 * c + cl) * dpitch + 16 * swz(cl, cq), sd, 0, 0);
+#pragma unroll
+    for (int c = 0; c < kBN / 64; ++c) {
+      const uint32_t line = PAIR ? 64 * (c >> 1) : 64 * c;  // first source line of the block
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(PAIR && (c & 1) ? b1d : b0d,
+                                               (lds_ptr_t)(base + kStB + 16 * (c * kThreads + wave * 64)), 16,
+                                               (line + cl) * dpitch + 16 * swz(cl, cq), sd, 0, 0);
+    }
+  };
+  // Scales of a block of steps: 128 lines a copy, 16 bytes a lane.
+  auto issue_scales = [&](uint32_t blk, uint8_t* sbase) {
+    const uint32_t so = blk * kScLine, sl = tid >> 1, sq = tid & 1;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(as, (lds_ptr_t)(sbase + 16 * (wave * 64)), 16, sl * spitch + 16 * sq, so,
+                                             0, 0);
+#pragma unroll
+    for (int c = 0; c < kBN / 128; ++c) {
+      const uint32_t line = PAIR ? 64 * c + (sl & 63) : 128 * c + sl;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bs, (lds_ptr_t)(sbase + kScB + 16 * (c * kThreads + wave * 64)), 16,
+                                               line * spitch + 16 * sq, so, 0, 0);
+    }
+  };
+
+  const int wm = wave / kWavesN, wn = wave % kWavesN, h = lane >> 5;
+  auto step = [&](uint32_t ks, const uint8_t* base, uint8_t* next) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __syncthreads();
+    h2_t sa[kWM][2], sb[kWN][2];
+    const uint8_t* scb = lsc + ((ks / kScSteps) & 1) * kScBlockBytes + kRowScales * (ks % kScSteps) + 4 * h;
+#pragma unroll
+    for (int im = 0; im < kWM; ++im) {
+      const uint32_t sc = *reinterpret_cast<const uint32_t*>(scb + kScLine * (wm * (kWM * 32) + im * 32 + (lane & 31)));
+      sa[im][0] = scales_h2(sc & 0xFFFFu);
+      sa[im][1] = scales_h2(sc >> 16);
+    }
+#pragma unroll
+    for (int in = 0; in < kWN; ++in) {
+      const uint32_t sc =
+          *reinterpret_cast<const uint32_t*>(scb + kScB + kScLine * (wn * (kWN * 32) + in * 32 + (lane & 31)));
+      sb[in][0] = scales_h2(sc & 0xFFFFu);
+      sb[in][1] = scales_h2(sc >> 16);
+    }
+    if (ks + 1 < nk) {
+      issue(ks + 1, next);
+      const uint32_t nb = (ks + 1) / kScSteps;
+      if ((ks + 1) % kScSteps == 0) issue_scales(nb, lsc + (nb & 1) * kScBlockBytes);
+    }
+    u32x4 wa[kWM][2], wb[kWN][2];
+#pragma unroll
+    for (int im = 0; im < kWM; ++im) {
+      const uint32_t line = wm * (kWM * 32) + im * 32 + (lane & 31);
+      wa[im][0] = *reinterpret_cast<const u32x4*>(base + kRowBytes * line + 16 * swz(line, 2 * h));
+      wa[im][1] = *reinterpret_cast<const u32x4*>(base + kRowBytes * line + 16 * swz(line, 2 * h + 1));
+    }
+#pragma unroll
+    for (int in = 0; in < kWN; ++in) {
+      const uint32_t line = wn * (kWN * 32) + in * 32 + (lane & 31);
+      wb[in][0] = *reinterpret_cast<const u32x4*>(base + kStB + kRowBytes * line + 16 * swz(line, 2 * h));
+      wb[in][1] = *reinterpret_cast<const u32x4*>(base + kStB + kRowBytes * line + 16 * swz(line, 2 * h + 1));
+    }
+    // the next sub-step's fragments are decoded between this one's MFMAs
+    h8_t af[2][kWM], bf[2][kWN];
+#pragma unroll
+    for (int im = 0; im < kWM; ++im) af[0][im] = decode8(wa[im][0][0], sa[im][0][0]);
+#pragma unroll
+    for (int in = 0; in < kWN; ++in) bf[0][in] = decode8(wb[in][0][0], sb[in][0][0]);
+#pragma unroll
+    for (int s = 0; s < kBK / 16; ++s) {
+      const int cu = s & 1, nx = cu ^ 1, t = s + 1;
+      if (t < kBK / 16) {
+#pragma unroll
+        for (int im = 0; im < kWM; ++im) af[nx][im] = decode8(wa[im][t >> 2][t & 3], sa[im][t >> 2][(t >> 1) & 1]);
+#pragma unroll
+        for (int in = 0; in < kWN; ++in) bf[nx][in] = decode8(wb[in][t >> 2][t & 3], sb[in][t >> 2][(t >> 1) & 1]);
+      }
+#pragma unroll
+      for (int im = 0; im < kWM; ++im)
+#pragma unroll
+        for (int in = 0; in < kWN; ++in)
+          acc[im][in] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[cu][im], bf[cu][in], acc[im][in], 0, 0, 0);
+      if (t < kBK / 16) {
+#pragma unroll
+        for (int i = 0; i < kWM * kWN; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
+          __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);  // six VALU
+        }
+      }
+    }
+  };
+  issue(0, lds0);
+  issue_scales(0, lsc);
+#pragma unroll 1
+  for (uint32_t ks = 0; ks < nk; ks += 2) {
+    step(ks, lds0, lds1);
+    if (ks + 1 >= nk) break;
+    step(ks + 1, lds1, lds0);
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  __syncthreads();
+}
+
+// Logical tile: super-tiles of 64 consecutive tiles dealt round-robin to the
+// 8 XCDs, so that each XCD's L2 holds the operand slices its tiles share.
+__device__ __forceinline__ uint32_t xcd_tile() {
+  const uint32_t id = blockIdx.x, T = gridDim.x;
+  const uint32_t round = kNumXcd * 64, full = (T / round) * round;
+  if (id >= full) return uni(id);
+  const uint32_t j = id / kNumXcd, x = id % kNumXcd;
+  return uni((kNumXcd * (j / 64) + x) * 64 + j % 64);
+}
+
+__device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t ntm, uint32_t ntn, uint32_t* tm, uint32_t* tn) {
+  const uint32_t g = t / (kGroupRows * ntn), in = t % (kGroupRows * ntn);
+  const uint32_t first = g * kGroupRows, gm = min((uint32_t)kGroupRows, ntm - first);
+  *tm = uni(first + in % gm);
+  *tn = uni(in / gm);
+}
+
+struct Operands {
+  const uint8_t *a_data, *a_scale;
+  const float* a_amax;
+  const uint8_t *b_data, *b_scale;
+  const float* b_amax;
+};
+
+template <int ACT>
+__device__ __forceinline__ float glu(float g, float u) {
+  float dv;
+  return g * act_logistic<ACT>(g, &dv) * u;
+}
+
+// Forward: tiles of 128 packed rows x 128 columns (256 lines).
+template <int ACT, bool KEEP>
+__global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_t f, int64_t k, Routing R,
+                                                              uint32_t ntm, uint32_t ntn, uint16_t* __restrict__ h,
+                                                              uint16_t* __restrict__ gu) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds1[kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lsc[2 * kScBlockBytes];
+  __shared__ float lsa[kBM], lsb[kBN];
+  if (!routing_ok(R)) return;
+  const int32_t total = route_end(R, R.num_experts - 1);
+  uint32_t tm, tn;
+  grouped_tile(xcd_tile(), ntm, ntn, &tm, &tn);
+  const int32_t row0 = (int32_t)(tm * kBM);
+  if (row0 >= total) return;
+  int32_t rbeg, rend;
+  const int e = find_expert(R, row0, &rbeg, &rend);
+  const int64_t col0 = (int64_t)tn * (kBN / 2);
+  const uint32_t cols = (uint32_t)min<int64_t>(f - col0, kBN / 2);
+  const int64_t gl = (int64_t)e * 2 * f + col0, ul = gl + f;
+  const Lines A{O.a_data + (int64_t)row0 * (k / 2), O.a_scale + (int64_t)row0 * (k / 16), (uint32_t)kBM};
+  const Lines G{O.b_data + gl * (k / 2), O.b_scale + gl * (k / 16), cols};
+  const Lines U{O.b_data + ul * (k / 2), O.b_scale + ul * (k / 16), cols};
+  f32x16 acc[kWM][kWN];
+#pragma unroll
+  for (int im = 0; im < kWM; ++im)
+#pragma unroll
+    for (int in = 0; in < kWN; ++in) acc[im][in] = f32x16{};
+  multiply<true>(A, G, U, (uint32_t)k, acc, lds0, lds1, lsc);
+
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  if (tid < kBM) lsa[tid] = O.a_amax[row0 + tid] / 2688.0f;
+  {
+    const uint32_t j = tid & 127;
+    const float* am = O.b_amax + (tid < 128 ? gl : ul);
+    lsb[tid] = j < cols ? am[j] / 2688.0f : 0.0f;
+  }
+  __syncthreads();
+  const int wm = wave / kWavesN, wn = wave % kWavesN;
+  const bool odd = lane & 1;
+#pragma unroll
+  for (int in = 0; in < kWN / 2; ++in) {
+    const uint32_t j = wn * 64 + in * 32 + (lane & 31);
+    const float sg = lsb[j], su = lsb[128 + j];
+    const uint32_t jp = j & ~1u;
+    const bool write = jp < cols;
+#pragma unroll
+    for (int im = 0; im < kWM; ++im)
+#pragma unroll
+      for (int v = 0; v < 16; v += 2) {
+        const uint32_t i = wm * (kWM * 32) + im * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+        const float sa0 = lsa[i], sa1 = lsa[i + 1];
+        const float g0 = (acc[im][in][v] * sa0) * sg, g1 = (acc[im][in][v + 1] * sa1) * sg;
+        const float u0 = (acc[im][in + 2][v] * sa0) * su, u1 = (acc[im][in + 2][v + 1] * sa1) * su;
+        const int64_t row = row0 + i + (odd ? 1 : 0);
+        float lo, hi;
+        pair_columns(glu<ACT>(g0, u0), glu<ACT>(g1, u1), odd, &lo, &hi);
+        if (write) *reinterpret_cast<uint32_t*>(h + row * f + col0 + jp) = pack_bf16(lo, hi);
+        if (KEEP) {
+          uint16_t* p = gu + row * 2 * f + col0 + jp;
+          pair_columns(g0, g1, odd, &lo, &hi);
+          if (write) *reinterpret_cast<uint32_t*>(p) = pack_bf16(lo, hi);
+          pair_columns(u0, u1, odd, &lo, &hi);
+          if (write) *reinterpret_cast<uint32_t*>(p + f) = pack_bf16(lo, hi);
+        }
+      }
+  }
+}
+
+// Backward: tiles of 128 packed rows x 256 columns of dh.
+template <int ACT>
+__global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_t f, int64_t k, Routing R,
+                                                              uint32_t ntm, uint32_t ntn,
+                                                              const uint16_t* __restrict__ gu,
+                                                              uint16_t* __restrict__ dgu) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds1[kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lsc[2 * kScBlockBytes];
+  __shared__ float lsa[kBM], lsb[kBN];
+  if (!routing_ok(R)) return;
+  const int32_t total = route_end(R, R.num_experts - 1);
+  uint32_t tm, tn;
+  grouped_tile(xcd_tile(), ntm, ntn, &tm, &tn);
+  const int32_t row0 = (int32_t)(tm * kBM);
+  if (row0 >= total) return;
+  int32_t rbeg, rend;
+  const int e = find_expert(R, row0, &rbeg, &rend);
+  const int64_t col0 = (int64_t)tn * kBN;
+  const uint32_t cols = (uint32_t)min<int64_t>(f - col0, kBN);
+  const int64_t line0 = (int64_t)e * f + col0;
+  const Lines A{O.a_data + (int64_t)row0 * (k / 2), O.a_scale + (int64_t)row0 * (k / 16), (uint32_t)kBM};
+  const Lines B{O.b_data + line0 * (k / 2), O.b_scale + line0 * (k / 16), cols};
+  f32x16 acc[kWM][kWN];
+#pragma unroll
+  for (int im = 0; im < kWM; ++im)
+#pragma unroll
+    for (int in = 0; in < kWN; ++in) acc[im][in] = f32x16{};
+  multiply<false>(A, B, B, (uint32_t)k, acc, lds0, lds1, lsc);
+
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  if (tid < kBM) lsa[tid] = O.a_amax[row0 + tid] / 2688.0f;
+  lsb[tid] = (uint32_t)tid < cols ? O.b_amax[line0 + tid] / 2688.0f : 0.0f;
+  __syncthreads();
+  const int wm = wave / kWavesN, wn = wave % kWavesN;
+  const bool odd = lane & 1;
+#pragma unroll
+  for (int in = 0; in < kWN; ++in) {
+    const uint32_t j = wn * 128 + in * 32 + (lane & 31);
+    const float sb = lsb[j];
+    const uint32_t jp = j & ~1u;
+    const bool write = jp < cols;
+#pragma unroll
+    for (int im = 0; im < kWM; ++im)
+#pragma unroll
+      for (int v = 0; v < 16; v += 2) {
+        const uint32_t i = wm * (kWM * 32) + im * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+        float dh[2];
+        pair_columns((acc[im][in][v] * lsa[i]) * sb, (acc[im][in][v + 1] * lsa[i + 1]) * sb, odd, &dh[0], &dh[1]);
+        if (!write) continue;
+        const int64_t at = (row0 + i + (odd ? 1 : 0)) * 2 * f + col0 + jp;
+        const uint32_t gq = *reinterpret_cast<const uint32_t*>(gu + at);
+        const uint32_t uq = *reinterpret_cast<const uint32_t*>(gu + at + f);
+        const float g[2] = {bf16lo(gq), bf16hi(gq)}, u[2] = {bf16lo(uq), bf16hi(uq)};
+        float dg[2], du[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float dv;
+          const float q = act_logistic<ACT>(g[c], &dv), a = g[c] * q;
+          du[c] = dh[c] * a;
+          dg[c] = dh[c] * u[c] * __builtin_fmaf(a * (1.0f - q), dv, q);
+        }
+        *reinterpret_cast<uint32_t*>(dgu + at) = pack_bf16(dg[0], dg[1]);
+        *reinterpret_cast<uint32_t*>(dgu + at + f) = pack_bf16(du[0], du[1]);
+      }
+  }
+}
+
+// ------------------------------------------------------------- host side
+
+constexpr int64_t kMaxF = 1 << 19;  // 2f lines within the grouped GEMM's 2^20
+
+int check_glu(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, int32_t act, int cols_per_tile) {
+  if (k <= 0 || k % kBK != 0 || k > kMaxK || f <= 0 || f % 16 != 0 || f > kMaxF) return NVFP4G_EINVAL;
+  if (rows < 0 || rows > kMaxRows || E < 1) return NVFP4G_EINVAL;
+  if (act != MOE_ACT_SILU && act != MOE_ACT_GELU) return NVFP4G_EINVAL;
+  if ((rows / kBM) * ((f + cols_per_tile - 1) / cols_per_tile) > (int64_t)INT32_MAX) return NVFP4G_EINVAL;
+  if (!O.b_data || !O.b_scale || !O.b_amax || (rows && (!O.a_data || !O.a_scale || !O.a_amax))) return NVFP4G_EINVAL;
+  if (!aligned(O.a_data, 16) || !aligned(O.b_data, 16) || !aligned(O.a_scale, 4) || !aligned(O.b_scale, 4) ||
+      !aligned(O.a_amax, 4) || !aligned(O.b_amax, 4))
+    return NVFP4G_EALIGN;
+  return NVFP4G_OK;
+}
+
+// Routing of a host-split call (d_offs NULL) or of a graph-safe one.
+int make_routing(const int64_t* h_splits, const int32_t* d_offs, int32_t* d_status, int64_t rows, int32_t E,
+                 bool graph, Routing* R) {
+  R->num_experts = E;
+  R->m_capacity = (int32_t)rows;
+  R->d_offs = nullptr;
+  R->d_status = nullptr;
+  return graph ? graph_routing(d_offs, d_status, E, rows, R) : host_routing(h_splits, rows, E, R);
+}
+
+int launch_fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Routing& R, int32_t act, uint16_t* h,
+               uint16_t* gu, hipStream_t st) {
+  const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + kBN / 2 - 1) / (kBN / 2));
+  const dim3 grid(ntm * ntn);
+  if (act == MOE_ACT_SILU) {
+    if (gu) hipLaunchKernelGGL((glu_fwd_kernel<MOE_ACT_SILU, true>), grid, dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h, gu);
+    else hipLaunchKernelGGL((glu_fwd_kernel<MOE_ACT_SILU, false>), grid, dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h, gu);
+  } else {
+    if (gu) hipLaunchKernelGGL((glu_fwd_kernel<MOE_ACT_GELU, true>), grid, dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h, gu);
+    else hipLaunchKernelGGL((glu_fwd_kernel<MOE_ACT_GELU, false>), grid, dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h, gu);
+  }
+  return hip_status();
+}
+
+int fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
+        const int32_t* d_offs, int32_t* d_status, bool graph, int32_t act, uint16_t* h, uint16_t* gu, void* stream) {
+  int rc = check_glu(O, rows, f, k, E, act, kBN / 2);
+  if (rc) return rc;
+  if (rows && !h) return NVFP4G_EINVAL;
+  if (!aligned(h, 16) || !aligned(gu, 16)) return NVFP4G_EALIGN;
+  Routing R;
+  if ((rc = make_routing(h_splits, d_offs, d_status, rows, E, graph, &R))) return rc;
+  return rows ? launch_fwd(O, rows, f, k, R, act, h, gu, (hipStream_t)stream) : NVFP4G_OK;
+}
+
+int bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
+        const int32_t* d_offs, int32_t* d_status, bool graph, const uint16_t* gu, int32_t act, uint16_t* dgu,
+        void* stream) {
+  int rc = check_glu(O, rows, f, k, E, act, kBN);
+  if (rc) return rc;
+  if (rows && (!gu || !dgu)) return NVFP4G_EINVAL;
+  if (!aligned(gu, 16) || !aligned(dgu, 16)) return NVFP4G_EALIGN;
+  Routing R;
+  if ((rc = make_routing(h_splits, d_offs, d_status, rows, E, graph, &R))) return rc;
+  if (rows == 0) return NVFP4G_OK;
+  const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + kBN - 1) / kBN);
+  const dim3 grid(ntm * ntn);
+  if (act == MOE_ACT_SILU)
+    hipLaunchKernelGGL((glu_bwd_kernel<MOE_ACT_SILU>), grid, dim3(kThreads), 0, (hipStream_t)stream, O, f, k, R, ntm,
+                       ntn, gu, dgu);
+  else
+    hipLaunchKernelGGL((glu_bwd_kernel<MOE_ACT_GELU>), grid, dim3(kThreads), 0, (hipStream_t)stream, O, f, k, R, ntm,
+                       ntn, gu, dgu);
+  return hip_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_glu(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
+            const uint8_t* b_scale, const float* b_amax, int64_t sum_m, int64_t f, int64_t k, int32_t num_experts,
+            const int64_t* h_splits, int32_t act, uint16_t* h, uint16_t* gu, void* stream) {
+  return fwd({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, sum_m, f, k, num_experts, h_splits, nullptr, nullptr,
+             false, act, h, gu, stream);
+}
+
+int moe_glu_graphsafe(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
+                      const uint8_t* b_scale, const float* b_amax, int64_t m_capacity, int64_t f, int64_t k,
+                      int32_t num_experts, const int32_t* d_offs, int32_t act, uint16_t* h, uint16_t* gu,
+                      int32_t* d_status, void* stream) {
+  return fwd({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, m_capacity, f, k, num_experts, nullptr, d_offs,
+             d_status, true, act, h, gu, stream);
+}
+
+int moe_glu_bwd(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
+                const uint8_t* b_scale, const float* b_amax, int64_t sum_m, int64_t f, int64_t k, int32_t num_experts,
+                const int64_t* h_splits, const uint16_t* gu, int32_t act, uint16_t* dgu, void* stream) {
+  return bwd({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, sum_m, f, k, num_experts, h_splits, nullptr, nullptr,
+             false, gu, act, dgu, stream);
+}
+
+int moe_glu_bwd_graphsafe(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
+                          const uint8_t* b_scale, const float* b_amax, int64_t m_capacity, int64_t f, int64_t k,
+                          int32_t num_experts, const int32_t* d_offs, const uint16_t* gu, int32_t act, uint16_t* dgu,
+                          int32_t* d_status, void* stream) {
+  return bwd({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, m_capacity, f, k, num_experts, nullptr, d_offs,
+             d_status, true, gu, act, dgu, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,585 @@
+// moe_route.hip -- selection of experts with weights, its gradient, and the
+// plan of the packed 128-row groups, behind the C ABI of include/moe_ops.h.
+//
+// Selection.  A token's choice is the topk largest keys  l + bias, ties to the
+// lower index; its weights are softmax or sigmoid scores of the logits.  One
+// wave holds one token: lane i holds VPL consecutive experts (i*VPL ..), so
+// among equal keys the lowest lane, and in it the lowest element, is the
+// lowest index.  Keys are compared as order-preserving integers (0 = masked).
+// topk rounds: each lane keeps its own best, a 6-step wave maximum finds the
+// key, a ballot the lane, and that lane drops the element.
+//
+// Plan.  A stable counting sort of the pairs by expert without atomics that
+// decide an order: a wave ranks 64 pairs at a time by matching expert
+// numbers with one ballot a bit, on top of its running counts in LDS.
+#include "moe_common.hpp"
+
+namespace {
+
+using namespace moe;
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// Order-preserving integer of a key; 0 for a masked one (-inf), -0 as +0.
+__device__ __forceinline__ uint32_t key_bits(float k) {
+  if (!(k > kNegInf)) return 0;
+  const uint32_t b = __float_as_uint(k + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// A logit as the operator reads it: NaN and -inf masked, +inf as FLT_MAX.
+__device__ __forceinline__ float clean(float l) { return l > kNegInf ? fminf(l, FLT_MAX) : kNegInf; }
+
+template <class T>
+__device__ __forceinline__ float logit_at(const T* p, int64_t i);
+template <>
+__device__ __forceinline__ float logit_at<float>(const float* p, int64_t i) { return p[i]; }
+template <>
+__device__ __forceinline__ float logit_at<uint16_t>(const uint16_t* p, int64_t i) {
+  return __uint_as_float((uint32_t)p[i] << 16);
+}
+
+// The VPL logits of this lane (experts lane*VPL ..), -inf past E.  With
+// `wide` (E a multiple of VPL and the row aligned to the lane's piece) as
+// vector loads.
+template <class T, int VPL>
+__device__ __forceinline__ void load_logits(const T* row, int E, int lane, bool wide, float (&l)[VPL]) {
+  const int e0 = lane * VPL;
+  constexpr int kPer = 16 / (int)sizeof(T) < VPL ? 16 / (int)sizeof(T) : VPL;  // elements of one load
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += kPer) {
+      typedef T vec_t __attribute__((ext_vector_type(kPer)));
+      if (e0 < E) {
+        const vec_t v = *reinterpret_cast<const vec_t*>(row + e0 + i);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const T t = v[q];
+          l[i + q] = clean(logit_at<T>(&t, 0));
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) l[i + q] = kNegInf;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = e0 + i < E ? clean(logit_at<T>(row, e0 + i)) : kNegInf;
+  }
+}
+
+// Scores of the chosen logits, one choice a lane (lanes 0 .. topk-1; z = -inf
+// elsewhere and for no choice): the unscaled weight.  top and sum are the
+// softmax's maximum and sum over all unmasked experts (used without normalize).
+__device__ __forceinline__ float choice_score(float z, int score, int normalize, float top, float sum) {
+  const bool on = z > kNegInf;
+  float s;
+  if (score == MOE_SCORE_SIGMOID) {
+    s = on ? 1.0f / (1.0f + expf(-z)) : 0.0f;
+  } else if (normalize) {
+    const float m = wave_fmax(z);
+    s = on ? expf(z - m) : 0.0f;
+  } else {
+    s = on ? expf(z - top) / sum : 0.0f;
+  }
+  if (normalize) {
+    const float tot = wave_sum(s);
+    s = tot > 0.0f ? s / tot : 0.0f;
+  }
+  return s;
+}
+
+template <class T, int VPL>
+__global__ __launch_bounds__(kThreads) void route_kernel(const T* __restrict__ logits, int64_t tokens, int E, int topk,
+                                                         const float* __restrict__ bias, int score, int normalize,
+                                                         float scale, bool wide, int32_t* __restrict__ ids,
+                                                         float* __restrict__ weights) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (t >= tokens) return;
+  float l[VPL];
+  load_logits<T, VPL>(logits + t * E, E, lane, wide, l);
+  float top = 0.0f, sum = 1.0f;
+  if (score == MOE_SCORE_SOFTMAX && !normalize) {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+    top = fmaxf(wave_fmax(m), -FLT_MAX);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s += expf(l[i] - top);
+    sum = wave_sum(s);
+  }
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane * VPL + i;
+    key[i] = key_bits(bias && e < E ? l[i] + bias[e] : l[i]);
+  }
+  int my_id = -1;
+  float my_z = kNegInf;
+  for (int j = 0; j < topk; ++j) {
+    uint32_t best = key[0];
+    int at = 0;
+    float z = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) {
+      const bool g = key[i] > best;
+      best = g ? key[i] : best;
+      at = g ? i : at;
+      z = g ? l[i] : z;
+    }
+    const uint32_t w = wave_max(best);
+    if (uni(w) == 0) break;  // nothing unmasked is left
+    const int win = uni((int32_t)__builtin_ctzll(__ballot(best == w)));
+    const int id = __builtin_amdgcn_readlane(lane * VPL + at, win);
+    const float wz = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(z), win));
+    if (lane == j) {
+      my_id = id;
+      my_z = wz;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = lane * VPL + i == id ? 0u : key[i];
+  }
+  const float s = choice_score(my_z, score, normalize, top, sum);
+  if (lane < topk) {
+    ids[t * topk + lane] = my_id;
+    weights[t * topk + lane] = my_id >= 0 ? s * scale : 0.0f;
+  }
+}
+
+// Gradient: with q the (normalised) score of a choice and g = scale * dw,
+//   softmax            dl_i = p_i (g_i - sum_j p_j g_j) over all unmasked i
+//   softmax normalised the same over the chosen logits alone
+//   sigmoid            dl_j = g_j s_j (1 - s_j)
+//   sigmoid normalised dl_j = (g_j - sum_i q_i g_i) q_j (1 - s_j)
+// The choices' values are scattered into the token's row in LDS and the row
+// is written once, densely.
+template <class T, int VPL>
+__global__ __launch_bounds__(kThreads) void route_bwd_kernel(const T* __restrict__ logits, int64_t tokens, int E,
+                                                             int topk, const int32_t* __restrict__ ids,
+                                                             const float* __restrict__ dweights, int score,
+                                                             int normalize, float scale, bool wide,
+                                                             T* __restrict__ dlogits) {
+  extern __shared__ float lrows[];
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (t >= tokens) return;  // whole waves; no barrier below
+  float* row = lrows + (threadIdx.x >> 6) * (64 * VPL);
+  const bool dense = score == MOE_SCORE_SOFTMAX && !normalize;
+  float z = kNegInf, g = 0.0f;
+  int id = -1;
+  if (lane < topk) {
+    id = ids[t * topk + lane];
+    if ((uint32_t)id >= (uint32_t)E) id = -1;
+    if (id >= 0) {
+      z = clean(logit_at<T>(logits, t * E + id));
+      g = scale * dweights[t * topk + lane];
+    }
+  }
+  float l[VPL], top = 0.0f, sum = 1.0f;
+  if (dense) {
+    load_logits<T, VPL>(logits + t * E, E, lane, wide, l);
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+    top = fmaxf(wave_fmax(m), -FLT_MAX);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      l[i] = expf(l[i] - top);
+      s += l[i];
+    }
+    sum = wave_sum(s);
+  }
+  const bool on = z > kNegInf;  // a masked logit that was named as a choice has no gradient
+  const float q = choice_score(z, score, normalize, top, sum);
+  if (!on) g = 0.0f;
+  const float inner = wave_sum(q * g);
+  float d;
+  if (score == MOE_SCORE_SIGMOID) {
+    const float s1 = on ? 1.0f / (1.0f + expf(z)) : 0.0f;  // 1 - sigmoid(z)
+    d = normalize ? (g - inner) * q * s1 : g * q * s1;
+  } else {
+    d = normalize ? q * (g - inner) : q * g;
+  }
+  float v[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) row[lane * VPL + i] = dense && sum > 0.0f ? -inner * (l[i] / sum) : 0.0f;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (on) atomicAdd(&row[id], d);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) v[i] = row[lane * VPL + i];
+  T* out = dlogits + t * E;
+  const int e0 = lane * VPL;
+  if (wide) {
+    constexpr int kPer = 16 / (int)sizeof(T) < VPL ? 16 / (int)sizeof(T) : VPL;
+    if (e0 < E) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += kPer) {
+        typedef T vec_t __attribute__((ext_vector_type(kPer)));
+        vec_t o;
+#pragma unroll
+        for (int q2 = 0; q2 < kPer; ++q2) {
+          if constexpr (sizeof(T) == 4) o[q2] = v[i + q2];
+          else o[q2] = to_bf16(v[i + q2]);
+        }
+        *reinterpret_cast<vec_t*>(out + e0 + i) = o;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e0 + i < E) {
+        if constexpr (sizeof(T) == 4) out[e0 + i] = v[i];
+        else out[e0 + i] = to_bf16(v[i]);
+      }
+  }
+}
+
+// ------------------------------------------------------------------- plan
+
+constexpr int kPlanPairs = 512;       // pairs one wave ranks in the split form
+constexpr int kSmallPairs = 4096;     // the one-launch form: pairs, experts
+constexpr int kSmallExperts = 512;
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallWaves = kSmallThreads / 64;
+
+__device__ __forceinline__ int expert_of(const int32_t* ids, int64_t p, int64_t end, int E) {
+  const int e = p < end ? ids[p] : -1;
+  return (uint32_t)e < (uint32_t)E ? e : -1;
+}
+
+// Ranks the 64 pairs of a wave step: a pair's rank is base[e] plus the pairs
+// of the same expert in lower lanes; base[e] then moves on by their number.
+__device__ __forceinline__ int wave_rank(int e, int ebits, int32_t* base) {
+  uint64_t same = __ballot(e >= 0);
+  for (int b = 0; b < ebits; ++b) {
+    const uint64_t bal = __ballot((e >> b) & 1);
+    same &= (e >> b) & 1 ? bal : ~bal;
+  }
+  const uint64_t below = same & ((1ull << (threadIdx.x & 63)) - 1);
+  int r = 0;
+  if (e >= 0) r = base[e] + __popcll(below);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (e >= 0 && below == 0) base[e] += __popcll(same);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  return r;
+}
+
+// Exclusive prefix over the experts of their padded group sizes, from counts
+// in cnt[E]; leaves begin[e] in `begin`, returns the total.  All threads of
+// the work-group take part; blockDim.x is a multiple of 64.
+__device__ int group_begins(const int32_t* cnt, int E, int32_t* begin, int32_t* wtot) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
+  const int per = (E + blockDim.x - 1) / blockDim.x;
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < E) mine += (cnt[e] + kTileRows - 1) / kTileRows * kTileRows;
+  }
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 63) wtot[wave] = inc;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w < wave) before += wtot[w];
+    total += wtot[w];
+  }
+  int at = before + inc - mine;
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < E) {
+      begin[e] = at;
+      at += (cnt[e] + kTileRows - 1) / kTileRows * kTileRows;
+    }
+  }
+  __syncthreads();
+  return total;
+}
+
+// src of the rows [r0, r1): -1 for those no pair has (padding rows of a group
+// and rows past the last group).
+__device__ __forceinline__ void fill_padding(int64_t r0, int64_t r1, int E, int total, const int32_t* begin,
+                                             const int32_t* cnt, int32_t* src) {
+  for (int64_t r = r0 + threadIdx.x; r < r1; r += blockDim.x) {
+    bool pad = r >= total;
+    if (!pad) {  // the last expert whose group begins at or before r and is not empty before it
+      int lo = 0, hi = E - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (begin[mid] <= r) lo = mid; else hi = mid - 1;
+      }
+      pad = r - begin[lo] >= cnt[lo];
+    }
+    if (pad) src[r] = -1;
+  }
+}
+
+__device__ __forceinline__ void write_ends(int E, const int32_t* begin, const int32_t* cnt, int64_t cap, int total,
+                                           int32_t* offs, int32_t* counts, int32_t* status) {
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    offs[e] = begin[e] + (cnt[e] + kTileRows - 1) / kTileRows * kTileRows;
+    counts[e] = cnt[e];
+  }
+  if (threadIdx.x == 0 && total > cap) atomicOr(status, NVFP4G_DEV_OVERFLOW);
+}
+
+__device__ __forceinline__ void write_pair(int64_t p, int row, int64_t cap, int32_t* rows, int32_t* src) {
+  const bool fits = row >= 0 && row < cap;
+  rows[p] = fits ? row : -1;
+  if (fits) src[row] = (int32_t)p;
+}
+
+// Few pairs: one work-group does it all (a launch costs more than the work).
+__global__ __launch_bounds__(kSmallThreads) void plan_small_kernel(const int32_t* __restrict__ ids, int pairs, int E,
+                                                                   int ebits, int64_t cap, int32_t* offs,
+                                                                   int32_t* counts, int32_t* rows, int32_t* src,
+                                                                   int32_t* status) {
+  extern __shared__ int32_t lds[];
+  int32_t* hist = lds;                        // [kSmallWaves][E]: a wave's counts, then its first ranks
+  int32_t* cnt = hist + kSmallWaves * E;      // [E]
+  int32_t* begin = cnt + E;                   // [E]
+  int32_t* wtot = begin + E;                  // [kSmallWaves]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int share = (pairs + kSmallThreads - 1) / kSmallThreads * 64;  // pairs of a wave, whole steps
+  const int p0 = wave * share, p1 = min(p0 + share, pairs);
+  for (int i = tid; i < kSmallWaves * E; i += kSmallThreads) hist[i] = 0;
+  __syncthreads();
+  for (int p = p0; p < p1; p += 64) {
+    const int e = expert_of(ids, p + lane, p1, E);
+    if (e >= 0) atomicAdd(&hist[wave * E + e], 1);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kSmallThreads) {
+    int acc = 0;
+    for (int w = 0; w < kSmallWaves; ++w) {
+      const int v = hist[w * E + e];
+      hist[w * E + e] = acc;
+      acc += v;
+    }
+    cnt[e] = acc;
+  }
+  __syncthreads();
+  const int total = group_begins(cnt, E, begin, wtot);
+  for (int p = p0; p < p1; p += 64) {
+    const int e = expert_of(ids, p + lane, p1, E);
+    const int r = wave_rank(e, ebits, hist + wave * E);
+    if (p + lane < p1) write_pair(p + lane, e >= 0 ? begin[e] + r : -1, cap, rows, src);
+  }
+  fill_padding(0, cap, E, total, begin, cnt, src);
+  write_ends(E, begin, cnt, cap, total, offs, counts, status);
+}
+
+// Many pairs, step 1: counts of each wave's kPlanPairs pairs, ws[chunk][E].
+__global__ __launch_bounds__(kThreads) void plan_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int E,
+                                                              int32_t* __restrict__ ws, int64_t chunks) {
+  extern __shared__ int32_t lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * (blockDim.x >> 6) + wave;
+  for (int i = threadIdx.x; i < (int)(blockDim.x >> 6) * E; i += blockDim.x) lds[i] = 0;
+  __syncthreads();
+  const int64_t p0 = c * kPlanPairs, p1 = min(p0 + kPlanPairs, pairs);
+  for (int64_t p = p0; p < p1; p += 64) {
+    const int e = expert_of(ids, p + lane, p1, E);
+    if (e >= 0) atomicAdd(&lds[wave * E + e], 1);
+  }
+  __syncthreads();
+  if (c < chunks)
+    for (int e = lane; e < E; e += 64) ws[c * E + e] = lds[wave * E + e];
+}
+
+// Step 2: per expert the exclusive prefix over the chunks (in place) and the
+// count, which goes to the row after the last chunk.  A work-group takes 64
+// experts; its 16 waves take a run of chunks each.
+__global__ __launch_bounds__(kSmallThreads) void plan_scan_kernel(int32_t* __restrict__ ws, int64_t chunks, int E) {
+  __shared__ int32_t part[kSmallWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane;
+  const int64_t per = (chunks + kSmallWaves - 1) / kSmallWaves;
+  const int64_t c0 = min(wave * per, chunks), c1 = min(c0 + per, chunks);
+  int acc = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int64_t c = c0; c < c1; ++c) acc += ws[c * E + e];
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  int at = 0, total = 0;
+  for (int w = 0; w < kSmallWaves; ++w) {
+    if (w < wave) at += part[w][lane];
+    total += part[w][lane];
+  }
+  if (e < E) {
+#pragma unroll 8
+    for (int64_t c = c0; c < c1; ++c) {
+      const int v = ws[c * E + e];
+      ws[c * E + e] = at;
+      at += v;
+    }
+    if (wave == 0) ws[chunks * E + e] = total;
+  }
+}
+
+// Step 3: every work-group finds the groups' begins from the counts (they
+// are few), ranks its waves' pairs and fills its share of the padding.
+__global__ __launch_bounds__(kThreads) void plan_write_kernel(const int32_t* __restrict__ ids, int64_t pairs, int E,
+                                                              int ebits, int64_t cap, const int32_t* __restrict__ ws,
+                                                              int64_t chunks, int32_t* offs, int32_t* counts,
+                                                              int32_t* rows, int32_t* src, int32_t* status) {
+  extern __shared__ int32_t lds[];
+  int32_t* base = lds;                              // [waves][E]
+  int32_t* cnt = base + (blockDim.x >> 6) * E;      // [E]
+  int32_t* begin = cnt + E;                         // [E]
+  int32_t* wtot = begin + E;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * (blockDim.x >> 6) + wave;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = ws[chunks * E + e];
+  if (c < chunks)
+    for (int e = lane; e < E; e += 64) base[wave * E + e] = ws[c * E + e];
+  __syncthreads();
+  const int total = group_begins(cnt, E, begin, wtot);
+  const int64_t p0 = c * kPlanPairs, p1 = min(p0 + kPlanPairs, pairs);
+  for (int64_t p = p0; p < p1; p += 64) {
+    const int e = expert_of(ids, p + lane, p1, E);
+    const int r = wave_rank(e, ebits, base + wave * E);
+    if (p + lane < p1) write_pair(p + lane, e >= 0 ? begin[e] + r : -1, cap, rows, src);
+  }
+  const int64_t per = (cap + gridDim.x - 1) / gridDim.x;
+  fill_padding(blockIdx.x * per, min((blockIdx.x + 1) * per, cap), E, total, begin, cnt, src);
+  if (blockIdx.x == 0) write_ends(E, begin, cnt, cap, total, offs, counts, status);
+}
+
+// ------------------------------------------------------------- host side
+
+bool plan_is_small(int64_t pairs, int32_t E) { return pairs <= kSmallPairs && E <= kSmallExperts; }
+int64_t plan_chunks(int64_t pairs) { return pairs > 0 ? (pairs + kPlanPairs - 1) / kPlanPairs : 1; }
+// Threads of the counting and writing steps: four waves, each with its
+// counts of all experts in LDS; one wave where four would pass 64 KB.
+int plan_threads(int32_t E) { return E <= 2048 ? kThreads : 64; }
+
+int check_route(int32_t type, int64_t tokens, int32_t E, int32_t topk, int32_t score) {
+  if (!valid_type(type) || (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID)) return NVFP4G_EINVAL;
+  if (E < 1 || E > MOE_MAX_EXPERTS || topk < 1 || topk > MOE_MAX_TOPK || topk > E) return NVFP4G_EINVAL;
+  if (tokens < 0 || tokens > MOE_MAX_PAIRS / topk) return NVFP4G_EINVAL;
+  return NVFP4G_OK;
+}
+
+// Calls f(VPL) with the experts a lane holds as a compile-time constant.
+template <class F>
+void with_vpl(int E, F f) {
+  const int v = (E + 63) / 64;
+  if (v <= 1) f(std::integral_constant<int, 1>());
+  else if (v <= 2) f(std::integral_constant<int, 2>());
+  else if (v <= 4) f(std::integral_constant<int, 4>());
+  else if (v <= 8) f(std::integral_constant<int, 8>());
+  else if (v <= 16) f(std::integral_constant<int, 16>());
+  else f(std::integral_constant<int, 64>());
+}
+
+// Vector loads of a lane's experts: a row starts on their alignment and no
+// lane's piece is cut by the row's end.
+bool wide_rows(const void* p, int E, int vpl, int size) {
+  const int piece = vpl * size < 16 ? vpl * size : 16;
+  return E % vpl == 0 && (int64_t)E * size % piece == 0 && aligned(p, piece);
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_route(const void* logits, int32_t logits_type, int64_t tokens, int32_t num_experts, int32_t topk,
+              const float* select_bias, int32_t score, int32_t normalize, float scale, int32_t* ids, float* weights,
+              void* stream) {
+  const int rc = check_route(logits_type, tokens, num_experts, topk, score);
+  if (rc) return rc;
+  if (tokens == 0) return NVFP4G_OK;
+  if (!logits || !ids || !weights) return NVFP4G_EINVAL;
+  if (!aligned(logits, logits_type == MOE_F32 ? 4 : 2) || !aligned(select_bias, 4) || !aligned(ids, 4) ||
+      !aligned(weights, 4))
+    return NVFP4G_EALIGN;
+  const dim3 grid((uint32_t)((tokens + 3) / 4));
+  with_vpl(num_experts, [&](auto v) {
+    constexpr int VPL = decltype(v)::value;
+    if (logits_type == MOE_F32)
+      hipLaunchKernelGGL((route_kernel<float, VPL>), grid, dim3(kThreads), 0, (hipStream_t)stream,
+                         (const float*)logits, tokens, num_experts, topk, select_bias, score, normalize, scale,
+                         wide_rows(logits, num_experts, VPL, 4), ids, weights);
+    else
+      hipLaunchKernelGGL((route_kernel<uint16_t, VPL>), grid, dim3(kThreads), 0, (hipStream_t)stream,
+                         (const uint16_t*)logits, tokens, num_experts, topk, select_bias, score, normalize, scale,
+                         wide_rows(logits, num_experts, VPL, 2), ids, weights);
+  });
+  return hip_status();
+}
+
+int moe_route_bwd(const void* logits, int32_t logits_type, int64_t tokens, int32_t num_experts, int32_t topk,
+                  const int32_t* ids, const float* dweights, int32_t score, int32_t normalize, float scale,
+                  void* dlogits, void* stream) {
+  const int rc = check_route(logits_type, tokens, num_experts, topk, score);
+  if (rc) return rc;
+  if (tokens == 0) return NVFP4G_OK;
+  if (!logits || !ids || !dweights || !dlogits) return NVFP4G_EINVAL;
+  const int size = logits_type == MOE_F32 ? 4 : 2;
+  if (!aligned(logits, size) || !aligned(dlogits, size) || !aligned(ids, 4) || !aligned(dweights, 4))
+    return NVFP4G_EALIGN;
+  const dim3 grid((uint32_t)((tokens + 3) / 4));
+  with_vpl(num_experts, [&](auto v) {
+    constexpr int VPL = decltype(v)::value;
+    const bool wide = wide_rows(logits, num_experts, VPL, size) && wide_rows(dlogits, num_experts, VPL, size);
+    const uint32_t lds = 4 * 64 * VPL * 4;
+    if (logits_type == MOE_F32)
+      hipLaunchKernelGGL((route_bwd_kernel<float, VPL>), grid, dim3(kThreads), lds, (hipStream_t)stream,
+                         (const float*)logits, tokens, num_experts, topk, ids, dweights, score, normalize, scale, wide,
+                         (float*)dlogits);
+    else
+      hipLaunchKernelGGL((route_bwd_kernel<uint16_t, VPL>), grid, dim3(kThreads), lds, (hipStream_t)stream,
+                         (const uint16_t*)logits, tokens, num_experts, topk, ids, dweights, score, normalize, scale,
+                         wide, (uint16_t*)dlogits);
+  });
+  return hip_status();
+}
+
+int64_t moe_plan_workspace(int64_t pairs, int32_t num_experts) {
+  if (pairs < 0 || num_experts < 1 || plan_is_small(pairs, num_experts)) return 0;
+  return (plan_chunks(pairs) + 1) * num_experts * 4;
+}
+
+int moe_plan(const int32_t* ids, int64_t pairs, int32_t num_experts, int64_t m_capacity, int32_t* offs,
+             int32_t* counts, int32_t* rows, int32_t* src, int32_t* d_status, void* workspace,
+             int64_t workspace_bytes, void* stream) {
+  const int E = num_experts;
+  if (pairs < 0 || pairs > MOE_MAX_PAIRS || E < 1 || E > MOE_MAX_EXPERTS) return NVFP4G_EINVAL;
+  if (m_capacity < 0 || m_capacity > kMaxRows || m_capacity % kTileRows != 0) return NVFP4G_EINVAL;
+  if ((pairs && (!ids || !rows)) || (m_capacity && !src) || !offs || !counts || !d_status) return NVFP4G_EINVAL;
+  if (!aligned(ids, 4) || !aligned(rows, 4) || !aligned(src, 4) || !aligned(offs, 4) || !aligned(counts, 4) ||
+      !aligned(d_status, 4) || !aligned(workspace, 4))
+    return NVFP4G_EALIGN;
+  int ebits = 1;
+  while ((1 << ebits) < E) ++ebits;
+  const hipStream_t st = (hipStream_t)stream;
+  if (plan_is_small(pairs, E)) {
+    const uint32_t lds = ((kSmallWaves + 2) * E + kSmallWaves) * 4;
+    hipLaunchKernelGGL(plan_small_kernel, dim3(1), dim3(kSmallThreads), lds, st, ids, (int)pairs, E, ebits, m_capacity,
+                       offs, counts, rows, src, d_status);
+    return hip_status();
+  }
+  if (!workspace || workspace_bytes < moe_plan_workspace(pairs, E)) return NVFP4G_EINVAL;
+  int32_t* ws = (int32_t*)workspace;
+  const int64_t chunks = plan_chunks(pairs);
+  const int threads = plan_threads(E), waves = threads / 64;
+  const dim3 grid((uint32_t)((chunks + waves - 1) / waves));
+  hipLaunchKernelGGL(plan_count_kernel, grid, dim3(threads), waves * E * 4, st, ids, pairs, E, ws, chunks);
+  hipLaunchKernelGGL(plan_scan_kernel, dim3((E + 63) / 64), dim3(kSmallThreads), 0, st, ws, chunks, E);
+  hipLaunchKernelGGL(plan_write_kernel, grid, dim3(threads), ((waves + 2) * E + waves) * 4, st, ids, pairs, E, ebits,
+                     m_capacity, ws, chunks, offs, counts, rows, src, d_status);
+  return hip_status();
+}
+
+}  // extern "C"

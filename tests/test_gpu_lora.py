@@ -1,0 +1,115 @@
+"""Low-rank adapters of many requests beside a shared NVFP4 projection on the
+GPU, against the plain 64-bit implementation."""
+import numpy as np
+import pytest
+import torch
+
+import moe_reference as R
+from gpu_helpers import Guarded, log
+from nvfp4_block_scaled_group_amd import moe
+
+pytestmark = pytest.mark.gpu
+
+
+def make(seed, T, N, K, r, A):
+    rng = np.random.default_rng(seed)
+    w = R.random_lines(rng, N, K, big=8.0 / K)
+    xt, x = R.bf16_round(rng.standard_normal((T, K)))
+    at, a = R.bf16_round(rng.standard_normal((A, r, K)) * K ** -0.5)
+    bt, b = R.bf16_round(rng.standard_normal((A, N, r)))
+    alpha = rng.standard_normal(A).astype(np.float32)
+    return rng, w, xt, x, at, a, bt, b, alpha
+
+
+def call(w, xt, at, bt, ids, alpha, T, N, K, r):
+    y = Guarded(2 * T * N, torch.bfloat16, (T, N))
+    ws = torch.full((max(16, moe.lora_workspace(T, K, r)),), 0xFF, dtype=torch.uint8, device="cuda:0")  # NaN patterns
+    moe.lora_linear(xt.to("cuda:0"), *[R.to_dev(v) for v in w], at.to("cuda:0"), bt.to("cuda:0"),
+                    R.to_dev(ids.astype(np.int32)), R.to_dev(alpha), y.t, ws)
+    torch.cuda.synchronize()
+    assert y.guards_intact()
+    return y.t
+
+
+def expect(w, x, a, b, ids, alpha, K, r):
+    xw, f = R.decode(*w[:2]), w[2].astype(np.float64) / 2688
+    y, mag = (x @ xw.T) * f, (np.abs(x) @ np.abs(xw).T) * f
+    err = R.gemm_bound(mag, K)
+    for t, i in enumerate(ids):
+        if 0 <= i < a.shape[0]:
+            v, va = a[i] @ x[t], np.abs(a[i]) @ np.abs(x[t])
+            y[t] += alpha[i] * (b[i] @ v)
+            # fp32 sums over K and over the rank; v (or its two bf16 halves, 2^-18) and alpha rounded
+            err[t] += abs(alpha[i]) * (np.abs(b[i]) @ (((2 * K + 8) * R.U) * va + (2 * r + 8) * R.U * np.abs(v) + 2.0 ** -17 * np.abs(v)))
+    err = err + (np.abs(y) + err) * 4 * R.U
+    return y, err + R.UB * (np.abs(y) + err) + 1e-30
+
+
+SHAPES = [  # T, N, K, rank, adapters
+    (1, 16, 32, 8, 1), (3, 48, 96, 16, 2), (16, 272, 256, 24, 5), (17, 64, 1056, 40, 3), (33, 32, 128, 64, 40),
+    (64, 80, 544, 128, 7), (65, 16, 32, 8, 3), (130, 272, 96, 16, 4), (257, 528, 288, 24, 300), (300, 48, 2080, 128, 2),
+    (8, 512, 7168, 16, 6), (200, 256, 64, 32, 1),
+]
+
+
+@pytest.mark.parametrize("T,N,K,r,A", SHAPES)
+@pytest.mark.parametrize("mix", ["any", "runs", "none", "one"])
+def test_lora(T, N, K, r, A, mix):
+    log(f"lora T={T} N={N} K={K} r={r} A={A} {mix}")
+    rng, w, xt, x, at, a, bt, b, alpha = make(T + K, T, N, K, r, A)
+    if mix == "any":
+        ids = rng.integers(-2, A + 1, T)            # ids on both sides of the range
+    elif mix == "runs":
+        ids = np.sort(rng.integers(-1, A, T))
+    elif mix == "none":
+        ids = np.full(T, -1)
+    else:
+        ids = np.full(T, A - 1)
+    got = call(w, xt, at, bt, ids, alpha, T, N, K, r)
+    want, err = expect(w, x, a, b, ids, alpha.astype(np.float64), K, r)
+    R.check(got, want, err, "y")
+
+
+def test_an_adapter_that_overflows_stays_in_its_rows():
+    T, N, K, r, A = 130, 64, 128, 16, 3
+    rng, w, xt, x, at, a, bt, b, alpha = make(4, T, N, K, r, A)
+    ids = rng.integers(0, 3, T)
+    ref = call(w, xt, at, bt, ids, alpha, T, N, K, r).clone()
+    at[1] = float("nan")
+    bt[1] = float("inf")
+    for rows in (T, 40):
+        got = call(w, xt[:rows], at, bt, ids[:rows], alpha, rows, N, K, r)
+        keep = torch.from_numpy(ids[:rows] != 1).to("cuda:0")
+        assert torch.isfinite(got[keep].float()).all()
+        if rows == T:
+            assert torch.equal(got[keep], ref[keep])
+        assert torch.isnan(got[~keep].float()).all()
+
+
+def test_results_do_not_depend_on_the_run():
+    T, N, K, r, A = 48, 256, 2048, 32, 9
+    rng, w, xt, x, at, a, bt, b, alpha = make(5, T, N, K, r, A)
+    ids = rng.integers(-1, A, T)
+    first = call(w, xt, at, bt, ids, alpha, T, N, K, r).clone()
+    for _ in range(3):
+        assert torch.equal(call(w, xt, at, bt, ids, alpha, T, N, K, r), first)
+
+
+def test_offsets_past_32_bits():
+    """Rows of x and y beyond 4 GiB."""
+    K, N, r, A = 8192, 16, 8, 1
+    T = (1 << 32) // (2 * K) + 200
+    rng, w, _, _, at, a, bt, b, alpha = make(6, 1, N, K, r, A)
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda:0")
+    rows = [0, 1, T - 130, T - 1]
+    vt, v = R.bf16_round(rng.standard_normal((len(rows), K)))
+    x[rows] = vt.to("cuda:0")
+    y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda:0")
+    ids = torch.full((T,), -1, dtype=torch.int32, device="cuda:0")
+    ids[rows] = 0
+    ws = torch.empty(moe.lora_workspace(T, K, r), dtype=torch.uint8, device="cuda:0")
+    moe.lora_linear(x, *[R.to_dev(t) for t in w], at.to("cuda:0"), bt.to("cuda:0"), ids, R.to_dev(alpha), y, ws)
+    torch.cuda.synchronize()
+    want, err = expect(w, v, a, b, [0] * len(rows), alpha.astype(np.float64), K, r)
+    R.check(y[rows], want, err, "y")
+    assert float(y.float().abs().sum()) == float(y[rows].float().abs().sum())
