@@ -25,7 +25,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kFewRows = 64;      // rows of the first form
 constexpr int kShrinkRows = 16;   // rows of a work-group of the first launch
-constexpr int kMaxSplit = 4;      // parts of the contraction over work-groups (few rows)
+constexpr int kMaxSplit = 8;      // parts of the contraction over work-groups (few rows)
+constexpr int kShrinkStep = 128;  // contraction step of a wave of the first launch
 
 constexpr int round16(int r) { return (r + 15) / 16 * 16; }
 
@@ -49,7 +50,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(const uint16_t* __rest
   uint64_t left = __ballot((uint32_t)my < (uint32_t)adapters && lane < kShrinkRows);
   int slot = FEW ? uni((int32_t)blockIdx.z) : 0;
   const int parts = FEW ? uni((int32_t)gridDim.y) * 4 : 4, part = (FEW ? uni((int32_t)blockIdx.y) * 4 : 0) + wave;
-  const int64_t steps = (k + kStepK - 1) / kStepK, share = (steps + parts - 1) / parts;
+  const int64_t steps = (k + kShrinkStep - 1) / kShrinkStep, share = (steps + parts - 1) / parts;
   const int64_t s0 = min<int64_t>(part * share, steps), s1 = min<int64_t>(s0 + share, steps);
   const int m = min(row0 + (lane & 15), tokens - 1);
   const uint16_t* xr = x + (int64_t)m * k;
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(const uint16_t* __rest
 #pragma unroll
     for (int r = 0; r < NR; ++r) ar[r] = lora_a + ((int64_t)a * rank + min(16 * r + (lane & 15), rank - 1)) * k;
     for (int64_t s = s0; s < s1; ++s) {
-      const int64_t e0 = s * kStepK + 32 * (lane >> 4);
+      const int64_t e0 = s * kShrinkStep + 32 * (lane >> 4);
       u32x4 xq[4], aq[NR][4];
       const bool in = e0 < k;
 #pragma unroll
@@ -117,24 +118,23 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(const uint16_t* __rest
 // ------------------------------------------------------ projection, few rows
 
 template <int MT, int NL>
-__global__ __launch_bounds__(kThreads, MT * NL >= 8 ? 2 : MT * NL >= 4 ? 3 : 4) void few_rows_kernel(
+__global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void few_rows_kernel(
     const uint16_t* __restrict__ x, int tokens, int64_t k, const uint8_t* __restrict__ w_data,
     const uint8_t* __restrict__ w_scale, const float* __restrict__ w_amax, int64_t n,
     const uint16_t* __restrict__ lora_b, const float* __restrict__ alpha, int adapters, int rank,
-    const int32_t* __restrict__ ids, const float* __restrict__ v, int parts, uint16_t* __restrict__ y) {
-  constexpr int KS = 4;
-  __shared__ f32x4 red[KS * MT * NL * 64];
-  extern __shared__ float lv[];  // [tokens][rank]: alpha * v of every row
+    const int32_t* __restrict__ ids, const float* __restrict__ v, int parts, TokenPlan P, uint16_t* __restrict__ y) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = uni((int32_t)(threadIdx.x >> 6));
-  const int64_t col0 = (int64_t)uni(blockIdx.x) * (NL * 16);
+  const int groups = kTokenWaves / P.ks, group = wave / P.ks, part = wave % P.ks;
+  const int64_t col0 = ((int64_t)uni(blockIdx.x) * groups + group) * (NL * 16);
   TileLines<kModeLinear, NL> W;
   W.init(w_data, w_scale, 0, col0, n, k, lane);
-  const uint16_t* xr[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) xr[mt] = x + (int64_t)min(mt * 16 + (lane & 15), tokens - 1) * k;
   f32x4 acc[MT][NL];
-  token_multiply<MT, NL, KS>(W, xr, k, wave, lane, acc);
-  for (int i = threadIdx.x; i < tokens * rank; i += kThreads) {
+  token_multiply<MT, NL>(W, P, x, k, tokens, part, lane, lds, [](int i) { return (int64_t)i; }, acc);
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+  float* lv = reinterpret_cast<float*>(lds + kTokenWaves * MT * NL * 1024);  // [tokens][rank]: alpha * v of every row
+  __syncthreads();
+  for (int i = threadIdx.x; i < tokens * rank; i += kTokenThreads) {
     const int a = ids[i / rank];
     float s = 0.0f;
     if ((uint32_t)a < (uint32_t)adapters) {
@@ -143,15 +143,15 @@ __global__ __launch_bounds__(kThreads, MT * NL >= 8 ? 2 : MT * NL >= 4 ? 3 : 4) 
     }
     lv[i] = s;
   }
-  join_waves<MT, NL, KS>(acc, red, wave, lane);
+  join_waves<MT, NL>(acc, red, wave, lane);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     if (mt * 16 >= tokens) continue;
 #pragma unroll
     for (int c = 0; c < NL; ++c) {
-      if ((mt * NL + c) % KS != wave || col0 + 16 * c >= n) continue;
+      if ((mt * NL + c) % P.ks != part || col0 + 16 * c >= n) continue;
       const int64_t col = col0 + 16 * c + (lane & 15);
-      const f32x4 sum = joined<MT, NL, KS>(red, mt, c, lane);
+      const f32x4 sum = joined<MT, NL>(red, group, P.ks, mt, c, lane);
       const float s = w_amax[col] / 2688.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -189,12 +189,6 @@ constexpr uint32_t kStage = kXBytes + kWBytes;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
-__device__ __forceinline__ rsrc_t range_rsrc(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(
-      reinterpret_cast<void*>(uni(reinterpret_cast<int64_t>(p))), 0,
-      uni((uint32_t)(bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF)), 0x00020000);
-}
-
 // Tile of 128 rows x 256 lines; wave w takes all rows and lines 64 w .. + 63,
 // so no weight is decoded twice in a work-group.  Element granules (8 of x,
 // 16 bytes) and code granules are XOR-placed in LDS so that fragment reads of
@@ -221,22 +215,22 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   const rsrc_t ws = range_rsrc(w_scale + col0 * sp, (int64_t)cols * sp);
   const uint32_t nk = (uint32_t)((k + kBK - 1) / kBK);
 
+  // x: 32 rows a copy, lane g: slot g % 8 of row g / 8 (rows 32 apart have the
+  // same granule); codes: 128 lines a copy, lane g: slot g % 2 of line g / 2.
+  // In the last step a granule past k is moved out of the buffer's range.
+  const uint32_t xgr = (tid & 7) ^ ((tid >> 3) & 7), xoff = (tid >> 3) * xp + 16 * xgr;
+  const uint32_t woff = (tid >> 1) * dp + 16 * ((tid & 1) ^ ((tid >> 3) & 1));
+  const uint32_t past = (nk - 1) * kBK + 8 * xgr < (uint32_t)k ? 0u : kOutOfRange;
   auto issue = [&](uint32_t ks, uint8_t* base) {
-    // x: 32 rows a copy, lane g: slot g % 8 of row g / 8
+    const uint32_t off = ks + 1 == nk ? xoff | past : xoff;
 #pragma unroll
-    for (int c = 0; c < kBM / 32; ++c) {
-      const uint32_t row = 32 * c + (tid >> 3), gr = (tid & 7) ^ (row & 7);
-      const bool in = ks * kBK + 8 * gr < (uint32_t)k;
+    for (int c = 0; c < kBM / 32; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xs, (lds_ptr_t)(base + 16 * (c * kThreads + wave * 64)), 16,
-                                               in ? row * xp + 16 * gr : kOutOfRange, ks * (2 * kBK), 0, 0);
-    }
-    // codes: 128 lines a copy, lane g: slot g % 2 of line g / 2
+                                               off + 32 * c * xp, ks * (2 * kBK), 0, 0);
 #pragma unroll
-    for (int c = 0; c < kBN / 128; ++c) {
-      const uint32_t line = 128 * c + (tid >> 1), gr = (tid & 1) ^ ((line >> 2) & 1);
+    for (int c = 0; c < kBN / 128; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(wd, (lds_ptr_t)(base + kXBytes + 16 * (c * kThreads + wave * 64)), 16,
-                                               line * dp + 16 * gr, ks * (kBK / 2), 0, 0);
-    }
+                                               woff + 128 * c * dp, ks * (kBK / 2), 0, 0);
   };
   // Scales of a step, two bytes a line for each lane half (blocks 2h, 2h + 1),
   // fetched a step ahead: a line's scales may start on any even byte.
@@ -272,105 +266,104 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
       const uint32_t line = wave * 64 + in * 32 + (lane & 31);
       wq[in] = *reinterpret_cast<const u32x4*>(base + kXBytes + 32 * line + 16 * (h ^ ((line >> 2) & 1)));
     }
-    // sub-step s, lane half h: the 8 elements of word 4h + s
-#pragma unroll
-    for (int s = 0; s < kBK / 16; ++s) {
-      __builtin_amdgcn_sched_barrier(0);  // keeps the four sub-steps' fragments from being live together
-      bf16x8 xf[kIM];
+    // Sub-step s, lane half h: the 8 elements of word 4h + s.  The next
+    // sub-step's fragments are read and decoded between this one's MFMAs (one
+    // MFMA to four VALU instructions: 32 decode a sub-step's two line tiles).
+    bf16x8 xf[2][kIM], wf[2][kIN];
+    auto fetch = [&](int s) {
 #pragma unroll
       for (int im = 0; im < kIM; ++im) {
         const uint32_t row = im * 32 + (lane & 31);
-        xf[im] = *reinterpret_cast<const bf16x8*>(base + 128 * row + 16 * ((4 * h + s) ^ (row & 7)));
+        xf[s & 1][im] = *reinterpret_cast<const bf16x8*>(base + 128 * row + 16 * ((4 * h + s) ^ (row & 7)));
       }
 #pragma unroll
-      for (int in = 0; in < kIN; ++in) {
-        const bf16x8 b = decode8_bf16(wq[in][s], sv[in][s >> 1]);
+      for (int in = 0; in < kIN; ++in) wf[s & 1][in] = decode8_bf16(wq[in][s], sv[in][s >> 1]);
+    };
+    fetch(0);
+#pragma unroll
+    for (int s = 0; s < kBK / 16; ++s) {
+      if (s + 1 < kBK / 16) fetch(s + 1);
+#pragma unroll
+      for (int in = 0; in < kIN; ++in)
 #pragma unroll
         for (int im = 0; im < kIM; ++im)
-          acc[im][in] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf[im], b, acc[im][in], 0, 0, 0);
+          acc[im][in] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf[s & 1][im], wf[s & 1][in], acc[im][in], 0, 0, 0);
+      if (s + 1 < kBK / 16) {
+        __builtin_amdgcn_sched_group_barrier(0x100, kIM, 0);  // the fragment reads
+#pragma unroll
+        for (int i = 0; i < kIM * kIN; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // four VALU
+        }
       }
     }
   };
   issue(0, lds0);
   fetch_scales(0);
+  uint32_t ks = 0;
 #pragma unroll 1
-  for (uint32_t ks = 0; ks < nk; ks += 2) {
+  for (; ks + 1 < nk; ks += 2) {
     step(ks, lds0, lds1);
-    if (ks + 1 >= nk) break;
     step(ks + 1, lds1, lds0);
   }
+  if (ks < nk) step(ks, lds0, lds1);
 
+  // Epilogue, one 32 x 32 block after the other: line factor, then every
+  // adapter that a row of the block has adds rank/16 MFMA steps of v B_a^T.
+  // Rows of other adapters meet B_a only as zeros, but a B_a that is not finite
+  // must not reach them either: each adapter's product is formed apart and
+  // added to its own rows alone.  Rows past the last are out of the output
+  // buffer's range, columns past the last are moved out of it.
   const uint32_t jw = wave * 64;  // first line of the wave in the tile
+  const uint32_t r16 = round16(rank), yp = (uint32_t)(2 * n);
+  const rsrc_t vh = range_rsrc(v + row0 * r16, (int64_t)rows * r16 * 2);
+  const rsrc_t vl = range_rsrc(v + (tokens + row0) * r16, (int64_t)rows * r16 * 2);
+  const rsrc_t ys = range_rsrc(y + row0 * n + col0, ((int64_t)rows - 1) * yp + 2 * cols);
+  const bool odd = lane & 1;
+  float lf[kIN];
 #pragma unroll
   for (int in = 0; in < kIN; ++in) {
     const uint32_t j = jw + in * 32 + (lane & 31);
-    const float s = j < cols ? w_amax[col0 + j] / 2688.0f : 0.0f;
-#pragma unroll
-    for (int im = 0; im < kIM; ++im) acc[im][in] *= s;
+    lf[in] = j < cols ? w_amax[col0 + j] / 2688.0f : 0.0f;
   }
-  // the adapters of the tile's rows, one after the other
-  int my[2];
-  uint64_t left[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t r = 64 * i + lane;
-    my[i] = adapters && r < rows ? ids[row0 + r] : -1;
-    left[i] = __ballot((uint32_t)my[i] < (uint32_t)adapters);
-  }
-  const int r16 = round16(rank);
-  while (left[0] | left[1]) {
-    const int a = left[0] ? __builtin_amdgcn_readlane(my[0], (int)__builtin_ctzll(left[0]))
-                          : __builtin_amdgcn_readlane(my[1], (int)__builtin_ctzll(left[1]));
-    const uint64_t sel[2] = {__ballot(my[0] == a), __ballot(my[1] == a)};
-    left[0] &= ~sel[0];
-    left[1] &= ~sel[1];
-    // Rows of other adapters meet B_a only as zeros, but a B_a that is not
-    // finite must not reach them either: unless a block of 32 rows is all this
-    // adapter's, its product is formed apart and added to its own rows alone.
+  for (int im = 0; im < kIM; ++im) {
+    const uint32_t row = im * 32 + (lane & 31);
+    const int my = adapters && row < rows ? ids[row0 + row] : -1;
+    const uint32_t any = (uint32_t)__ballot((uint32_t)my < (uint32_t)adapters);  // lanes 32-63 repeat lanes 0-31
 #pragma unroll
-    for (int im = 0; im < kIM; ++im) {
-      const uint32_t in32 = (uint32_t)(sel[im >> 1] >> (32 * (im & 1)));
-      if (in32 == 0) continue;
-      const bool mine = (in32 >> (lane & 31)) & 1;
-      const uint16_t* p = v + (row0 + im * 32 + (lane & 31)) * r16 + 8 * h;
-#pragma unroll
-      for (int in = 0; in < kIN; ++in) {
-        const uint32_t j = jw + in * 32 + (lane & 31);
-        const uint16_t* bp = lora_b + ((int64_t)a * n + col0 + j) * rank + 8 * h;
-        f32x16 part = in32 == 0xFFFFFFFFu ? acc[im][in] : f32x16{};
-        for (int r = 0; r < r16; r += 16) {
-          u32x4 b = u32x4{0, 0, 0, 0}, hi = b, lo = b;
-          if (j < cols && r + 8 * h < rank) b = *reinterpret_cast<const u32x4*>(bp + r);
-          if (mine) {
-            hi = *reinterpret_cast<const u32x4*>(p + r);
-            lo = *reinterpret_cast<const u32x4*>(p + tokens * r16 + r);
-          }
-          part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, hi), __builtin_bit_cast(bf16x8, b), part, 0, 0, 0);
-          part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, lo), __builtin_bit_cast(bf16x8, b), part, 0, 0, 0);
+    for (int in = 0; in < kIN; ++in) {
+      f32x16 sum = f32x16{};
+      const uint32_t boff = (jw + in * 32 + (lane & 31)) * rank * 2 + 16 * h;
+#pragma unroll 1
+      for (uint32_t left = any; left;) {
+        const int a = __builtin_amdgcn_readlane(my, (int)__builtin_ctz(left));
+        const uint32_t own = (uint32_t)__ballot(my == a);
+        left &= ~own;
+        const rsrc_t bs = range_rsrc(lora_b + ((int64_t)a * n + col0) * rank, (int64_t)cols * rank * 2);
+        const uint32_t voff = my == a ? row * r16 * 2 + 16 * h : kOutOfRange;
+        f32x16 part = f32x16{};
+#pragma unroll 1
+        for (uint32_t r = 0; r < r16; r += 16) {
+          const uint32_t bo = r + 8 * h < (uint32_t)rank ? boff + 2 * r : kOutOfRange;
+          const bf16x8 b = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(bs, bo, 0, 0));
+          const bf16x8 hi = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(vh, voff + 2 * r, 0, 0));
+          const bf16x8 lo = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(vl, voff + 2 * r, 0, 0));
+          part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, b, part, 0, 0, 0);
+          part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, b, part, 0, 0, 0);
         }
-        if (in32 == 0xFFFFFFFFu) {
-          acc[im][in] = part;
-        } else {
 #pragma unroll
-          for (int q = 0; q < 16; ++q)
-            if ((in32 >> (8 * (q >> 2) + 4 * h + (q & 3))) & 1) acc[im][in][q] += part[q];
-        }
+        for (int q = 0; q < 16; ++q) sum[q] += (own >> (8 * (q >> 2) + 4 * h + (q & 3))) & 1 ? part[q] : 0.0f;
       }
-    }
-  }
-  const bool odd = lane & 1;
-#pragma unroll
-  for (int in = 0; in < kIN; ++in) {
-    const uint32_t jp = (jw + in * 32 + (lane & 31)) & ~1u;
-#pragma unroll
-    for (int im = 0; im < kIM; ++im)
+      const uint32_t jp = (jw + in * 32 + (lane & 31)) & ~1u;
+      const uint32_t off = jp < cols ? (im * 32 + 4 * h + odd) * yp + 2 * jp : kOutOfRange;
 #pragma unroll
       for (int q = 0; q < 16; q += 2) {
-        const uint32_t i = im * 32 + 8 * (q >> 2) + 4 * h + (q & 3) + (odd ? 1 : 0);
         float lo, hi;
-        pair_columns(acc[im][in][q], acc[im][in][q + 1], odd, &lo, &hi);
-        if (jp < cols && i < rows) *reinterpret_cast<uint32_t*>(y + (row0 + i) * n + col0 + jp) = pack_bf16(lo, hi);
+        pair_columns(acc[im][in][q] * lf[in] + sum[q], acc[im][in][q + 1] * lf[in] + sum[q + 1], odd, &lo, &hi);
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(lo, hi), ys, off + (8 * (q >> 2) + (q & 3)) * yp, 0, 0);
       }
+    }
   }
 }
 
@@ -379,7 +372,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
 // Parts of the contraction over work-groups for few rows: enough to spread a
 // long contraction, whole steps each.
 int shrink_parts(int64_t k) {
-  const int64_t steps = (k + kStepK - 1) / kStepK, p = (steps + 7) / 8;
+  const int64_t steps = (k + kShrinkStep - 1) / kShrinkStep, p = (steps + 3) / 4;
   return (int)(p < 1 ? 1 : p > kMaxSplit ? kMaxSplit : p);
 }
 
@@ -395,9 +388,13 @@ template <int MT, int NL>
 void launch_few(const uint16_t* x, int tokens, int64_t k, const uint8_t* wd, const uint8_t* ws, const float* wa,
                 int64_t n, const uint16_t* b, const float* alpha, int adapters, int rank, const int32_t* ids,
                 const float* v, int parts, uint16_t* y, hipStream_t st) {
-  const dim3 grid((uint32_t)((n + NL * 16 - 1) / (NL * 16)));
-  hipLaunchKernelGGL((few_rows_kernel<MT, NL>), grid, dim3(kThreads), adapters ? tokens * rank * 4 : 0, st, x, tokens,
-                     k, wd, ws, wa, n, b, alpha, adapters, adapters ? rank : 0, ids, v, parts, y);
+  int ks = 1;
+  while (ks < 8 && (n + 16 * NL * (8 / ks) - 1) / (16 * NL * (8 / ks)) < 200) ks *= 2;
+  const TokenPlan P = token_plan(k, tokens, ks, MT * NL, adapters ? (int64_t)tokens * rank * 4 : 0,
+                                 (n + 16 * NL * (8 / ks) - 1) / (16 * NL * (8 / ks)));
+  const int cols = NL * 16 * (kTokenWaves / P.ks);
+  hipLaunchKernelGGL((few_rows_kernel<MT, NL>), dim3((uint32_t)((n + cols - 1) / cols)), dim3(kTokenThreads), P.lds, st, x,
+                     tokens, k, wd, ws, wa, n, b, alpha, adapters, adapters ? rank : 0, ids, v, parts, P, y);
 }
 
 }  // namespace

@@ -2,17 +2,12 @@
 // times NVFP4 weights, no packed groups, behind the C ABI of
 // include/moe_ops.h.  Also the adapter projection of a few tokens.
 //
-// What bounds it is reading the chosen experts' weights once (0.5625 byte an
-// element).  A work-group takes one expert (the first pair that chose it is
-// its leader; the work-groups of later pairs with the same expert end at once)
-// and a run of weight lines, and multiplies them by all pairs of that expert,
-// 16 * MT at a time.  MFMA 16x16x32: rows are tokens, columns are lines, so a
-// tile costs the same for 1 token as for 16, and the matrix units are far from
-// the limit.  Lane (n = lane % 16, g = lane / 16) loads 16 bytes of line n's
-// 64-byte step (32 codes, two blocks) and its two scale bytes, decodes them in
-// registers, and the same lane mapping picks the matching 32 values of x.
-// With few work-groups the contraction is split over the KS waves of a
-// work-group and joined in LDS in a fixed order.
+// A work-group takes one expert (the first pair that chose it is its leader;
+// the work-groups of later pairs with the same expert end at once) and a run
+// of weight lines, and multiplies them by all pairs of that expert, 16 * MT at
+// a time, so each chosen expert's weights are read once.
+#include <algorithm>
+
 #include "moe_token.hpp"
 
 namespace {
@@ -25,7 +20,7 @@ __device__ int gather_pairs(const int32_t* ids, int pairs, int lead, int e, int3
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int at = 0;
   bool earlier = false;
-  for (int p0 = 0; p0 < pairs; p0 += kThreads) {
+  for (int p0 = 0; p0 < pairs; p0 += kTokenThreads) {
     const int p = p0 + tid;
     const bool mine = p < pairs && ids[p] == e;
     earlier |= mine && p < lead;
@@ -33,7 +28,7 @@ __device__ int gather_pairs(const int32_t* ids, int pairs, int lead, int e, int3
     if (lane == 0) wcnt[wave] = __popcll(b);
     if (__syncthreads_or(earlier)) return 0;
     int before = at;
-    for (int w = 0; w < kThreads / 64; ++w) {
+    for (int w = 0; w < kTokenWaves; ++w) {
       if (w < wave) before += wcnt[w];
       at += wcnt[w];
     }
@@ -44,67 +39,69 @@ __device__ int gather_pairs(const int32_t* ids, int pairs, int lead, int e, int3
 }
 
 // x rows: pair / per (per = topk: the token's row is shared by its choices).
-template <int MODE, int ACT, int MT, int NL, int KS>
-__global__ __launch_bounds__(kThreads, MT * NL >= 8 ? 2 : MT * NL >= 4 ? 3 : 4) void token_kernel(
+template <int MODE, int ACT, int MT, int NL>
+__global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void token_kernel(
     const uint16_t* __restrict__ x, int64_t k, int per, const int32_t* __restrict__ ids, int pairs,
     const uint8_t* __restrict__ b_data, const uint8_t* __restrict__ b_scale, const float* __restrict__ b_amax,
-    int64_t n, int E, void* __restrict__ out) {
+    int64_t n, int E, TokenPlan P, void* __restrict__ out) {
   __shared__ int32_t list[MOE_MAX_TOKEN_PAIRS];
-  __shared__ int32_t wcnt[kThreads / 64];
-  __shared__ f32x4 red[KS > 1 ? KS * MT * NL * 64 : 1];
+  __shared__ int32_t wcnt[kTokenWaves];
+  extern __shared__ __attribute__((aligned(16))) uint8_t xlds[];
   constexpr int kCols = MODE == kModeGlu ? NL / 2 * 16 : NL * 16;   // output columns of a wave
   const int lane = threadIdx.x & 63, wave = uni((int32_t)(threadIdx.x >> 6));
   const int lead = uni((int32_t)blockIdx.y);
   const int e = uni(ids[lead]);
   const int64_t ocols = MODE == kModeGlu ? n / 2 : n;
-  const int64_t col0 = ((int64_t)blockIdx.x * (4 / KS) + wave / KS) * kCols;
+  const int groups = kTokenWaves / P.ks, group = wave / P.ks, part = wave % P.ks;
+  const int64_t first_col = (int64_t)blockIdx.x * groups * kCols, col0 = first_col + group * kCols;
   if ((uint32_t)e >= (uint32_t)E) {  // no expert: a row of zeros
-    const int64_t c0 = (int64_t)blockIdx.x * (4 / KS) * kCols, c1 = min<int64_t>(c0 + 4 / KS * kCols, ocols);
-    for (int64_t c = c0 + threadIdx.x; c < c1; c += kThreads) {
+    const int64_t c1 = min<int64_t>(first_col + groups * kCols, ocols);
+    for (int64_t c = first_col + threadIdx.x; c < c1; c += kTokenThreads) {
       if (MODE == kModeGlu) reinterpret_cast<uint16_t*>(out)[lead * ocols + c] = 0;
       else reinterpret_cast<float*>(out)[lead * ocols + c] = 0.0f;
     }
     return;
   }
-  const int cnt = gather_pairs(ids, pairs, lead, e, list, wcnt);
+  // The choices of a lone token are taken one by one (a token that names an
+  // expert twice reads its weights twice), with nothing to gather.
+  const bool lone = pairs <= per;
+  const int cnt = lone ? 1 : gather_pairs(ids, pairs, lead, e, list, wcnt);
   if (cnt == 0) return;
+  auto pair_at = [&](int i) { return lone ? lead : list[i]; };
   const int64_t line0 = (int64_t)e * n;
   TileLines<MODE, NL> W;
   W.init(b_data, b_scale, line0, col0, ocols, k, lane);
-  for (int first = 0; first < cnt; first += 16 * MT) {
-    const uint16_t* xr[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int i = first + mt * 16 + (lane & 15);
-      xr[mt] = x + (int64_t)(list[i < cnt ? i : first] / per) * k;
-    }
+  f32x4* red = reinterpret_cast<f32x4*>(xlds);
+  for (int first = 0; first < cnt; first += P.rows) {
     f32x4 acc[MT][NL];
-    token_multiply<MT, NL, KS>(W, xr, k, wave % KS, lane, acc);
-    if (KS > 1) join_waves<MT, NL, KS>(acc, red, wave, lane);
-    // each wave finishes its share: all of its tiles, or with split waves the
-    // tiles whose number is the wave's own
+    if (first) __syncthreads();  // the last pass is done with the staged rows and the joined sums
+    const int rows = min(cnt - first, P.rows);
+    token_multiply<MT, NL>(W, P, x, k, rows, part, lane, xlds,
+                           [&](int i) { return (int64_t)(pair_at(first + i) / per); }, acc);
+    if (P.ks > 1) join_waves<MT, NL>(acc, red, wave, lane);
+    // each wave finishes its share: with split waves the tiles whose number
+    // is its part's
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      if (first + mt * 16 >= cnt) continue;
+      if (mt * 16 >= rows) continue;
 #pragma unroll
       for (int c = 0; c < kCols / 16; ++c) {
-        if (KS > 1 && (mt * (kCols / 16) + c) % KS != wave) continue;
+        if ((mt * (kCols / 16) + c) % P.ks != part || col0 + 16 * c >= ocols) continue;
         const int64_t col = col0 + 16 * c + (lane & 15);
-        if (col0 + 16 * c >= ocols) continue;
         f32x4 a, b;
         if (MODE == kModeGlu) {
-          a = KS > 1 ? joined<MT, NL, KS>(red, mt, 2 * c, lane) : acc[mt][2 * c];
-          b = KS > 1 ? joined<MT, NL, KS>(red, mt, 2 * c + 1, lane) : acc[mt][2 * c + 1];
+          a = P.ks > 1 ? joined<MT, NL>(red, group, P.ks, mt, 2 * c, lane) : acc[mt][2 * c];
+          b = P.ks > 1 ? joined<MT, NL>(red, group, P.ks, mt, 2 * c + 1, lane) : acc[mt][2 * c + 1];
         } else {
-          a = KS > 1 ? joined<MT, NL, KS>(red, mt, c, lane) : acc[mt][c];
+          a = P.ks > 1 ? joined<MT, NL>(red, group, P.ks, mt, c, lane) : acc[mt][c];
         }
         const float s = b_amax[line0 + col] / 2688.0f;
         const float su = MODE == kModeGlu ? b_amax[line0 + ocols + col] / 2688.0f : 0.0f;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const int i = first + mt * 16 + 4 * (lane >> 4) + v;
-          if (i >= cnt) continue;
-          const int64_t p = list[i];
+          const int i = mt * 16 + 4 * (lane >> 4) + v;
+          if (i >= rows) continue;
+          const int64_t p = pair_at(first + i);
           if (MODE == kModeGlu) {
             float dv;
             const float g = a[v] * s, u = b[v] * su;
@@ -115,40 +112,38 @@ __global__ __launch_bounds__(kThreads, MT * NL >= 8 ? 2 : MT * NL >= 4 ? 3 : 4) 
         }
       }
     }
-    if (KS > 1) __syncthreads();  // red is written again by the next pass
   }
 }
 
 // ------------------------------------------------------------- host side
 
-template <int MODE, int ACT, int MT, int NL, int KS>
+template <int MODE, int ACT, int MT>
 void launch(const uint16_t* x, int64_t k, int per, const int32_t* ids, int pairs, const uint8_t* bd,
             const uint8_t* bs, const float* ba, int64_t n, int E, void* out, hipStream_t st) {
-  constexpr int kCols = (MODE == kModeGlu ? NL / 2 * 16 : NL * 16) * (4 / KS);
-  const int64_t ocols = MODE == kModeGlu ? n / 2 : n;
-  const dim3 grid((uint32_t)((ocols + kCols - 1) / kCols), (uint32_t)pairs);
-  hipLaunchKernelGGL((token_kernel<MODE, ACT, MT, NL, KS>), grid, dim3(kThreads), 0, st, x, k, per, ids, pairs, bd, bs,
-                     ba, n, E, out);
+  constexpr int NL = 2, kCols = MODE == kModeGlu ? 16 : 32;
+  const int64_t ocols = MODE == kModeGlu ? n / 2 : n, experts = std::min(pairs, E);
+  auto tiles = [&](int ks) { return (ocols + kCols * (kTokenWaves / ks) - 1) / (kCols * (kTokenWaves / ks)); };
+  // Waves that split the contraction: as few as leave two work-groups a CU,
+  // with the experts that the pairs can reach.
+  int ks = 1;
+  while (ks < kTokenWaves && experts * tiles(ks) < 2 * kCus) ks *= 2;
+  // an expert has at most one pair of a token, or takes more passes
+  const int rows = std::min((pairs + per - 1) / per, 16 * MT);
+  const TokenPlan P = token_plan(k, rows, ks, MT * NL, 0, experts * tiles(ks));
+  hipLaunchKernelGGL((token_kernel<MODE, ACT, MT, NL>), dim3((uint32_t)tiles(P.ks), (uint32_t)pairs),
+                     dim3(kTokenThreads), P.lds, st, x, k, per, ids, pairs, bd, bs, ba, n, E, P, out);
 }
 
 template <int MODE, int ACT>
 void dispatch(const uint16_t* x, int64_t k, int per, const int32_t* ids, int pairs, const uint8_t* bd,
               const uint8_t* bs, const float* ba, int64_t n, int E, void* out, hipStream_t st) {
-  // Work-groups there will be at least: the experts that pairs can reach.
-  const int64_t experts = pairs < E ? pairs : E;
   // Token tiles of a pass: the pairs an expert gets on average, with room for
   // an uneven choice, never more than the tokens there are.
-  const int64_t mean = (pairs + experts - 1) / experts, most = (pairs + per - 1) / per;
-  const int64_t tiles = ((mean * 3 / 2 < most ? mean * 3 / 2 : most) + 15) / 16;
-  const int64_t wide_waves = experts * ((n + 63) / 64);
-  if (tiles <= 1) {
-    if (wide_waves >= 4096) launch<MODE, ACT, 1, 4, 1>(x, k, per, ids, pairs, bd, bs, ba, n, E, out, st);
-    else launch<MODE, ACT, 1, 2, 4>(x, k, per, ids, pairs, bd, bs, ba, n, E, out, st);
-  } else if (tiles == 2) {
-    launch<MODE, ACT, 2, 2, 4>(x, k, per, ids, pairs, bd, bs, ba, n, E, out, st);
-  } else {
-    launch<MODE, ACT, 4, 2, 4>(x, k, per, ids, pairs, bd, bs, ba, n, E, out, st);
-  }
+  const int64_t experts = std::min(pairs, E), mean = (pairs + experts - 1) / experts, most = (pairs + per - 1) / per;
+  const int64_t rows = std::min(mean * 3 / 2, most);
+  if (rows <= 16) launch<MODE, ACT, 1>(x, k, per, ids, pairs, bd, bs, ba, n, E, out, st);
+  else if (rows <= 32) launch<MODE, ACT, 2>(x, k, per, ids, pairs, bd, bs, ba, n, E, out, st);
+  else launch<MODE, ACT, 4>(x, k, per, ids, pairs, bd, bs, ba, n, E, out, st);
 }
 
 int check_token(const uint16_t* x, int64_t pairs, int64_t k, const int32_t* ids, const uint8_t* bd, const uint8_t* bs,
