@@ -88,8 +88,10 @@ __device__ __forceinline__ rsrc_t lines_rsrc(const uint8_t* p, uint32_t bytes) {
 // Contraction order: word 8h + s of a line's 64-byte chunk feeds sub-step s of
 // lane half h, in A and B alike, so a lane reads its eight sub-steps' words
 // with two 16-byte LDS reads.
+// A wave whose columns all lie past the last one (`live` false) copies and
+// waits with the others but multiplies nothing.
 template <bool PAIR>
-__device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const Lines& B1, uint32_t L,
+__device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const Lines& B1, uint32_t L, bool live,
                                          f32x16 (&acc)[kWM][kWN], uint8_t* lds0, uint8_t* lds1, uint8_t* lsc) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const uint32_t dpitch = uni(L / 2), spitch = uni(L / 16);
@@ -156,6 +158,7 @@ __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const 
       const uint32_t nb = (ks + 1) / kScSteps;
       if ((ks + 1) % kScSteps == 0) issue_scales(nb, lsc + (nb & 1) * kScBlockBytes);
     }
+    if (!live) return;
     u32x4 wa[kWM][2], wb[kWN][2];
 #pragma unroll
     for (int im = 0; im < kWM; ++im) {
@@ -227,6 +230,36 @@ __device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t ntm, uint32_t 
   *tn = uni(in / gm);
 }
 
+// A wave's own 12 KB of the code stages, which are free in the epilogue: 32
+// rows x 64 columns of fp32 go in as the MFMA layout holds them (column in the
+// lane, two 32-column blocks) and come out as 8 consecutive columns of a row,
+// so that memory sees 16 bytes a lane and 128 contiguous bytes a row.
+constexpr int kStagePitch = 72;  // floats: the two lane halves, 4 rows apart, on different banks
+static_assert(32 * kStagePitch * 4 <= (int)kStageBytes / 2, "two waves share a stage");
+__device__ __forceinline__ float* wave_stage(uint8_t* lds0, uint8_t* lds1, int wave) {
+  return reinterpret_cast<float*>((wave < 2 ? lds0 : lds1) + (wave & 1) * (kStageBytes / 2));
+}
+__device__ __forceinline__ void stage_put(float* stage, int block, int v, int lane, float x) {
+  stage[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * kStagePitch + 32 * block + (lane & 31)] = x;
+}
+__device__ __forceinline__ void stage_get(const float* stage, int row, int col, float (&x)[8]) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(stage + row * kStagePitch + col);
+  const f32x4 b = *reinterpret_cast<const f32x4*>(stage + row * kStagePitch + col + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = a[i];
+    x[4 + i] = b[i];
+  }
+}
+// Orders a wave's own LDS writes and reads (they run in issue order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+
 struct Operands {
   const uint8_t *a_data, *a_scale;
   const float* a_amax;
@@ -268,9 +301,11 @@ __global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_
   for (int im = 0; im < kWM; ++im)
 #pragma unroll
     for (int in = 0; in < kWN; ++in) acc[im][in] = f32x16{};
-  multiply<true>(A, G, U, (uint32_t)k, acc, lds0, lds1, lsc);
+  const int tid = threadIdx.x, wave = uni((int32_t)(tid >> 6)), lane = tid & 63;
+  const int wm = wave / kWavesN, wn = wave % kWavesN;
+  const bool live = (uint32_t)wn * 64 < cols;
+  multiply<true>(A, G, U, (uint32_t)k, live, acc, lds0, lds1, lsc);
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   if (tid < kBM) lsa[tid] = O.a_amax[row0 + tid] / 2688.0f;
   {
     const uint32_t j = tid & 127;
@@ -278,34 +313,48 @@ __global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_
     lsb[tid] = j < cols ? am[j] / 2688.0f : 0.0f;
   }
   __syncthreads();
-  const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const bool odd = lane & 1;
+  if (!live) return;
+  float* stage = wave_stage(lds0, lds1, wave);
+  const uint32_t j0 = wn * 64, c = 8 * (lane & 7);
+  const bool write = j0 + c < cols;
 #pragma unroll
-  for (int in = 0; in < kWN / 2; ++in) {
-    const uint32_t j = wn * 64 + in * 32 + (lane & 31);
-    const float sg = lsb[j], su = lsb[128 + j];
-    const uint32_t jp = j & ~1u;
-    const bool write = jp < cols;
+  for (int im = 0; im < kWM; ++im) {
+    const int64_t out0 = row0 + wm * (kWM * 32) + im * 32;
+    float g[2][16], u[2][16];
 #pragma unroll
-    for (int im = 0; im < kWM; ++im)
+    for (int in = 0; in < 2; ++in) {
+      const float sg = lsb[j0 + in * 32 + (lane & 31)], su = lsb[128 + j0 + in * 32 + (lane & 31)];
 #pragma unroll
-      for (int v = 0; v < 16; v += 2) {
-        const uint32_t i = wm * (kWM * 32) + im * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-        const float sa0 = lsa[i], sa1 = lsa[i + 1];
-        const float g0 = (acc[im][in][v] * sa0) * sg, g1 = (acc[im][in][v + 1] * sa1) * sg;
-        const float u0 = (acc[im][in + 2][v] * sa0) * su, u1 = (acc[im][in + 2][v + 1] * sa1) * su;
-        const int64_t row = row0 + i + (odd ? 1 : 0);
-        float lo, hi;
-        pair_columns(glu<ACT>(g0, u0), glu<ACT>(g1, u1), odd, &lo, &hi);
-        if (write) *reinterpret_cast<uint32_t*>(h + row * f + col0 + jp) = pack_bf16(lo, hi);
-        if (KEEP) {
-          uint16_t* p = gu + row * 2 * f + col0 + jp;
-          pair_columns(g0, g1, odd, &lo, &hi);
-          if (write) *reinterpret_cast<uint32_t*>(p) = pack_bf16(lo, hi);
-          pair_columns(u0, u1, odd, &lo, &hi);
-          if (write) *reinterpret_cast<uint32_t*>(p + f) = pack_bf16(lo, hi);
-        }
+      for (int v = 0; v < 16; ++v) {
+        const float sa = lsa[wm * (kWM * 32) + im * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
+        g[in][v] = (acc[im][in][v] * sa) * sg;
+        u[in][v] = (acc[im][in + 2][v] * sa) * su;
+        stage_put(stage, in, v, lane, glu<ACT>(g[in][v], u[in][v]));
       }
+    }
+    auto put_rows = [&](uint16_t* base, int64_t pitch) {
+      wave_sync();
+#pragma unroll
+      for (int r = 0; r < 32; r += 8) {
+        float v[8];
+        stage_get(stage, r + (lane >> 3), c, v);
+        if (write) *reinterpret_cast<u32x4*>(base + (out0 + r + (lane >> 3)) * pitch + col0 + j0 + c) = pack8(v);
+      }
+      wave_sync();
+    };
+    put_rows(h, f);
+    if (KEEP) {
+#pragma unroll
+      for (int in = 0; in < 2; ++in)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) stage_put(stage, in, v, lane, g[in][v]);
+      put_rows(gu, 2 * f);
+#pragma unroll
+      for (int in = 0; in < 2; ++in)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) stage_put(stage, in, v, lane, u[in][v]);
+      put_rows(gu + f, 2 * f);
+    }
   }
 }
 
@@ -337,44 +386,62 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
   for (int im = 0; im < kWM; ++im)
 #pragma unroll
     for (int in = 0; in < kWN; ++in) acc[im][in] = f32x16{};
-  multiply<false>(A, B, B, (uint32_t)k, acc, lds0, lds1, lsc);
+  const int tid = threadIdx.x, wave = uni((int32_t)(tid >> 6)), lane = tid & 63;
+  const int wm = wave / kWavesN, wn = wave % kWavesN;
+  const bool live = (uint32_t)wn * 128 < cols;
+  multiply<false>(A, B, B, (uint32_t)k, live, acc, lds0, lds1, lsc);
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   if (tid < kBM) lsa[tid] = O.a_amax[row0 + tid] / 2688.0f;
   lsb[tid] = (uint32_t)tid < cols ? O.b_amax[line0 + tid] / 2688.0f : 0.0f;
   __syncthreads();
-  const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const bool odd = lane & 1;
+  if (!live) return;
+  float* stage = wave_stage(lds0, lds1, wave);
 #pragma unroll
-  for (int in = 0; in < kWN; ++in) {
-    const uint32_t j = wn * 128 + in * 32 + (lane & 31);
-    const float sb = lsb[j];
-    const uint32_t jp = j & ~1u;
-    const bool write = jp < cols;
+  for (int im = 0; im < kWM; ++im)
 #pragma unroll
-    for (int im = 0; im < kWM; ++im)
+    for (int pair = 0; pair < kWN; pair += 2) {
+      const uint32_t j0 = wn * 128 + pair * 32, c = 8 * (lane & 7);
+      const bool write = j0 + c < cols;
+      const int64_t at0 = (row0 + wm * (kWM * 32) + im * 32 + (lane >> 3)) * 2 * f + col0 + j0 + c;
+      u32x4 gq[4], uq[4];
 #pragma unroll
-      for (int v = 0; v < 16; v += 2) {
-        const uint32_t i = wm * (kWM * 32) + im * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-        float dh[2];
-        pair_columns((acc[im][in][v] * lsa[i]) * sb, (acc[im][in][v + 1] * lsa[i + 1]) * sb, odd, &dh[0], &dh[1]);
-        if (!write) continue;
-        const int64_t at = (row0 + i + (odd ? 1 : 0)) * 2 * f + col0 + jp;
-        const uint32_t gq = *reinterpret_cast<const uint32_t*>(gu + at);
-        const uint32_t uq = *reinterpret_cast<const uint32_t*>(gu + at + f);
-        const float g[2] = {bf16lo(gq), bf16hi(gq)}, u[2] = {bf16lo(uq), bf16hi(uq)};
-        float dg[2], du[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float dv;
-          const float q = act_logistic<ACT>(g[c], &dv), a = g[c] * q;
-          du[c] = dh[c] * a;
-          dg[c] = dh[c] * u[c] * __builtin_fmaf(a * (1.0f - q), dv, q);
+      for (int r = 0; r < 4; ++r) {
+        gq[r] = uq[r] = u32x4{0, 0, 0, 0};
+        if (write) {
+          gq[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(gu + at0 + 16 * r * f));
+          uq[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(gu + at0 + 16 * r * f + f));
         }
-        *reinterpret_cast<uint32_t*>(dgu + at) = pack_bf16(dg[0], dg[1]);
-        *reinterpret_cast<uint32_t*>(dgu + at + f) = pack_bf16(du[0], du[1]);
       }
-  }
+#pragma unroll
+      for (int in = 0; in < 2; ++in) {
+        const float sb = lsb[j0 + in * 32 + (lane & 31)];
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const float sa = lsa[wm * (kWM * 32) + im * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
+          stage_put(stage, in, v, lane, (acc[im][pair + in][v] * sa) * sb);
+        }
+      }
+      wave_sync();
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float dh[8], dg[8], du[8];
+        stage_get(stage, 8 * r + (lane >> 3), c, dh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float g = i & 1 ? bf16hi(gq[r][i >> 1]) : bf16lo(gq[r][i >> 1]);
+          const float u = i & 1 ? bf16hi(uq[r][i >> 1]) : bf16lo(uq[r][i >> 1]);
+          float dv;
+          const float q = act_logistic<ACT>(g, &dv), a = g * q;
+          du[i] = dh[i] * a;
+          dg[i] = dh[i] * u * __builtin_fmaf(a * (1.0f - q), dv, q);
+        }
+        if (write) {
+          *reinterpret_cast<u32x4*>(dgu + at0 + 16 * r * f) = pack8(dg);
+          *reinterpret_cast<u32x4*>(dgu + at0 + 16 * r * f + f) = pack8(du);
+        }
+      }
+      wave_sync();
+    }
 }
 
 // ------------------------------------------------------------- host side
