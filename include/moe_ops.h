@@ -204,9 +204,10 @@ int moe_token_linear(const uint16_t* x, int64_t pairs, int64_t k,
  * is kept in fp32 between the two steps.  adapter_ids may be in any order.  k: a positive
  * multiple of 32, n of 16, rank of 8 up to LORA_MAX_RANK; num_adapters 0 (with
  * NULL lora_a, lora_b, alpha) is the projection alone.  workspace: at least
- * lora_workspace(tokens, k, rank) bytes, 16-byte aligned. */
+ * lora_workspace(tokens, k, n, rank) bytes (rank 0 without adapters), 16-byte
+ * aligned; about 24 MiB at most beside the adapters' inner products. */
 #define LORA_MAX_RANK 128
-int64_t lora_workspace(int64_t tokens, int64_t k, int32_t rank);
+int64_t lora_workspace(int64_t tokens, int64_t k, int64_t n, int32_t rank);
 int lora_linear(const uint16_t* x, int64_t tokens, int64_t k,
                 const uint8_t* w_data, const uint8_t* w_scale,
                 const float* w_amax, int64_t n, const uint16_t* lora_a,

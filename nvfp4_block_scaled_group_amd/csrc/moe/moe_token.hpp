@@ -27,6 +27,10 @@ constexpr int kTokenWaves = kTokenThreads / 64;
 constexpr int kTokenLds = 72 * 1024;  // of the 160 KB of a CU, so that two work-groups fit; twice that where one is enough
 constexpr int kCus = 256;
 
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+// s_waitcnt for at most n outstanding vector-memory operations.
+constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
 // Waves on a SIMD that the registers leave room for.
 constexpr int token_waves(int mt) { return mt >= 4 ? 2 : 4; }
 
@@ -124,13 +128,14 @@ struct StepCodes {
 // after the caller's next barrier.
 template <int MT, int NL, class W, class RowOf>
 __device__ __forceinline__ void token_multiply(const W& w, const TokenPlan& P, const uint16_t* x, int64_t k,
-                                               int rows, int part, int lane, uint8_t* xlds, RowOf row_of,
+                                               int rows, int wave, int lane, uint8_t* xlds, RowOf row_of,
                                                f32x4 (&acc)[MT][NL]) {
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < NL; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
   const uint32_t steps = (uint32_t)((k + kStepK - 1) / kStepK);
+  const int part = wave % P.ks;
   const uint32_t span = P.ks * P.per;  // steps of a chunk
   const int e0 = (int)(k - (int64_t)(steps - 1) * kStepK) - 64 * (lane >> 4);  // this lane's elements in the last step
   const uint32_t cut[2] = {e0 > 0 ? 0u : kOutOfRange, e0 > 32 ? 0u : kOutOfRange};
@@ -166,17 +171,17 @@ __device__ __forceinline__ void token_multiply(const W& w, const TokenPlan& P, c
   };
   for (int c = 0; c < P.chunks; ++c) {
     if (c) __syncthreads();
-    // stage the chunk's x: 16-byte pieces, zeros past k
+    // stage the chunk's x by direct copies, 1 KB of a row each (past k, out of
+    // the row's range, they write zeros)
     const int64_t k0 = (int64_t)c * span * kStepK;
-    const int pieces = span * (kStepK / 8);
-    for (int r = threadIdx.x >> 6; r < rows; r += kTokenWaves) {
-      const uint16_t* src = x + row_of(r) * k + k0;
-      for (int p = lane; p < pieces; p += 64) {
-        u32x4 v = u32x4{0, 0, 0, 0};
-        if (k0 + 8 * p < k) v = *reinterpret_cast<const u32x4*>(src + 8 * p);
-        *reinterpret_cast<u32x4*>(xlds + r * P.pitch + 16 * p) = v;
-      }
+    const int pieces = span / 2;
+    for (int i = wave; i < rows * pieces; i += kTokenWaves) {
+      const int r = i / pieces, p = i - r * pieces;
+      const rsrc_t xs = range_rsrc(x + row_of(r) * k + k0, 2 * (k > k0 ? k - k0 : 0));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xs, (lds_ptr_t)(xlds + r * P.pitch + 1024 * p), 16, 16 * lane + 1024 * p, 0, 0,
+                                               0);
     }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
     const uint8_t* xs = xlds + part * P.per * (2 * kStepK);
 #pragma unroll 1

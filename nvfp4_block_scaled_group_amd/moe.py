@@ -64,7 +64,7 @@ def load_library() -> ctypes.CDLL:
     L.moe_glu_bwd_graphsafe.argtypes = _NVFP4 * 2 + [_I64, _I64, _I64, _I32, _P, _P, _I32, _P, _P, _P]
     L.moe_token_glu.argtypes = [_P, _I64, _I64, _I32, _P] + _NVFP4 + [_I64, _I32, _I32, _P, _P]
     L.moe_token_linear.argtypes = [_P, _I64, _I64, _P] + _NVFP4 + [_I64, _I32, _P, _P]
-    L.lora_workspace.argtypes = [_I64, _I64, _I32]
+    L.lora_workspace.argtypes = [_I64, _I64, _I64, _I32]
     L.lora_linear.argtypes = [_P, _I64, _I64] + _NVFP4 + [_I64, _P, _P, _P, _I32, _I32, _P, _P, _P, _I64, _P]
     for name in EXPORTS:
         getattr(L, name).restype = ctypes.c_int64 if name.endswith("_workspace") else ctypes.c_int
@@ -299,9 +299,9 @@ def moe_token_linear(x, ids, b_data, b_scale, b_amax, out, stream=None):
 
 # ----------------------------------------------------------------- adapters
 
-def lora_workspace(tokens: int, k: int, rank: int) -> int:
-    """Bytes of workspace that lora_linear needs."""
-    return int(load_library().lora_workspace(int(tokens), int(k), int(rank)))
+def lora_workspace(tokens: int, k: int, n: int, rank: int) -> int:
+    """Bytes of workspace that lora_linear needs (rank 0: no adapters)."""
+    return int(load_library().lora_workspace(int(tokens), int(k), int(n), int(rank)))
 
 
 def lora_linear(x, w_data, w_scale, w_amax, lora_a, lora_b, adapter_ids, alpha, y, workspace, stream=None):

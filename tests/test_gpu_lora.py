@@ -23,7 +23,7 @@ def make(seed, T, N, K, r, A):
 
 def call(w, xt, at, bt, ids, alpha, T, N, K, r):
     y = Guarded(2 * T * N, torch.bfloat16, (T, N))
-    ws = torch.full((max(16, moe.lora_workspace(T, K, r)),), 0xFF, dtype=torch.uint8, device="cuda:0")  # NaN patterns
+    ws = torch.full((max(16, moe.lora_workspace(T, K, N, r)),), 0xFF, dtype=torch.uint8, device="cuda:0")  # NaN patterns
     moe.lora_linear(xt.to("cuda:0"), *[R.to_dev(v) for v in w], at.to("cuda:0"), bt.to("cuda:0"),
                     R.to_dev(ids.astype(np.int32)), R.to_dev(alpha), y.t, ws)
     torch.cuda.synchronize()
@@ -107,7 +107,7 @@ def test_offsets_past_32_bits():
     y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda:0")
     ids = torch.full((T,), -1, dtype=torch.int32, device="cuda:0")
     ids[rows] = 0
-    ws = torch.empty(moe.lora_workspace(T, K, r), dtype=torch.uint8, device="cuda:0")
+    ws = torch.empty(moe.lora_workspace(T, K, N, r), dtype=torch.uint8, device="cuda:0")
     moe.lora_linear(x, *[R.to_dev(t) for t in w], at.to("cuda:0"), bt.to("cuda:0"), ids, R.to_dev(alpha), y, ws)
     torch.cuda.synchronize()
     want, err = expect(w, v, a, b, [0] * len(rows), alpha.astype(np.float64), K, r)

@@ -121,8 +121,8 @@ def test_nothing_to_do_is_no_error(lib):
 def test_workspace_sizes(lib):
     assert moe.moe_plan_workspace(4096, 512) == 0 and moe.moe_plan_workspace(4097, 512) > 0
     assert moe.moe_plan_workspace(0, 4096) > 0
-    assert moe.lora_workspace(0, 64, 8) == 0
-    assert moe.lora_workspace(65, 64, 8) == 65 * 16 * 4
+    assert moe.lora_workspace(0, 64, 16, 8) == 0
+    assert moe.lora_workspace(65, 64, 16, 8) >= 65 * 16 * 4
 
 
 class _NoCalls:
