@@ -7,7 +7,7 @@
 // takes 16 rows and multiplies them (MFMA 16x16x32) by one of the adapters
 // that any of them has.  Then the shared projection follows, with the adapters
 // in its epilogue:
-//   few rows (at most 64)  the weight is read once and bounds it; every
+//   few rows (at most 32)  the weight is read once and bounds it; every
 //                          16-line tile adds its rows' B_a v in fp32;
 //   more rows              128 x 256 tiles, MFMA 32x32x16; each adapter present
 //                          in the tile adds rank/16 MFMA steps of v B_a^T to
@@ -23,79 +23,134 @@ using namespace moe;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kFewRows = 64;      // rows of the first form
+constexpr int kFewRows = 32;      // rows of the first form
 constexpr int kShrinkRows = 16;   // rows of a work-group of the first launch
 constexpr int kMaxSplit = 8;      // parts of the contraction over work-groups (few rows)
+constexpr int kShrinkThreads = 512, kShrinkWaves = kShrinkThreads / 64;
 constexpr int kShrinkStep = 128;  // contraction step of a wave of the first launch
 
 constexpr int round16(int r) { return (r + 15) / 16 * 16; }
 
+// ------------------------------------------------------------- row order
+
+// Rows in windows of kWindow are put in the order of their adapters (stable,
+// no adapter last), so that a tile of the next launches has few of them even
+// where every row is another request.  A work-group ranks 64 rows, four lanes
+// a row: each compares it with a quarter of the window, in LDS.
+constexpr int kWindow = 1024;
+constexpr int kOrderRows = kThreads / 4;
+__global__ __launch_bounds__(kThreads) void order_kernel(const int32_t* __restrict__ ids, int tokens, int adapters,
+                                                         int32_t* __restrict__ order) {
+  __shared__ __attribute__((aligned(16))) uint32_t key[kWindow];
+  const int tid = threadIdx.x, first = uni((int32_t)blockIdx.x) * kOrderRows, row0 = first / kWindow * kWindow;
+  const int count = min(tokens - row0, kWindow), quarter = (count + 15) / 16 * 4;
+  // adapter and place in one number: all different, and the rank a count
+  for (int j = tid; j < 4 * quarter; j += kThreads) {
+    uint32_t v = 0xFFFFFFFFu;  // past the last row
+    if (j < count) v = min((uint32_t)ids[row0 + j], (uint32_t)adapters) * kWindow + j;
+    key[j] = v;
+  }
+  __syncthreads();
+  const int i = first - row0 + (tid >> 2), part = tid & 3;
+  const uint32_t mine = i < count ? key[i] : 0u;
+  uint32_t rank = 0;
+#pragma unroll 8
+  for (int j = part * quarter; j < (part + 1) * quarter; j += 4) {
+    const u32x4 q = *reinterpret_cast<const u32x4*>(key + j);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) rank += q[c] < mine;
+  }
+  rank += dpp_x1(rank);
+  rank += dpp_x2(rank);
+  if (part == 0 && i < count) order[row0 + rank] = row0 + i;
+}
+
 // ---------------------------------------------------------------- A_a x[t]
 
-// blockIdx = (tile of 16 rows, part of the contraction, which of the tile's
-// adapters); v [parts][tokens][rank] fp32, rows without an adapter not written.
-// The four waves take a share of the part each and join in LDS.  A step's
-// loads are in flight together; parts and adapters are work-groups of their
-// own because the chain of steps, not the bytes, is what takes the time.
-template <int NR>
-__global__ __launch_bounds__(kThreads) void shrink_kernel(const uint16_t* __restrict__ x, int tokens, int64_t k,
-                                                          const uint16_t* __restrict__ lora_a, int adapters, int rank,
-                                                          const int32_t* __restrict__ ids, float* __restrict__ v) {
-  __shared__ f32x4 red[4 * NR * 64];
+// blockIdx = (tile of 16 rows in `order`, or as they are if that is NULL, part
+// of the contraction, first of the tile's adapters that it takes).  v [parts][tokens][rank]
+// fp32, or with HALVES (one part) alpha * v as two bf16 halves hi, then lo,
+// [tokens][rank rounded up to 16] each, zeros past the rank.  Rows without an
+// adapter are not written.  The waves take a share of the part each and join
+// in LDS.  A step's loads are in flight together; parts and adapters are
+// work-groups of their own because the chain of steps, not the bytes, is what
+// takes the time.
+template <int NR, bool HALVES>
+__global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const uint16_t* __restrict__ x, int tokens, int64_t k,
+                                                          const uint16_t* __restrict__ lora_a,
+                                                          const float* __restrict__ alpha, int adapters, int rank,
+                                                          const int32_t* __restrict__ ids,
+                                                          const int32_t* __restrict__ order, void* __restrict__ v) {
+  __shared__ f32x4 red[kShrinkWaves * NR * 64];
+  __shared__ int32_t token[kShrinkRows];
   const int lane = threadIdx.x & 63, wave = uni((int32_t)(threadIdx.x >> 6));
   const int row0 = uni((int32_t)blockIdx.x) * kShrinkRows;
-  const int my = lane < kShrinkRows && row0 + lane < tokens ? ids[row0 + lane] : -1;
-  uint64_t left = __ballot((uint32_t)my < (uint32_t)adapters && lane < kShrinkRows), rows = 0;
-  int a = 0;
-  for (int slot = uni((int32_t)blockIdx.z); slot >= 0; --slot) {
-    if (!left) return;  // the tile has fewer adapters
-    a = __builtin_amdgcn_readlane(my, (int)__builtin_ctzll(left));
-    rows = __ballot(my == a) & left;
-    left &= ~rows;
-  }
-  const int parts = uni((int32_t)gridDim.y) * 4, part = uni((int32_t)blockIdx.y) * 4 + wave;
+  const int pos = min(row0 + (lane & 15), tokens - 1), t = order ? order[pos] : pos;  // lanes 16 apart share a row
+  if (threadIdx.x < kShrinkRows) token[threadIdx.x] = t;
+  const int my = lane < kShrinkRows && row0 + lane < tokens ? ids[t] : -1;
+  uint64_t left = __ballot((uint32_t)my < (uint32_t)adapters && lane < kShrinkRows);
+  const int parts = uni((int32_t)gridDim.y) * kShrinkWaves, part = uni((int32_t)blockIdx.y) * kShrinkWaves + wave;
   const int64_t steps = (k + kShrinkStep - 1) / kShrinkStep, share = (steps + parts - 1) / parts;
   const int64_t s0 = min<int64_t>(part * share, steps), s1 = min<int64_t>(s0 + share, steps);
-  const uint16_t* xr = x + (int64_t)min(row0 + (lane & 15), tokens - 1) * k;
-  f32x4 acc[NR];
-  const uint16_t* ar[NR];  // this lane's line of each 16 ranks (a line past the rank reads the last)
+  const uint16_t* xr = x + (int64_t)t * k;
+  for (int slot = 0; left; ++slot) {
+    const int a = __builtin_amdgcn_readlane(my, (int)__builtin_ctzll(left));
+    const uint64_t rows = __ballot(my == a) & left;
+    left &= ~rows;
+    if (slot % (int)gridDim.z != (int)blockIdx.z) continue;
+    f32x4 acc[NR];
+    const uint16_t* ar[NR];  // this lane's line of each 16 ranks (a line past the rank reads the last)
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    acc[r] = f32x4{0, 0, 0, 0};
-    ar[r] = lora_a + ((int64_t)a * rank + min(16 * r + (lane & 15), rank - 1)) * k;
-  }
-  for (int64_t s = s0; s < s1; ++s) {
-    const int64_t e0 = s * kShrinkStep + 32 * (lane >> 4);
-    const bool in = e0 < k;
-    u32x4 xq[4], aq[NR][4];
+    for (int r = 0; r < NR; ++r) {
+      acc[r] = f32x4{0, 0, 0, 0};
+      ar[r] = lora_a + ((int64_t)a * rank + min(16 * r + (lane & 15), rank - 1)) * k;
+    }
+    for (int64_t s = s0; s < s1; ++s) {
+      const int64_t e0 = s * kShrinkStep + 32 * (lane >> 4);
+      const bool in = e0 < k;
+      u32x4 xq[4], aq[NR][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      xq[q] = in ? *reinterpret_cast<const u32x4*>(xr + e0 + 8 * q) : u32x4{0, 0, 0, 0};
+      for (int q = 0; q < 4; ++q) {
+        xq[q] = in ? *reinterpret_cast<const u32x4*>(xr + e0 + 8 * q) : u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int r = 0; r < NR; ++r)
-        aq[r][q] = in ? *reinterpret_cast<const u32x4*>(ar[r] + e0 + 8 * q) : u32x4{0, 0, 0, 0};
+        for (int r = 0; r < NR; ++r)
+          aq[r][q] = in ? *reinterpret_cast<const u32x4*>(ar[r] + e0 + 8 * q) : u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xq[q]),
+                                                           __builtin_bit_cast(bf16x8, aq[r][q]), acc[r], 0, 0, 0);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int r = 0; r < NR; ++r) red[(wave * NR + r) * 64 + lane] = acc[r];
+    __syncthreads();
+    // thread -> (row, rank column); element (row, col) of a tile is component
+    // row % 4 of lane 16 (row / 4) + col
+    const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
+    if (row < kShrinkRows && ((rows >> row) & 1)) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r)
-        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xq[q]),
-                                                         __builtin_bit_cast(bf16x8, aq[r][q]), acc[r], 0, 0, 0);
-  }
+      for (int r = 0; r < NR; ++r) {
+        const float* f = reinterpret_cast<const float*>(red) + (r * 64 + 16 * (row >> 2) + col) * 4 + (row & 3);
+        float sum = f[0];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) red[(wave * NR + r) * 64 + lane] = acc[r];
-  __syncthreads();
-  // thread -> (row, rank column); element (row, col) of a tile is component
-  // row % 4 of lane 16 (row / 4) + col
-  const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
-  if (!((rows >> row) & 1)) return;
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const float* f = reinterpret_cast<const float*>(red) + (r * 64 + 16 * (row >> 2) + col) * 4 + (row & 3);
-    float sum = f[0];
-#pragma unroll
-    for (int w = 1; w < 4; ++w) sum += f[w * NR * 64 * 4];
-    if (16 * r + col < rank) v[((int64_t)blockIdx.y * tokens + row0 + row) * rank + 16 * r + col] = sum;
+        for (int w = 1; w < kShrinkWaves; ++w) sum += f[w * NR * 64 * 4];
+        const int c = 16 * r + col;
+        if (HALVES) {
+          const int r16 = round16(rank);
+          if (c >= r16) break;
+          const float w = c < rank ? sum * alpha[a] : 0.0f;
+          const uint16_t hi = to_bf16(w);
+          uint16_t* o = reinterpret_cast<uint16_t*>(v) + (int64_t)token[row] * r16 + c;
+          o[0] = hi;
+          o[(int64_t)tokens * r16] = to_bf16(w - __uint_as_float((uint32_t)hi << 16));
+        } else if (c < rank) {
+          reinterpret_cast<float*>(v)[((int64_t)blockIdx.y * tokens + token[row]) * rank + c] = sum;
+        }
+      }
+    }
+    if (left) __syncthreads();  // red is written again
   }
 }
 
@@ -130,22 +185,6 @@ __device__ __forceinline__ float row_v(const float* v, int parts, int64_t tokens
   float s = 0.0f;
   for (int p = 0; p < parts; ++p) s += v[(p * tokens + t) * rank + c];
   return s * alpha[a];
-}
-
-// For many rows: alpha * v, the parts summed in their order, as two bf16
-// halves hi and lo [tokens][rank rounded up to 16], zeros past the rank.
-__global__ __launch_bounds__(kThreads) void halves_kernel(const float* __restrict__ v, int parts, int64_t tokens,
-                                                          int rank, const float* __restrict__ alpha, int adapters,
-                                                          const int32_t* __restrict__ ids, uint16_t* __restrict__ out) {
-  const int r16 = round16(rank);
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, t = i / r16, c = i % r16;
-  if (t >= tokens) return;
-  const int a = ids[t];
-  if ((uint32_t)a >= (uint32_t)adapters) return;  // never read
-  const float s = c < rank ? row_v(v, parts, tokens, t, rank, (int)c, a, alpha) : 0.0f;
-  const uint16_t hi = to_bf16(s);
-  out[i] = hi;
-  out[tokens * r16 + i] = to_bf16(s - __uint_as_float((uint32_t)hi << 16));
 }
 
 // ------------------------------------------------------ projection, few rows
@@ -220,10 +259,11 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
     const uint16_t* __restrict__ x, int64_t tokens, int64_t k, const uint8_t* __restrict__ w_data,
     const uint8_t* __restrict__ w_scale, const float* __restrict__ w_amax, int64_t n,
     const uint16_t* __restrict__ lora_b, int adapters, int rank, const int32_t* __restrict__ ids,
-    const uint16_t* __restrict__ v, uint32_t ntm, uint32_t ntn, uint16_t* __restrict__ y, float* __restrict__ partial) {
+    const int32_t* __restrict__ order, const uint16_t* __restrict__ v, uint32_t ntm, uint32_t ntn, uint16_t* __restrict__ y, float* __restrict__ partial) {
   __shared__ __attribute__((aligned(16))) uint8_t lds0[kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds1[kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds2[SPLIT ? kStage : 16];
+  __shared__ int32_t lrow[kBM];  // the tile's rows, counted from base0; past the last: -1
   const int tid = threadIdx.x, wave = uni((int32_t)(tid >> 6)), lane = tid & 63, h = lane >> 5;
   // groups of 8 row tiles sweep the column tiles together, a run of tiles an XCD
   const uint32_t nb = gridDim.x, xcd = blockIdx.x % kNumXcd, q8 = nb / kNumXcd, r8 = nb % kNumXcd;
@@ -232,7 +272,13 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   const int64_t row0 = (int64_t)uni(8 * grp + gin % gm) * kBM, col0 = (int64_t)uni(gin / gm) * kBN;
   const uint32_t rows = (uint32_t)min<int64_t>(tokens - row0, kBM), cols = (uint32_t)min<int64_t>(n - col0, kBN);
   const uint32_t dp = uni((uint32_t)(k / 2)), sp = uni((uint32_t)(k / 16)), xp = uni((uint32_t)(2 * k));
-  const rsrc_t xs = range_rsrc(x + row0 * k, (int64_t)rows * xp);
+  // Rows are addressed from base0: the window's first row if they are in an
+  // order of their own, the tile's first if not.
+  const int64_t base0 = order ? row0 / kWindow * kWindow : row0;
+  const int64_t span = order ? min<int64_t>(tokens - base0, kWindow) : rows;
+  const rsrc_t xs = range_rsrc(x + base0 * k, span * xp);
+  if (tid < kBM) lrow[tid] = (uint32_t)tid < rows ? (order ? (int32_t)(order[row0 + tid] - base0) : tid) : -1;
+  __syncthreads();
   const rsrc_t wd = range_rsrc(w_data + col0 * dp, (int64_t)cols * dp);
   const rsrc_t ws = range_rsrc(w_scale + col0 * sp, (int64_t)cols * sp);
   const uint32_t steps = (uint32_t)((k + kBK - 1) / kBK), share = (steps + gridDim.y - 1) / gridDim.y;
@@ -241,15 +287,20 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   // x: 32 rows a copy, lane g: slot g % 8 of row g / 8 (rows 32 apart have the
   // same granule); codes: 128 lines a copy, lane g: slot g % 2 of line g / 2.
   // In the last step a granule past k is moved out of the buffer's range.
-  const uint32_t xgr = (tid & 7) ^ ((tid >> 3) & 7), xoff = (tid >> 3) * xp + 16 * xgr;
-  const uint32_t woff = (tid >> 1) * dp + 16 * ((tid & 1) ^ ((tid >> 3) & 1));
+  const uint32_t xgr = (tid & 7) ^ ((tid >> 3) & 7), woff = (tid >> 1) * dp + 16 * ((tid & 1) ^ ((tid >> 3) & 1));
   const uint32_t past = (steps - 1) * kBK + 8 * xgr < (uint32_t)k ? 0u : kOutOfRange;
+  uint32_t xoff[kBM / 32];
+#pragma unroll
+  for (int c = 0; c < kBM / 32; ++c) {
+    const int32_t r = lrow[32 * c + (tid >> 3)];
+    xoff[c] = r < 0 ? kOutOfRange : r * xp + 16 * xgr;
+  }
   auto issue = [&](uint32_t ks, uint8_t* base) {
-    const uint32_t off = ks + 1 == steps ? xoff | past : xoff;
+    const uint32_t cut = ks + 1 == steps ? past : 0u;
 #pragma unroll
     for (int c = 0; c < kBM / 32; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xs, (lds_ptr_t)(base + 16 * (c * kThreads + wave * 64)), 16,
-                                               off + 32 * c * xp, ks * (2 * kBK), 0, 0);
+                                               xoff[c] | cut, ks * (2 * kBK), 0, 0);
 #pragma unroll
     for (int c = 0; c < kBN / 128; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(wd, (lds_ptr_t)(base + kXBytes + 16 * (c * kThreads + wave * 64)), 16,
@@ -363,18 +414,20 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   // Rows past the last are out of the output buffer's range, columns past the
   // last are moved out of it.
   if constexpr (SPLIT) {
-    const rsrc_t ps = range_rsrc(partial + ((int64_t)blockIdx.y * tokens + row0) * n + col0,
-                                 ((int64_t)rows - 1) * 2 * yp + 4 * cols);
+    const rsrc_t ps = range_rsrc(partial + ((int64_t)blockIdx.y * tokens + base0) * n + col0,
+                                 (span - 1) * 2 * yp + 4 * cols);
 #pragma unroll
-    for (int in = 0; in < kIN; ++in) {
-      const uint32_t j = jw + in * 32 + (lane & 31), off = j < cols ? 8 * h * yp + 4 * j : kOutOfRange;
+    for (int im = 0; im < kIM; ++im)
 #pragma unroll
-      for (int im = 0; im < kIM; ++im)
+      for (int q = 0; q < 16; ++q) {
+        const int32_t r = lrow[im * 32 + 8 * (q >> 2) + 4 * h + (q & 3)];
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
+        for (int in = 0; in < kIN; ++in) {
+          const uint32_t j = jw + in * 32 + (lane & 31);
           __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[im][in][q] * lf[in]), ps,
-                                                off + (im * 32 + 8 * (q >> 2) + (q & 3)) * 2 * yp, 0, 0);
-    }
+                                                r >= 0 && j < cols ? r * 2 * yp + 4 * j : kOutOfRange, 0, 0);
+        }
+      }
     return;
   }
   // Every adapter that one of 32 rows has adds rank/16 MFMA steps of v B_a^T.
@@ -382,14 +435,14 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   // must not reach them either: each adapter's product is formed apart and
   // added to its own rows alone.  The loads of 32 ranks are in flight together.
   const uint32_t r16 = round16(rank);
-  const rsrc_t vh = range_rsrc(v + row0 * r16, (int64_t)rows * r16 * 2);
-  const rsrc_t vl = range_rsrc(v + (tokens + row0) * r16, (int64_t)rows * r16 * 2);
-  const rsrc_t ys = range_rsrc(y + row0 * n + col0, ((int64_t)rows - 1) * yp + 2 * cols);
+  const rsrc_t vh = range_rsrc(v + base0 * r16, span * r16 * 2);
+  const rsrc_t vl = range_rsrc(v + (tokens + base0) * r16, span * r16 * 2);
+  const rsrc_t ys = range_rsrc(y + base0 * n + col0, (span - 1) * yp + 2 * cols);
   const bool odd = lane & 1;
 #pragma unroll
   for (int im = 0; im < kIM; ++im) {
-    const uint32_t row = im * 32 + (lane & 31);
-    const int my = adapters && row < rows ? ids[row0 + row] : -1;
+    const int32_t row = lrow[im * 32 + (lane & 31)];
+    const int my = adapters && row >= 0 ? ids[base0 + row] : -1;
     uint32_t left = (uint32_t)__ballot((uint32_t)my < (uint32_t)adapters);  // lanes 32-63 repeat lanes 0-31
     f32x16 sum[kIN];
 #pragma unroll
@@ -435,12 +488,13 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
 #pragma unroll
     for (int in = 0; in < kIN; ++in) {
       const uint32_t jp = (jw + in * 32 + (lane & 31)) & ~1u;
-      const uint32_t off = jp < cols ? (im * 32 + 4 * h + odd) * yp + 2 * jp : kOutOfRange;
 #pragma unroll
       for (int q = 0; q < 16; q += 2) {
+        const int32_t r = lrow[im * 32 + 8 * (q >> 2) + 4 * h + (q & 3) + odd];
         float lo, hi;
         pair_columns(acc[im][in][q] * lf[in] + sum[in][q], acc[im][in][q + 1] * lf[in] + sum[in][q + 1], odd, &lo, &hi);
-        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(lo, hi), ys, off + (8 * (q >> 2) + (q & 3)) * yp, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(lo, hi), ys, r >= 0 && jp < cols ? r * yp + 2 * jp : kOutOfRange,
+                                              0, 0);
       }
     }
   }
@@ -483,14 +537,10 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(const float* __restric
 int shrink_parts(int64_t tokens, int64_t k) {
   const int64_t tiles = (tokens + kShrinkRows - 1) / kShrinkRows, steps = (k + kShrinkStep - 1) / kShrinkStep;
   const int64_t want = (4 * kCus + tiles - 1) / tiles;
-  return (int)std::max<int64_t>(1, std::min(std::min(want, (steps + 3) / 4), (int64_t)kMaxSplit));
+  return (int)std::max<int64_t>(1, std::min(std::min(want, (steps + kShrinkWaves - 1) / kShrinkWaves), (int64_t)kMaxSplit));
 }
 
 constexpr int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
-// Workspace: the parts of v; for many rows its halves; the parts of the projection.
-int64_t v_bytes(int64_t tokens, int64_t k, int32_t rank) { return round256(tokens * rank * 4 * shrink_parts(tokens, k)); }
-int64_t half_bytes(int64_t tokens, int32_t rank) { return tokens <= kFewRows ? 0 : round256(tokens * round16(rank) * 4); }
-
 // Parts of the contraction of many rows: as many as give every CU two
 // work-groups where the tiles alone do not give it one, at least 8 steps each,
 // and their sums within kMaxWorkspace.
@@ -500,6 +550,25 @@ int project_parts(int64_t tokens, int64_t k, int64_t n) {
   if (tokens <= kFewRows || tiles >= kCus) return 1;
   const int64_t by_steps = (k + kBK - 1) / kBK / 8, by_room = kMaxWorkspace / (tokens * n * 4);
   return (int)std::max<int64_t>(1, std::min(std::min(2 * kCus / tiles, by_steps), by_room));
+}
+
+// Whether the rows are put in order first: worth a launch where tiles meet the
+// adapters (not in parts, where the last launch adds them row by row) and there
+// are several; a window's rows have to be within 31-bit offsets.
+bool ordered(int64_t tokens, int64_t k, int64_t n, int adapters) {
+  return tokens > kFewRows && project_parts(tokens, k, n) == 1 && adapters > 1 &&
+         adapters < (1 << 21) && kWindow * std::max(2 * k, 2 * n) <= INT32_MAX;
+}
+
+// Workspace: v (its parts, or its halves and the order), the projection's parts.
+struct Workspace {
+  int64_t v, order, partial;
+};
+Workspace workspace_of(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
+  const int parts = project_parts(tokens, k, n);
+  const bool halves = tokens > kFewRows && parts == 1;
+  return {round256(halves ? tokens * round16(rank) * 4 : tokens * rank * 4 * shrink_parts(tokens, k)),
+          halves && rank ? round256(tokens * 4) : 0, parts > 1 ? parts * tokens * n * 4 : 0};
 }
 
 template <class F>
@@ -529,8 +598,8 @@ extern "C" {
 
 int64_t lora_workspace(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
   if (tokens <= 0 || k <= 0 || n <= 0 || rank < 0) return 0;
-  const int parts = project_parts(tokens, k, n);
-  return v_bytes(tokens, k, rank) + half_bytes(tokens, rank) + (parts > 1 ? parts * tokens * n * 4 : 0);
+  const Workspace w = workspace_of(tokens, k, n, rank);
+  return w.v + w.order + w.partial;
 }
 
 int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_data, const uint8_t* w_scale,
@@ -550,39 +619,46 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
   const int64_t need = lora_workspace(tokens, k, n, num_adapters ? rank : 0);
   if (need && (!workspace || workspace_bytes < need)) return NVFP4G_EINVAL;
   const hipStream_t st = (hipStream_t)stream;
-  const int T = (int)tokens, parts = shrink_parts(tokens, k), r = num_adapters ? rank : 0;
-  const bool few = tokens <= kFewRows;
-  const int split = project_parts(tokens, k, n);
-  float* v = (float*)workspace;
-  uint16_t* halves = (uint16_t*)((char*)workspace + v_bytes(tokens, k, r));
-  float* partial = (float*)((char*)halves + half_bytes(tokens, r));
   if (((tokens + kBM - 1) / kBM) * ((n + kBN - 1) / kBN) > (int64_t)INT32_MAX) return NVFP4G_EINVAL;
+  const int T = (int)tokens, r = num_adapters ? rank : 0, split = project_parts(tokens, k, n);
+  const bool few = tokens <= kFewRows, halves = !few && split == 1;
+  const int parts = halves ? 1 : shrink_parts(tokens, k);
+  const Workspace w = workspace_of(tokens, k, n, r);
+  float* v = (float*)workspace;
+  int32_t* order = ordered(tokens, k, n, num_adapters) ? (int32_t*)((char*)workspace + w.v) : nullptr;
+  float* partial = (float*)((char*)workspace + w.v + w.order);
   if (num_adapters) {
-    const dim3 grid((uint32_t)((T + kShrinkRows - 1) / kShrinkRows), parts, std::min(std::min(T, kShrinkRows), num_adapters));
+    if (order)
+      hipLaunchKernelGGL(order_kernel, dim3((uint32_t)((tokens + kOrderRows - 1) / kOrderRows)), dim3(kThreads), 0, st,
+                         adapter_ids, T, num_adapters, order);
+    // adapters of a tile side by side: two where the rows are in order
+    const dim3 grid((uint32_t)((T + kShrinkRows - 1) / kShrinkRows), parts,
+                    std::min(order ? 2 : std::min(T, kShrinkRows), num_adapters));
     with_ranks(rank, [&](auto nr) {
-      hipLaunchKernelGGL((shrink_kernel<decltype(nr)::value>), grid, dim3(kThreads), 0, st, x, T, k, lora_a,
-                         num_adapters, rank, adapter_ids, v);
+      constexpr int NR = decltype(nr)::value;
+      if (halves)
+        hipLaunchKernelGGL((shrink_kernel<NR, true>), grid, dim3(kShrinkThreads), 0, st, x, T, k, lora_a, alpha, num_adapters,
+                           rank, adapter_ids, order, v);
+      else
+        hipLaunchKernelGGL((shrink_kernel<NR, false>), grid, dim3(kShrinkThreads), 0, st, x, T, k, lora_a, alpha,
+                           num_adapters, rank, adapter_ids, order, v);
     });
-    if (split == 1 && !few)
-      hipLaunchKernelGGL(halves_kernel, dim3((uint32_t)((tokens * round16(rank) + kThreads - 1) / kThreads)),
-                         dim3(kThreads), 0, st, v, parts, tokens, rank, alpha, num_adapters, adapter_ids, halves);
   }
   if (few) {
     // one 16-line tile a work-group: the most work-groups a projection gives
     if (T <= 16) launch_few<1, 1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
-    else if (T <= 32) launch_few<2, 1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
-    else launch_few<4, 1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
+    else launch_few<2, 1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
   } else {
     const uint32_t ntm = (uint32_t)((tokens + kBM - 1) / kBM), ntn = (uint32_t)((n + kBN - 1) / kBN);
     if (split > 1) {
       hipLaunchKernelGGL((many_rows_kernel<true>), dim3(ntm * ntn, split), dim3(kThreads), 0, st, x, tokens, k, w_data,
-                         w_scale, w_amax, n, lora_b, num_adapters, r, adapter_ids, halves, ntm, ntn, y, partial);
+                         w_scale, w_amax, n, lora_b, num_adapters, r, adapter_ids, order, (const uint16_t*)v, ntm, ntn, y, partial);
       hipLaunchKernelGGL(finish_kernel, dim3((uint32_t)tokens, (uint32_t)((n + 8 * kThreads - 1) / (8 * kThreads))),
                          dim3(kThreads), 0, st, partial, split, tokens, n, lora_b, alpha, num_adapters, r, adapter_ids,
                          v, parts, y);
     } else {
       hipLaunchKernelGGL((many_rows_kernel<false>), dim3(ntm * ntn), dim3(kThreads), 0, st, x, tokens, k, w_data,
-                         w_scale, w_amax, n, lora_b, num_adapters, r, adapter_ids, halves, ntm, ntn, y, partial);
+                         w_scale, w_amax, n, lora_b, num_adapters, r, adapter_ids, order, (const uint16_t*)v, ntm, ntn, y, partial);
     }
   }
   return hip_status();
