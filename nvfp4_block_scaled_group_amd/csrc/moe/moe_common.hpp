@@ -37,14 +37,6 @@ __device__ __forceinline__ uint32_t wave_reduce(uint32_t v, Op op) {
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return op(b[0], b[1]);
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  return wave_reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
-}
-__device__ __forceinline__ float wave_fmax(float v) {
-  return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  }));
-}
 __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));

@@ -2,12 +2,15 @@
 // plan of the packed 128-row groups, behind the C ABI of include/moe_ops.h.
 //
 // Selection.  A token's choice is the topk largest keys  l + bias, ties to the
-// lower index; its weights are softmax or sigmoid scores of the logits.  One
-// wave holds one token: lane i holds VPL consecutive experts (i*VPL ..), so
-// among equal keys the lowest lane, and in it the lowest element, is the
-// lowest index.  Keys are compared as order-preserving integers (0 = masked).
-// topk rounds: each lane keeps its own best, a 6-step wave maximum finds the
-// key, a ballot the lane, and that lane drops the element.
+// lower index; its weights are softmax or sigmoid scores of the logits.  It is
+// bound by instructions, not by the read of the logits, so the lanes of a wave
+// share several tokens: LANES lanes hold VPL consecutive experts each.  A key
+// and its index become one 64-bit pattern, unique and ordered, that is also an
+// ordered finite double, so that one maximum or minimum instruction compares
+// both.  Each lane sorts its patterns once; then topk rounds take the maximum
+// of the lanes' heads (log2 LANES exchanges) and the lane that had it drops its
+// head.  32768 x 256, 8 chosen: 28 us with one token a wave and the keys
+// searched every round.
 //
 // Plan.  A stable counting sort of the pairs by expert without atomics that
 // decide an order: a wave ranks 64 pairs at a time by matching expert
@@ -39,112 +42,175 @@ __device__ __forceinline__ float logit_at<uint16_t>(const uint16_t* p, int64_t i
   return __uint_as_float((uint32_t)p[i] << 16);
 }
 
-// The VPL logits of this lane (experts lane*VPL ..), -inf past E.  With
-// `wide` (E a multiple of VPL and the row aligned to the lane's piece) as
-// vector loads.
+// VPL consecutive values of a row of E (experts lane*VPL ..) as fp32, whatever
+// is there past E.  With `wide` (E a multiple of VPL and the row aligned to the
+// lane's piece) as vector loads.  A lane or an element past E reads one inside
+// the row: no branch holds the other loads up.
 template <class T, int VPL>
-__device__ __forceinline__ void load_logits(const T* row, int E, int lane, bool wide, float (&l)[VPL]) {
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, bool wide, float (&v)[VPL]) {
   const int e0 = lane * VPL;
   constexpr int kPer = 16 / (int)sizeof(T) < VPL ? 16 / (int)sizeof(T) : VPL;  // elements of one load
   if (wide) {
+    const T* p = row + (e0 < E ? e0 : 0);
 #pragma unroll
     for (int i = 0; i < VPL; i += kPer) {
       typedef T vec_t __attribute__((ext_vector_type(kPer)));
-      if (e0 < E) {
-        const vec_t v = *reinterpret_cast<const vec_t*>(row + e0 + i);
+      const vec_t q = *reinterpret_cast<const vec_t*>(p + i);
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          const T t = v[q];
-          l[i + q] = clean(logit_at<T>(&t, 0));
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < kPer; ++q) l[i + q] = kNegInf;
+      for (int c = 0; c < kPer; ++c) {
+        const T x = q[c];
+        v[i + c] = logit_at<T>(&x, 0);
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) l[i] = e0 + i < E ? clean(logit_at<T>(row, e0 + i)) : kNegInf;
+    for (int i = 0; i < VPL; ++i) v[i] = logit_at<T>(row, min(e0 + i, E - 1));
   }
 }
+template <class T, int VPL>
+__device__ __forceinline__ void load_logits(const T* row, int E, int lane, bool wide, float (&l)[VPL]) {
+  load_row<T, VPL>(row, E, lane, wide, l);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) l[i] = lane * VPL + i < E ? clean(l[i]) : kNegInf;
+}
 
-// Scores of the chosen logits, one choice a lane (lanes 0 .. topk-1; z = -inf
-// elsewhere and for no choice): the unscaled weight.  top and sum are the
+// Value of lane ^ (the step's distance) inside a group of lanes: 1, 2, then
+// the mirror of 8 and the rotation of 16, which serve reductions as well.
+template <int STEP>
+__device__ __forceinline__ uint32_t exchange(uint32_t v) {
+  if constexpr (STEP == 0) return dpp_x1(v);
+  else if constexpr (STEP == 1) return dpp_x2(v);
+  else if constexpr (STEP == 2) return dpp_hmirror(v);
+  else if constexpr (STEP == 3) return swap8(v);
+  else {
+    // the swap gives own and other half; which is which depends on the lane
+    const auto r = STEP == 4 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                             : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const bool upper = (threadIdx.x >> STEP) & 1;
+    return upper ? r[0] : r[1];
+  }
+}
+template <int LANES, int STEP = 0>
+__device__ __forceinline__ double group_max(double v) {
+  if constexpr ((1 << STEP) >= LANES) {
+    return v;
+  } else {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t o = (uint64_t)exchange<STEP>((uint32_t)(b >> 32)) << 32 | exchange<STEP>((uint32_t)b);
+    return group_max<LANES, STEP + 1>(__builtin_fmax(v, __builtin_bit_cast(double, o)));
+  }
+}
+template <int LANES, int STEP = 0>
+__device__ __forceinline__ float group_fmax(float v) {
+  if constexpr ((1 << STEP) >= LANES) return v;
+  else return group_fmax<LANES, STEP + 1>(fmaxf(v, __uint_as_float(exchange<STEP>(__float_as_uint(v)))));
+}
+template <int LANES, int STEP = 0>
+__device__ __forceinline__ float group_sum(float v) {
+  if constexpr ((1 << STEP) >= LANES) return v;
+  else return group_sum<LANES, STEP + 1>(v + __uint_as_float(exchange<STEP>(__float_as_uint(v))));
+}
+
+// By value: a conditional on two array elements selects an address, and the
+// array leaves its registers.
+__device__ __forceinline__ double pick(bool c, double a, double b) { return c ? a : b; }
+
+// Key bits above the complemented index: the two top bits are 0, so the
+// pattern is a finite double and its order is that of the pair.
+__device__ __forceinline__ double key_pattern(uint32_t key, uint32_t index) {
+  return __builtin_bit_cast(double, (uint64_t)key << 30 | (uint64_t)(MOE_MAX_EXPERTS - 1 - index));
+}
+
+// Odd-even merge sort, descending.
+template <int N>
+__device__ __forceinline__ void sort_desc(double (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const double a = v[i + j], b = v[i + j + q];
+            v[i + j] = __builtin_fmax(a, b);
+            v[i + j + q] = __builtin_fmin(a, b);
+          }
+}
+
+// Scores of the chosen logits, slot j of a token in lane j of its group (z =
+// -inf elsewhere and for no choice): the unscaled weight.  top and sum are the
 // softmax's maximum and sum over all unmasked experts (used without normalize).
-__device__ __forceinline__ float choice_score(float z, int score, int normalize, float top, float sum) {
+template <int LANES>
+__device__ __forceinline__ float group_score(float z, int score, int normalize, float top, float sum) {
   const bool on = z > kNegInf;
   float s;
   if (score == MOE_SCORE_SIGMOID) {
     s = on ? 1.0f / (1.0f + expf(-z)) : 0.0f;
   } else if (normalize) {
-    const float m = wave_fmax(z);
+    const float m = group_fmax<LANES>(z);
     s = on ? expf(z - m) : 0.0f;
   } else {
     s = on ? expf(z - top) / sum : 0.0f;
   }
   if (normalize) {
-    const float tot = wave_sum(s);
+    const float tot = group_sum<LANES>(s);
     s = tot > 0.0f ? s / tot : 0.0f;
   }
   return s;
 }
 
-template <class T, int VPL>
+// KMAX: the sorted patterns a lane keeps, topk at least.
+template <class T, int LANES, int VPL, int KMAX>
 __global__ __launch_bounds__(kThreads) void route_kernel(const T* __restrict__ logits, int64_t tokens, int E, int topk,
                                                          const float* __restrict__ bias, int score, int normalize,
-                                                         float scale, bool wide, int32_t* __restrict__ ids,
-                                                         float* __restrict__ weights) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-  if (t >= tokens) return;
+                                                         float scale, bool wide, bool wide_bias,
+                                                         int32_t* __restrict__ ids, float* __restrict__ weights) {
+  const int li = threadIdx.x & (LANES - 1);
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const bool live = t < tokens;  // the others work on the last token and write nothing: exchanges need all lanes
+  const T* row = logits + (live ? t : tokens - 1) * E;
   float l[VPL];
-  load_logits<T, VPL>(logits + t * E, E, lane, wide, l);
+  load_logits<T, VPL>(row, E, li, wide, l);
   float top = 0.0f, sum = 1.0f;
   if (score == MOE_SCORE_SOFTMAX && !normalize) {
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-    top = fmaxf(wave_fmax(m), -FLT_MAX);
+    top = fmaxf(group_fmax<LANES>(m), -FLT_MAX);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) s += expf(l[i] - top);
-    sum = wave_sum(s);
+    sum = group_sum<LANES>(s);
   }
-  uint32_t key[VPL];
+  if (bias) {  // a masked logit stays -inf: the bias is finite
+    float b[VPL];
+    load_row<float, VPL>(bias, E, li, wide_bias, b);
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    key[i] = key_bits(bias && e < E ? l[i] + bias[e] : l[i]);
+    for (int i = 0; i < VPL; ++i) l[i] = l[i] > kNegInf ? l[i] + b[i] : kNegInf;
   }
+  double key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) key[i] = key_pattern(key_bits(l[i]), li * VPL + i);
+  sort_desc(key);
+  constexpr int kKeep = KMAX < VPL ? KMAX : VPL;
   int my_id = -1;
-  float my_z = kNegInf;
   for (int j = 0; j < topk; ++j) {
-    uint32_t best = key[0];
-    int at = 0;
-    float z = l[0];
+    const double w = group_max<LANES>(key[0]);
+    const uint64_t b = __builtin_bit_cast(uint64_t, w);
+    const int id = (uint32_t)(b >> 30) ? MOE_MAX_EXPERTS - 1 - (int)(b & (MOE_MAX_EXPERTS - 1)) : -1;  // key 0: masked
+    if (li == j) my_id = id;
+    const bool mine = key[0] == w;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) {
-      const bool g = key[i] > best;
-      best = g ? key[i] : best;
-      at = g ? i : at;
-      z = g ? l[i] : z;
-    }
-    const uint32_t w = wave_max(best);
-    if (uni(w) == 0) break;  // nothing unmasked is left
-    const int win = uni((int32_t)__builtin_ctzll(__ballot(best == w)));
-    const int id = __builtin_amdgcn_readlane(lane * VPL + at, win);
-    const float wz = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(z), win));
-    if (lane == j) {
-      my_id = id;
-      my_z = wz;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = lane * VPL + i == id ? 0u : key[i];
+    for (int i = 0; i + 1 < kKeep; ++i) key[i] = pick(mine, key[i + 1], key[i]);
+    if (mine) key[kKeep - 1] = 0.0;
   }
-  const float s = choice_score(my_z, score, normalize, top, sum);
-  if (lane < topk) {
-    ids[t * topk + lane] = my_id;
-    weights[t * topk + lane] = my_id >= 0 ? s * scale : 0.0f;
+  const float z = my_id >= 0 ? clean(logit_at<T>(row, my_id)) : kNegInf;
+  const float s = group_score<LANES>(z, score, normalize, top, sum);
+  if (live && li < topk) {
+    ids[t * topk + li] = my_id;
+    weights[t * topk + li] = my_id >= 0 ? s * scale : 0.0f;
   }
 }
 
@@ -183,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(const T* __restrict
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-    top = fmaxf(wave_fmax(m), -FLT_MAX);
+    top = fmaxf(group_fmax<64>(m), -FLT_MAX);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -193,7 +259,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(const T* __restrict
     sum = wave_sum(s);
   }
   const bool on = z > kNegInf;  // a masked logit that was named as a choice has no gradient
-  const float q = choice_score(z, score, normalize, top, sum);
+  const float q = group_score<64>(z, score, normalize, top, sum);
   if (!on) g = 0.0f;
   const float inner = wave_sum(q * g);
   float d;
@@ -240,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(const T* __restrict
 
 // ------------------------------------------------------------------- plan
 
-constexpr int kPlanPairs = 512;       // pairs one wave ranks in the split form
+constexpr int kPlanPairs = 256;       // pairs one wave ranks in the split form
 constexpr int kSmallPairs = 4096;     // the one-launch form: pairs, experts
 constexpr int kSmallExperts = 512;
 constexpr int kSmallThreads = 1024;
@@ -304,22 +370,17 @@ __device__ int group_begins(const int32_t* cnt, int E, int32_t* begin, int32_t* 
   return total;
 }
 
-// src of the rows [r0, r1): -1 for those no pair has (padding rows of a group
-// and rows past the last group).
-__device__ __forceinline__ void fill_padding(int64_t r0, int64_t r1, int E, int total, const int32_t* begin,
+// src of the rows no pair has: the padding of the groups of experts `part`,
+// `part` + `parts`, .., a wave each, and a share of the rows past the last
+// group.
+__device__ __forceinline__ void fill_padding(int part, int parts, int64_t cap, int E, int total, const int32_t* begin,
                                              const int32_t* cnt, int32_t* src) {
-  for (int64_t r = r0 + threadIdx.x; r < r1; r += blockDim.x) {
-    bool pad = r >= total;
-    if (!pad) {  // the last expert whose group begins at or before r and is not empty before it
-      int lo = 0, hi = E - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (begin[mid] <= r) lo = mid; else hi = mid - 1;
-      }
-      pad = r - begin[lo] >= cnt[lo];
-    }
-    if (pad) src[r] = -1;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  for (int e = part * waves + wave; e < E; e += parts * waves) {
+    const int64_t end = min<int64_t>(begin[e] + (cnt[e] + kTileRows - 1) / kTileRows * kTileRows, cap);
+    for (int64_t r = begin[e] + cnt[e] + lane; r < end; r += 64) src[r] = -1;
   }
+  for (int64_t r = total + (int64_t)part * blockDim.x + threadIdx.x; r < cap; r += (int64_t)parts * blockDim.x) src[r] = -1;
 }
 
 __device__ __forceinline__ void write_ends(int E, const int32_t* begin, const int32_t* cnt, int64_t cap, int total,
@@ -373,7 +434,7 @@ __global__ __launch_bounds__(kSmallThreads) void plan_small_kernel(const int32_t
     const int r = wave_rank(e, ebits, hist + wave * E);
     if (p + lane < p1) write_pair(p + lane, e >= 0 ? begin[e] + r : -1, cap, rows, src);
   }
-  fill_padding(0, cap, E, total, begin, cnt, src);
+  fill_padding(0, 1, cap, E, total, begin, cnt, src);
   write_ends(E, begin, cnt, cap, total, offs, counts, status);
 }
 
@@ -396,25 +457,29 @@ __global__ __launch_bounds__(kThreads) void plan_count_kernel(const int32_t* __r
 }
 
 // Step 2: per expert the exclusive prefix over the chunks (in place) and the
-// count, which goes to the row after the last chunk.  A work-group takes 64
-// experts; its 16 waves take a run of chunks each.
+// count, which goes to the row after the last chunk.  A work-group takes 16
+// experts; 64 groups of 16 lanes take a run of chunks each.
+constexpr int kScanExperts = 16;
 __global__ __launch_bounds__(kSmallThreads) void plan_scan_kernel(int32_t* __restrict__ ws, int64_t chunks, int E) {
-  __shared__ int32_t part[kSmallWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = blockIdx.x * 64 + lane;
-  const int64_t per = (chunks + kSmallWaves - 1) / kSmallWaves;
-  const int64_t c0 = min(wave * per, chunks), c1 = min(c0 + per, chunks);
+  constexpr int kRuns = kSmallThreads / kScanExperts;
+  __shared__ int32_t part[kRuns][kScanExperts];
+  const int le = threadIdx.x % kScanExperts, run = threadIdx.x / kScanExperts;
+  const int e = blockIdx.x * kScanExperts + le;
+  const int64_t per = (chunks + kRuns - 1) / kRuns;
+  const int64_t c0 = min(run * per, chunks), c1 = min(c0 + per, chunks);
   int acc = 0;
   if (e < E) {
 #pragma unroll 8
     for (int64_t c = c0; c < c1; ++c) acc += ws[c * E + e];
   }
-  part[wave][lane] = acc;
+  part[run][le] = acc;
   __syncthreads();
   int at = 0, total = 0;
-  for (int w = 0; w < kSmallWaves; ++w) {
-    if (w < wave) at += part[w][lane];
-    total += part[w][lane];
+#pragma unroll 16
+  for (int r = 0; r < kRuns; ++r) {
+    const int v = part[r][le];
+    at += r < run ? v : 0;
+    total += v;
   }
   if (e < E) {
 #pragma unroll 8
@@ -423,7 +488,7 @@ __global__ __launch_bounds__(kSmallThreads) void plan_scan_kernel(int32_t* __res
       ws[c * E + e] = at;
       at += v;
     }
-    if (wave == 0) ws[chunks * E + e] = total;
+    if (run == 0) ws[chunks * E + e] = total;
   }
 }
 
@@ -451,8 +516,7 @@ __global__ __launch_bounds__(kThreads) void plan_write_kernel(const int32_t* __r
     const int r = wave_rank(e, ebits, base + wave * E);
     if (p + lane < p1) write_pair(p + lane, e >= 0 ? begin[e] + r : -1, cap, rows, src);
   }
-  const int64_t per = (cap + gridDim.x - 1) / gridDim.x;
-  fill_padding(blockIdx.x * per, min((blockIdx.x + 1) * per, cap), E, total, begin, cnt, src);
+  fill_padding(blockIdx.x, gridDim.x, cap, E, total, begin, cnt, src);
   if (blockIdx.x == 0) write_ends(E, begin, cnt, cap, total, offs, counts, status);
 }
 
@@ -490,6 +554,42 @@ bool wide_rows(const void* p, int E, int vpl, int size) {
   return E % vpl == 0 && (int64_t)E * size % piece == 0 && aligned(p, piece);
 }
 
+struct RouteCall {
+  const void* logits;
+  int64_t tokens;
+  int32_t E, topk;
+  const float* bias;
+  int32_t score, normalize;
+  float scale;
+  int32_t* ids;
+  float* weights;
+  hipStream_t stream;
+};
+
+template <class T, int LANES, int VPL, int KMAX>
+int launch_route(const RouteCall& c) {
+  const dim3 grid((uint32_t)((c.tokens + kThreads / LANES - 1) / (kThreads / LANES)));
+  hipLaunchKernelGGL((route_kernel<T, LANES, VPL, KMAX>), grid, dim3(kThreads), 0, c.stream, (const T*)c.logits,
+                     c.tokens, c.E, c.topk, c.bias, c.score, c.normalize, c.scale,
+                     wide_rows(c.logits, c.E, VPL, sizeof(T)), wide_rows(c.bias, c.E, VPL, 4), c.ids, c.weights);
+  return hip_status();
+}
+
+// As few lanes as hold the experts, 8 or 16 each, and the choices, one each.
+template <class T>
+int route(const RouteCall& c) {
+  if (c.topk <= 8) {
+    if (c.E <= 64) return launch_route<T, 8, 8, 8>(c);
+    if (c.E <= 128) return launch_route<T, 8, 16, 8>(c);
+    if (c.E <= 256) return launch_route<T, 16, 16, 8>(c);
+    if (c.E <= 512) return launch_route<T, 32, 16, 8>(c);
+    if (c.E <= 1024) return launch_route<T, 64, 16, 8>(c);
+  }
+  if (c.E <= 256) return launch_route<T, 16, 16, 16>(c);
+  if (c.E <= 1024) return launch_route<T, 64, 16, 16>(c);
+  return launch_route<T, 64, 64, 16>(c);
+}
+
 }  // namespace
 
 extern "C" {
@@ -504,19 +604,8 @@ int moe_route(const void* logits, int32_t logits_type, int64_t tokens, int32_t n
   if (!aligned(logits, logits_type == MOE_F32 ? 4 : 2) || !aligned(select_bias, 4) || !aligned(ids, 4) ||
       !aligned(weights, 4))
     return NVFP4G_EALIGN;
-  const dim3 grid((uint32_t)((tokens + 3) / 4));
-  with_vpl(num_experts, [&](auto v) {
-    constexpr int VPL = decltype(v)::value;
-    if (logits_type == MOE_F32)
-      hipLaunchKernelGGL((route_kernel<float, VPL>), grid, dim3(kThreads), 0, (hipStream_t)stream,
-                         (const float*)logits, tokens, num_experts, topk, select_bias, score, normalize, scale,
-                         wide_rows(logits, num_experts, VPL, 4), ids, weights);
-    else
-      hipLaunchKernelGGL((route_kernel<uint16_t, VPL>), grid, dim3(kThreads), 0, (hipStream_t)stream,
-                         (const uint16_t*)logits, tokens, num_experts, topk, select_bias, score, normalize, scale,
-                         wide_rows(logits, num_experts, VPL, 2), ids, weights);
-  });
-  return hip_status();
+  const RouteCall c{logits, tokens, num_experts, topk, select_bias, score, normalize, scale, ids, weights, (hipStream_t)stream};
+  return logits_type == MOE_F32 ? route<float>(c) : route<uint16_t>(c);
 }
 
 int moe_route_bwd(const void* logits, int32_t logits_type, int64_t tokens, int32_t num_experts, int32_t topk,
@@ -576,7 +665,8 @@ int moe_plan(const int32_t* ids, int64_t pairs, int32_t num_experts, int64_t m_c
   const int threads = plan_threads(E), waves = threads / 64;
   const dim3 grid((uint32_t)((chunks + waves - 1) / waves));
   hipLaunchKernelGGL(plan_count_kernel, grid, dim3(threads), waves * E * 4, st, ids, pairs, E, ws, chunks);
-  hipLaunchKernelGGL(plan_scan_kernel, dim3((E + 63) / 64), dim3(kSmallThreads), 0, st, ws, chunks, E);
+  hipLaunchKernelGGL(plan_scan_kernel, dim3((E + kScanExperts - 1) / kScanExperts), dim3(kSmallThreads), 0, st, ws,
+                     chunks, E);
   hipLaunchKernelGGL(plan_write_kernel, grid, dim3(threads), ((waves + 2) * E + waves) * 4, st, ids, pairs, E, ebits,
                      m_capacity, ws, chunks, offs, counts, rows, src, d_status);
   return hip_status();
