@@ -72,18 +72,21 @@ def load_library() -> ctypes.CDLL:
     return L
 
 
-def _device_index() -> int:
-    return torch.cuda.current_device()
+# the current device's index without the Python layers of torch.cuda (these
+# calls sit in decoding loops; a CUDA tensor has initialised the runtime)
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream):
+    if stream is None and _b._raw_current_stream is not None:
+        return _b._raw_current_stream(_device_index())
     return _b._stream(stream)
 
 
 def _buf(name, t, dtypes, numel, required=False):
     """Address of a caller buffer that passes the binding's checks.  The usual
-    case is settled in one expression (these calls sit in decoding loops);
-    anything else goes through binding._buf, which names what is wrong."""
+    case is settled in one expression; anything else goes through
+    binding._buf, which names what is wrong."""
     if (type(t) is torch.Tensor and t.dtype in dtypes and t.numel() >= numel and t.is_contiguous()
             and t.get_device() == _device_index()):
         return t.data_ptr()
@@ -102,7 +105,7 @@ def _dims(name: str, t, dim: int):
 
 def _shape(name: str, t, want):
     """A tensor argument whose whole shape is fixed by the others."""
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(want):
+    if not isinstance(t, torch.Tensor) or t.shape != want:
         got = tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name} must be a tensor of shape {tuple(want)}, got {got}")
 
