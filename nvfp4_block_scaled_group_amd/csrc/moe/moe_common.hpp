@@ -13,6 +13,8 @@ namespace moe {
 
 using namespace nvfp4g;
 
+constexpr int kCus = 256;  // compute units of the device
+
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));

@@ -31,9 +31,8 @@ typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kWavesN = 2;
-constexpr int kWM = 2, kWN = 4;   // 32 x 32 MFMA tiles of a wave (rows, lines)
+constexpr int kWM = 2;            // 32 x 32 MFMA tiles of a wave along the rows; NW along the lines
 constexpr int kBM = 128;          // rows of a work-group: the expert granule
-constexpr int kBN = 256;          // weight lines of a work-group
 constexpr int kBK = 128;          // contraction step
 constexpr int kGroupRows = 8;     // row tiles that sweep the column tiles together
 
@@ -48,9 +47,15 @@ struct Lines {
 // arrays, so that reads of one need not wait for copies into the other);
 // scales of four steps at a time, 32 bytes a line, double-buffered.
 constexpr uint32_t kRowBytes = kBK / 2, kRowScales = kBK / 16;
-constexpr uint32_t kStB = kBM * kRowBytes, kStageBytes = kStB + kBN * kRowBytes;  // 24 KB
+constexpr uint32_t kStB = kBM * kRowBytes;
 constexpr uint32_t kScSteps = 4, kScLine = kScSteps * kRowScales;
-constexpr uint32_t kScB = kBM * kScLine, kScBlockBytes = kScB + kBN * kScLine;    // 12 KB
+constexpr uint32_t kScB = kBM * kScLine;
+template <int NW>
+struct Tile {
+  static constexpr int kLines = 2 * 32 * NW;                                    // weight lines of a work-group
+  static constexpr uint32_t kStageBytes = kStB + kLines * kRowBytes;            // 24 KB (NW 4), 16 KB (NW 2)
+  static constexpr uint32_t kScBlockBytes = kScB + kLines * kScLine;            // 12 KB, 8 KB
+};
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
@@ -81,27 +86,30 @@ __device__ __forceinline__ rsrc_t lines_rsrc(const uint8_t* p, uint32_t bytes) {
 }
 
 // acc[im][in] += A lines x B lines^T over the contraction length L (a multiple
-// of kBK).  PAIR: B's 256 LDS lines are four blocks of 64: lines 0-63 of B0
-// (gate), 0-63 of B1 (up), 64-127 of B0, 64-127 of B1; otherwise 256 lines of
-// B0.  Each step waits for its own copies, passes one barrier, issues the
+// of kBK).  PAIR: B's LDS lines are four blocks of 16 NW: the first of B0
+// (gate), the first of B1 (up), the second of B0, the second of B1; otherwise
+// 64 NW lines of B0.  Each step waits for its own copies, passes one barrier, issues the
 // copies of the next step into the other stage and multiplies meanwhile.
 // Contraction order: word 8h + s of a line's 64-byte chunk feeds sub-step s of
 // lane half h, in A and B alike, so a lane reads its eight sub-steps' words
 // with two 16-byte LDS reads.
 // A wave whose columns all lie past the last one (`live` false) copies and
 // waits with the others but multiplies nothing.
-template <bool PAIR>
+template <bool PAIR, int NW>
 __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const Lines& B1, uint32_t L, bool live,
-                                         f32x16 (&acc)[kWM][kWN], uint8_t* lds0, uint8_t* lds1, uint8_t* lsc) {
+                                         f32x16 (&acc)[kWM][NW], uint8_t* lds0, uint8_t* lds1, uint8_t* lsc) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const uint32_t dpitch = uni(L / 2), spitch = uni(L / 16);
   const uint32_t av = uni(A.valid), b0v = uni(B0.valid), b1v = uni(B1.valid);
   const rsrc_t ad = lines_rsrc(A.data, av * dpitch), as = lines_rsrc(A.scale, av * spitch);
   const rsrc_t b0d = lines_rsrc(B0.data, b0v * dpitch), b0s = lines_rsrc(B0.scale, b0v * spitch);
   const rsrc_t b1d = PAIR ? lines_rsrc(B1.data, b1v * dpitch) : b0d;
-  // a wave's scale copies come from one of the two operands (32 lines a wave)
-  const bool up = PAIR && uni((uint32_t)wave) >= 2;
-  const rsrc_t bs = up ? lines_rsrc(B1.scale, b1v * spitch) : b0s;
+  constexpr uint32_t kScBlockBytes = Tile<NW>::kScBlockBytes;
+  constexpr int kLines = Tile<NW>::kLines;
+  constexpr uint32_t kBlock = 16 * NW;  // lines of a PAIR block: a wave's copies stay inside one
+  const uint32_t uw = uni((uint32_t)wave);
+  // a wave's scale copies move 32 lines, its code copies 16
+  const rsrc_t bs = PAIR && (32 * uw / kBlock) % 2 ? lines_rsrc(B1.scale, b1v * spitch) : b0s;
   const uint32_t nk = L / kBK;
   if (nk == 0) return;
 
@@ -114,11 +122,13 @@ __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const 
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ad, (lds_ptr_t)(base + 16 * (c * kThreads + wave * 64)), 16,
                                                (64 * c + cl) * dpitch + 16 * swz(cl, cq), sd, 0, 0);
 #pragma unroll
-    for (int c = 0; c < kBN / 64; ++c) {
-      const uint32_t line = PAIR ? 64 * (c >> 1) : 64 * c;  // first source line of the block
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(PAIR && (c & 1) ? b1d : b0d,
+    for (int c = 0; c < kLines / 64; ++c) {
+      const uint32_t at = 64 * c + cl, blk = at / kBlock;  // LDS line; its block's parity is the wave's
+      const bool up = PAIR && ((64 * c + 16 * uw) / kBlock) % 2;
+      const uint32_t line = PAIR ? blk / 2 * kBlock + at % kBlock : at;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? b1d : b0d,
                                                (lds_ptr_t)(base + kStB + 16 * (c * kThreads + wave * 64)), 16,
-                                               (line + cl) * dpitch + 16 * swz(cl, cq), sd, 0, 0);
+                                               line * dpitch + 16 * swz(cl, cq), sd, 0, 0);
     }
   };
   // Scales of a block of steps: 128 lines a copy, 16 bytes a lane.
@@ -127,8 +137,9 @@ __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const 
     __builtin_amdgcn_raw_ptr_buffer_load_lds(as, (lds_ptr_t)(sbase + 16 * (wave * 64)), 16, sl * spitch + 16 * sq, so,
                                              0, 0);
 #pragma unroll
-    for (int c = 0; c < kBN / 128; ++c) {
-      const uint32_t line = PAIR ? 64 * c + (sl & 63) : 128 * c + sl;
+    for (int c = 0; c < kLines / 128; ++c) {
+      const uint32_t at = 128 * c + sl;
+      const uint32_t line = PAIR ? at / kBlock / 2 * kBlock + at % kBlock : at;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bs, (lds_ptr_t)(sbase + kScB + 16 * (c * kThreads + wave * 64)), 16,
                                                line * spitch + 16 * sq, so, 0, 0);
     }
@@ -138,7 +149,7 @@ __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const 
   auto step = [&](uint32_t ks, const uint8_t* base, uint8_t* next) {
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
-    h2_t sa[kWM][2], sb[kWN][2];
+    h2_t sa[kWM][2], sb[NW][2];
     const uint8_t* scb = lsc + ((ks / kScSteps) & 1) * kScBlockBytes + kRowScales * (ks % kScSteps) + 4 * h;
 #pragma unroll
     for (int im = 0; im < kWM; ++im) {
@@ -147,9 +158,9 @@ __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const 
       sa[im][1] = scales_h2(sc >> 16);
     }
 #pragma unroll
-    for (int in = 0; in < kWN; ++in) {
+    for (int in = 0; in < NW; ++in) {
       const uint32_t sc =
-          *reinterpret_cast<const uint32_t*>(scb + kScB + kScLine * (wn * (kWN * 32) + in * 32 + (lane & 31)));
+          *reinterpret_cast<const uint32_t*>(scb + kScB + kScLine * (wn * (NW * 32) + in * 32 + (lane & 31)));
       sb[in][0] = scales_h2(sc & 0xFFFFu);
       sb[in][1] = scales_h2(sc >> 16);
     }
@@ -159,7 +170,7 @@ __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const 
       if ((ks + 1) % kScSteps == 0) issue_scales(nb, lsc + (nb & 1) * kScBlockBytes);
     }
     if (!live) return;
-    u32x4 wa[kWM][2], wb[kWN][2];
+    u32x4 wa[kWM][2], wb[NW][2];
 #pragma unroll
     for (int im = 0; im < kWM; ++im) {
       const uint32_t line = wm * (kWM * 32) + im * 32 + (lane & 31);
@@ -167,17 +178,17 @@ __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const 
       wa[im][1] = *reinterpret_cast<const u32x4*>(base + kRowBytes * line + 16 * swz(line, 2 * h + 1));
     }
 #pragma unroll
-    for (int in = 0; in < kWN; ++in) {
-      const uint32_t line = wn * (kWN * 32) + in * 32 + (lane & 31);
+    for (int in = 0; in < NW; ++in) {
+      const uint32_t line = wn * (NW * 32) + in * 32 + (lane & 31);
       wb[in][0] = *reinterpret_cast<const u32x4*>(base + kStB + kRowBytes * line + 16 * swz(line, 2 * h));
       wb[in][1] = *reinterpret_cast<const u32x4*>(base + kStB + kRowBytes * line + 16 * swz(line, 2 * h + 1));
     }
     // the next sub-step's fragments are decoded between this one's MFMAs
-    h8_t af[2][kWM], bf[2][kWN];
+    h8_t af[2][kWM], bf[2][NW];
 #pragma unroll
     for (int im = 0; im < kWM; ++im) af[0][im] = decode8(wa[im][0][0], sa[im][0][0]);
 #pragma unroll
-    for (int in = 0; in < kWN; ++in) bf[0][in] = decode8(wb[in][0][0], sb[in][0][0]);
+    for (int in = 0; in < NW; ++in) bf[0][in] = decode8(wb[in][0][0], sb[in][0][0]);
 #pragma unroll
     for (int s = 0; s < kBK / 16; ++s) {
       const int cu = s & 1, nx = cu ^ 1, t = s + 1;
@@ -185,18 +196,18 @@ __device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const 
 #pragma unroll
         for (int im = 0; im < kWM; ++im) af[nx][im] = decode8(wa[im][t >> 2][t & 3], sa[im][t >> 2][(t >> 1) & 1]);
 #pragma unroll
-        for (int in = 0; in < kWN; ++in) bf[nx][in] = decode8(wb[in][t >> 2][t & 3], sb[in][t >> 2][(t >> 1) & 1]);
+        for (int in = 0; in < NW; ++in) bf[nx][in] = decode8(wb[in][t >> 2][t & 3], sb[in][t >> 2][(t >> 1) & 1]);
       }
 #pragma unroll
       for (int im = 0; im < kWM; ++im)
 #pragma unroll
-        for (int in = 0; in < kWN; ++in)
+        for (int in = 0; in < NW; ++in)
           acc[im][in] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[cu][im], bf[cu][in], acc[im][in], 0, 0, 0);
       if (t < kBK / 16) {
 #pragma unroll
-        for (int i = 0; i < kWM * kWN; ++i) {
+        for (int i = 0; i < kWM * NW; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
-          __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);  // six VALU
+          __builtin_amdgcn_sched_group_barrier(0x002, 8 * (kWM + NW) / (kWM * NW), 0);  // and its share of the decode
         }
       }
     }
@@ -230,27 +241,33 @@ __device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t ntm, uint32_t 
   *tn = uni(in / gm);
 }
 
-// A wave's own 12 KB of the code stages, which are free in the epilogue: 32
-// rows x 64 columns of fp32 go in as the MFMA layout holds them (column in the
-// lane, two 32-column blocks) and come out as 8 consecutive columns of a row,
-// so that memory sees 16 bytes a lane and 128 contiguous bytes a row.
-constexpr int kStagePitch = 72;  // floats: the two lane halves, 4 rows apart, on different banks
-static_assert(32 * kStagePitch * 4 <= (int)kStageBytes / 2, "two waves share a stage");
-__device__ __forceinline__ float* wave_stage(uint8_t* lds0, uint8_t* lds1, int wave) {
-  return reinterpret_cast<float*>((wave < 2 ? lds0 : lds1) + (wave & 1) * (kStageBytes / 2));
-}
-__device__ __forceinline__ void stage_put(float* stage, int block, int v, int lane, float x) {
-  stage[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * kStagePitch + 32 * block + (lane & 31)] = x;
-}
-__device__ __forceinline__ void stage_get(const float* stage, int row, int col, float (&x)[8]) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(stage + row * kStagePitch + col);
-  const f32x4 b = *reinterpret_cast<const f32x4*>(stage + row * kStagePitch + col + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = a[i];
-    x[4 + i] = b[i];
+// A wave's own half of a code stage, which is free in the epilogue: 32 rows x
+// BLK blocks of 32 columns of fp32 go in as the MFMA layout holds them (column
+// in the lane) and come out as 8 consecutive columns of a row, so that memory
+// sees 16 bytes a lane and 64 or 128 contiguous bytes a row.
+template <int BLK>
+struct Stage {
+  static constexpr int kPitch = 32 * BLK + 8;    // floats: the two lane halves, 4 rows apart, on different banks
+  static constexpr int kLanes = 4 * BLK;         // of a row on the way out
+  static constexpr int kRows = 64 / kLanes;      // rows of one pass
+  float* p;
+  __device__ __forceinline__ Stage(uint8_t* lds0, uint8_t* lds1, int wave)
+      : p(reinterpret_cast<float*>((wave < 2 ? lds0 : lds1) + (wave & 1) * (Tile<2 * BLK>::kStageBytes / 2))) {
+    static_assert(32 * kPitch * 4 <= (int)Tile<2 * BLK>::kStageBytes / 2, "two waves share a stage");
   }
-}
+  __device__ __forceinline__ void put(int block, int v, int lane, float x) {
+    p[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * kPitch + 32 * block + (lane & 31)] = x;
+  }
+  __device__ __forceinline__ void get(int row, int col, float (&x)[8]) const {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p + row * kPitch + col);
+    const f32x4 b = *reinterpret_cast<const f32x4*>(p + row * kPitch + col + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = a[i];
+      x[4 + i] = b[i];
+    }
+  }
+};
 // Orders a wave's own LDS writes and reads (they run in issue order).
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -273,15 +290,16 @@ __device__ __forceinline__ float glu(float g, float u) {
   return g * act_logistic<ACT>(g, &dv) * u;
 }
 
-// Forward: tiles of 128 packed rows x 128 columns (256 lines).
-template <int ACT, bool KEEP>
+// Forward: tiles of 128 packed rows x 32 NW columns (64 NW lines).
+template <int ACT, bool KEEP, int NW>
 __global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_t f, int64_t k, Routing R,
                                                               uint32_t ntm, uint32_t ntn, uint16_t* __restrict__ h,
                                                               uint16_t* __restrict__ gu) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds0[kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t lds1[kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t lsc[2 * kScBlockBytes];
-  __shared__ float lsa[kBM], lsb[kBN];
+  constexpr int kCols = 32 * NW;
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[Tile<NW>::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds1[Tile<NW>::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lsc[2 * Tile<NW>::kScBlockBytes];
+  __shared__ float lsa[kBM], lsb[Tile<NW>::kLines];
   if (!routing_ok(R)) return;
   const int32_t total = route_end(R, R.num_experts - 1);
   uint32_t tm, tn;
@@ -290,84 +308,86 @@ __global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_
   if (row0 >= total) return;
   int32_t rbeg, rend;
   const int e = find_expert(R, row0, &rbeg, &rend);
-  const int64_t col0 = (int64_t)tn * (kBN / 2);
-  const uint32_t cols = (uint32_t)min<int64_t>(f - col0, kBN / 2);
+  const int64_t col0 = (int64_t)tn * kCols;
+  const uint32_t cols = (uint32_t)min<int64_t>(f - col0, kCols);
   const int64_t gl = (int64_t)e * 2 * f + col0, ul = gl + f;
   const Lines A{O.a_data + (int64_t)row0 * (k / 2), O.a_scale + (int64_t)row0 * (k / 16), (uint32_t)kBM};
   const Lines G{O.b_data + gl * (k / 2), O.b_scale + gl * (k / 16), cols};
   const Lines U{O.b_data + ul * (k / 2), O.b_scale + ul * (k / 16), cols};
-  f32x16 acc[kWM][kWN];
+  f32x16 acc[kWM][NW];
 #pragma unroll
   for (int im = 0; im < kWM; ++im)
 #pragma unroll
-    for (int in = 0; in < kWN; ++in) acc[im][in] = f32x16{};
+    for (int in = 0; in < NW; ++in) acc[im][in] = f32x16{};
   const int tid = threadIdx.x, wave = uni((int32_t)(tid >> 6)), lane = tid & 63;
   const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const bool live = (uint32_t)wn * 64 < cols;
-  multiply<true>(A, G, U, (uint32_t)k, live, acc, lds0, lds1, lsc);
+  const bool live = (uint32_t)wn * (kCols / 2) < cols;
+  multiply<true, NW>(A, G, U, (uint32_t)k, live, acc, lds0, lds1, lsc);
 
   if (tid < kBM) lsa[tid] = O.a_amax[row0 + tid] / 2688.0f;
-  {
-    const uint32_t j = tid & 127;
-    const float* am = O.b_amax + (tid < 128 ? gl : ul);
+  if (tid < 2 * kCols) {
+    const uint32_t j = tid % kCols;
+    const float* am = O.b_amax + (tid < kCols ? gl : ul);
     lsb[tid] = j < cols ? am[j] / 2688.0f : 0.0f;
   }
   __syncthreads();
   if (!live) return;
-  float* stage = wave_stage(lds0, lds1, wave);
-  const uint32_t j0 = wn * 64, c = 8 * (lane & 7);
+  constexpr int BLK = NW / 2;
+  Stage<BLK> stage(lds0, lds1, wave);
+  const uint32_t j0 = wn * (32 * BLK), c = 8 * (lane % Stage<BLK>::kLanes), srow = lane / Stage<BLK>::kLanes;
   const bool write = j0 + c < cols;
 #pragma unroll
   for (int im = 0; im < kWM; ++im) {
-    const int64_t out0 = row0 + wm * (kWM * 32) + im * 32;
-    float g[2][16], u[2][16];
+    const int64_t out0 = row0 + wm * (kWM * 32) + im * 32 + srow;
+    float g[BLK][16], u[BLK][16];
 #pragma unroll
-    for (int in = 0; in < 2; ++in) {
-      const float sg = lsb[j0 + in * 32 + (lane & 31)], su = lsb[128 + j0 + in * 32 + (lane & 31)];
+    for (int in = 0; in < BLK; ++in) {
+      const float sg = lsb[j0 + in * 32 + (lane & 31)], su = lsb[kCols + j0 + in * 32 + (lane & 31)];
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         const float sa = lsa[wm * (kWM * 32) + im * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
         g[in][v] = (acc[im][in][v] * sa) * sg;
-        u[in][v] = (acc[im][in + 2][v] * sa) * su;
-        stage_put(stage, in, v, lane, glu<ACT>(g[in][v], u[in][v]));
+        u[in][v] = (acc[im][in + BLK][v] * sa) * su;
+        stage.put(in, v, lane, glu<ACT>(g[in][v], u[in][v]));
       }
     }
     auto put_rows = [&](uint16_t* base, int64_t pitch) {
       wave_sync();
 #pragma unroll
-      for (int r = 0; r < 32; r += 8) {
+      for (int r = 0; r < 32; r += Stage<BLK>::kRows) {
         float v[8];
-        stage_get(stage, r + (lane >> 3), c, v);
-        if (write) *reinterpret_cast<u32x4*>(base + (out0 + r + (lane >> 3)) * pitch + col0 + j0 + c) = pack8(v);
+        stage.get(r + srow, c, v);
+        if (write) *reinterpret_cast<u32x4*>(base + (out0 + r) * pitch + col0 + j0 + c) = pack8(v);
       }
       wave_sync();
     };
     put_rows(h, f);
     if (KEEP) {
 #pragma unroll
-      for (int in = 0; in < 2; ++in)
+      for (int in = 0; in < BLK; ++in)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) stage_put(stage, in, v, lane, g[in][v]);
+        for (int v = 0; v < 16; ++v) stage.put(in, v, lane, g[in][v]);
       put_rows(gu, 2 * f);
 #pragma unroll
-      for (int in = 0; in < 2; ++in)
+      for (int in = 0; in < BLK; ++in)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) stage_put(stage, in, v, lane, u[in][v]);
+        for (int v = 0; v < 16; ++v) stage.put(in, v, lane, u[in][v]);
       put_rows(gu + f, 2 * f);
     }
   }
 }
 
-// Backward: tiles of 128 packed rows x 256 columns of dh.
-template <int ACT>
+// Backward: tiles of 128 packed rows x 64 NW columns of dh.
+template <int ACT, int NW>
 __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_t f, int64_t k, Routing R,
                                                               uint32_t ntm, uint32_t ntn,
                                                               const uint16_t* __restrict__ gu,
                                                               uint16_t* __restrict__ dgu) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds0[kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t lds1[kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t lsc[2 * kScBlockBytes];
-  __shared__ float lsa[kBM], lsb[kBN];
+  constexpr int kCols = Tile<NW>::kLines;
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[Tile<NW>::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds1[Tile<NW>::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lsc[2 * Tile<NW>::kScBlockBytes];
+  __shared__ float lsa[kBM], lsb[Tile<NW>::kLines];
   if (!routing_ok(R)) return;
   const int32_t total = route_end(R, R.num_experts - 1);
   uint32_t tm, tn;
@@ -376,56 +396,58 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
   if (row0 >= total) return;
   int32_t rbeg, rend;
   const int e = find_expert(R, row0, &rbeg, &rend);
-  const int64_t col0 = (int64_t)tn * kBN;
-  const uint32_t cols = (uint32_t)min<int64_t>(f - col0, kBN);
+  const int64_t col0 = (int64_t)tn * kCols;
+  const uint32_t cols = (uint32_t)min<int64_t>(f - col0, kCols);
   const int64_t line0 = (int64_t)e * f + col0;
   const Lines A{O.a_data + (int64_t)row0 * (k / 2), O.a_scale + (int64_t)row0 * (k / 16), (uint32_t)kBM};
   const Lines B{O.b_data + line0 * (k / 2), O.b_scale + line0 * (k / 16), cols};
-  f32x16 acc[kWM][kWN];
+  f32x16 acc[kWM][NW];
 #pragma unroll
   for (int im = 0; im < kWM; ++im)
 #pragma unroll
-    for (int in = 0; in < kWN; ++in) acc[im][in] = f32x16{};
+    for (int in = 0; in < NW; ++in) acc[im][in] = f32x16{};
   const int tid = threadIdx.x, wave = uni((int32_t)(tid >> 6)), lane = tid & 63;
   const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const bool live = (uint32_t)wn * 128 < cols;
-  multiply<false>(A, B, B, (uint32_t)k, live, acc, lds0, lds1, lsc);
+  const bool live = (uint32_t)wn * (kCols / 2) < cols;
+  multiply<false, NW>(A, B, B, (uint32_t)k, live, acc, lds0, lds1, lsc);
 
   if (tid < kBM) lsa[tid] = O.a_amax[row0 + tid] / 2688.0f;
-  lsb[tid] = (uint32_t)tid < cols ? O.b_amax[line0 + tid] / 2688.0f : 0.0f;
+  if (tid < kCols) lsb[tid] = (uint32_t)tid < cols ? O.b_amax[line0 + tid] / 2688.0f : 0.0f;
   __syncthreads();
   if (!live) return;
-  float* stage = wave_stage(lds0, lds1, wave);
+  constexpr int BLK = NW / 2, kRows = Stage<BLK>::kRows, kPasses = 32 / kRows;
+  Stage<BLK> stage(lds0, lds1, wave);
+  const int c = 8 * (lane % Stage<BLK>::kLanes), srow = lane / Stage<BLK>::kLanes;
 #pragma unroll
   for (int im = 0; im < kWM; ++im)
 #pragma unroll
-    for (int pair = 0; pair < kWN; pair += 2) {
-      const uint32_t j0 = wn * 128 + pair * 32, c = 8 * (lane & 7);
+    for (int in0 = 0; in0 < NW; in0 += BLK) {
+      const uint32_t j0 = wn * (kCols / 2) + in0 * 32;
       const bool write = j0 + c < cols;
-      const int64_t at0 = (row0 + wm * (kWM * 32) + im * 32 + (lane >> 3)) * 2 * f + col0 + j0 + c;
-      u32x4 gq[4], uq[4];
+      const int64_t at0 = (row0 + wm * (kWM * 32) + im * 32 + srow) * 2 * f + col0 + j0 + c;
+      u32x4 gq[kPasses], uq[kPasses];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < kPasses; ++r) {
         gq[r] = uq[r] = u32x4{0, 0, 0, 0};
         if (write) {
-          gq[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(gu + at0 + 16 * r * f));
-          uq[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(gu + at0 + 16 * r * f + f));
+          gq[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(gu + at0 + 2 * kRows * r * f));
+          uq[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(gu + at0 + 2 * kRows * r * f + f));
         }
       }
 #pragma unroll
-      for (int in = 0; in < 2; ++in) {
+      for (int in = 0; in < BLK; ++in) {
         const float sb = lsb[j0 + in * 32 + (lane & 31)];
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const float sa = lsa[wm * (kWM * 32) + im * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
-          stage_put(stage, in, v, lane, (acc[im][pair + in][v] * sa) * sb);
+          stage.put(in, v, lane, (acc[im][in0 + in][v] * sa) * sb);
         }
       }
       wave_sync();
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < kPasses; ++r) {
         float dh[8], dg[8], du[8];
-        stage_get(stage, 8 * r + (lane >> 3), c, dh);
+        stage.get(kRows * r + srow, c, dh);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float g = i & 1 ? bf16hi(gq[r][i >> 1]) : bf16lo(gq[r][i >> 1]);
@@ -436,8 +458,8 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
           dg[i] = dh[i] * u * __builtin_fmaf(a * (1.0f - q), dv, q);
         }
         if (write) {
-          *reinterpret_cast<u32x4*>(dgu + at0 + 16 * r * f) = pack8(dg);
-          *reinterpret_cast<u32x4*>(dgu + at0 + 16 * r * f + f) = pack8(du);
+          *reinterpret_cast<u32x4*>(dgu + at0 + 2 * kRows * r * f) = pack8(dg);
+          *reinterpret_cast<u32x4*>(dgu + at0 + 2 * kRows * r * f + f) = pack8(du);
         }
       }
       wave_sync();
@@ -470,50 +492,60 @@ int make_routing(const int64_t* h_splits, const int32_t* d_offs, int32_t* d_stat
   return graph ? graph_routing(d_offs, d_status, E, rows, R) : host_routing(h_splits, rows, E, R);
 }
 
-int launch_fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Routing& R, int32_t act, uint16_t* h,
-               uint16_t* gu, hipStream_t st) {
-  const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + kBN / 2 - 1) / (kBN / 2));
-  const dim3 grid(ntm * ntn);
-  if (act == MOE_ACT_SILU) {
-    if (gu) hipLaunchKernelGGL((glu_fwd_kernel<MOE_ACT_SILU, true>), grid, dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h, gu);
-    else hipLaunchKernelGGL((glu_fwd_kernel<MOE_ACT_SILU, false>), grid, dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h, gu);
-  } else {
-    if (gu) hipLaunchKernelGGL((glu_fwd_kernel<MOE_ACT_GELU, true>), grid, dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h, gu);
-    else hipLaunchKernelGGL((glu_fwd_kernel<MOE_ACT_GELU, false>), grid, dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h, gu);
-  }
+// Half as wide tiles where the wide ones leave at least half of the CUs idle:
+// they decode a third more for an MFMA, but there are twice as many.  Forward,
+// 7168 x 2 x 2048: 1024 rows (128 wide tiles) 93 us wide, 70 narrow; 2944 rows
+// of 4096 x 2 x 1024 (184) 64 and 66; 65536 rows 3.03 and 3.32 ms.
+bool narrow(int64_t wide_tiles) { return wide_tiles <= kCus / 2; }
+
+template <int ACT, bool KEEP, int NW>
+int launch_fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Routing& R, uint16_t* h, uint16_t* gu,
+               hipStream_t st) {
+  const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + 32 * NW - 1) / (32 * NW));
+  if (NW == 4 && narrow((int64_t)ntm * ntn)) return launch_fwd<ACT, KEEP, 2>(O, rows, f, k, R, h, gu, st);
+  hipLaunchKernelGGL((glu_fwd_kernel<ACT, KEEP, NW>), dim3(ntm * ntn), dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h,
+                     gu);
+  return hip_status();
+}
+
+template <int ACT, int NW>
+int launch_bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Routing& R, const uint16_t* gu,
+               uint16_t* dgu, hipStream_t st) {
+  const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + 64 * NW - 1) / (64 * NW));
+  if (NW == 4 && narrow((int64_t)ntm * ntn)) return launch_bwd<ACT, 2>(O, rows, f, k, R, gu, dgu, st);
+  hipLaunchKernelGGL((glu_bwd_kernel<ACT, NW>), dim3(ntm * ntn), dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, gu, dgu);
   return hip_status();
 }
 
 int fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
         const int32_t* d_offs, int32_t* d_status, bool graph, int32_t act, uint16_t* h, uint16_t* gu, void* stream) {
-  int rc = check_glu(O, rows, f, k, E, act, kBN / 2);
+  int rc = check_glu(O, rows, f, k, E, act, 64);
   if (rc) return rc;
   if (rows && !h) return NVFP4G_EINVAL;
   if (!aligned(h, 16) || !aligned(gu, 16)) return NVFP4G_EALIGN;
   Routing R;
   if ((rc = make_routing(h_splits, d_offs, d_status, rows, E, graph, &R))) return rc;
-  return rows ? launch_fwd(O, rows, f, k, R, act, h, gu, (hipStream_t)stream) : NVFP4G_OK;
+  if (rows == 0) return NVFP4G_OK;
+  const hipStream_t st = (hipStream_t)stream;
+  if (act == MOE_ACT_SILU)
+    return gu ? launch_fwd<MOE_ACT_SILU, true, 4>(O, rows, f, k, R, h, gu, st)
+              : launch_fwd<MOE_ACT_SILU, false, 4>(O, rows, f, k, R, h, gu, st);
+  return gu ? launch_fwd<MOE_ACT_GELU, true, 4>(O, rows, f, k, R, h, gu, st)
+            : launch_fwd<MOE_ACT_GELU, false, 4>(O, rows, f, k, R, h, gu, st);
 }
 
 int bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
         const int32_t* d_offs, int32_t* d_status, bool graph, const uint16_t* gu, int32_t act, uint16_t* dgu,
         void* stream) {
-  int rc = check_glu(O, rows, f, k, E, act, kBN);
+  int rc = check_glu(O, rows, f, k, E, act, 128);
   if (rc) return rc;
   if (rows && (!gu || !dgu)) return NVFP4G_EINVAL;
   if (!aligned(gu, 16) || !aligned(dgu, 16)) return NVFP4G_EALIGN;
   Routing R;
   if ((rc = make_routing(h_splits, d_offs, d_status, rows, E, graph, &R))) return rc;
   if (rows == 0) return NVFP4G_OK;
-  const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + kBN - 1) / kBN);
-  const dim3 grid(ntm * ntn);
-  if (act == MOE_ACT_SILU)
-    hipLaunchKernelGGL((glu_bwd_kernel<MOE_ACT_SILU>), grid, dim3(kThreads), 0, (hipStream_t)stream, O, f, k, R, ntm,
-                       ntn, gu, dgu);
-  else
-    hipLaunchKernelGGL((glu_bwd_kernel<MOE_ACT_GELU>), grid, dim3(kThreads), 0, (hipStream_t)stream, O, f, k, R, ntm,
-                       ntn, gu, dgu);
-  return hip_status();
+  return act == MOE_ACT_SILU ? launch_bwd<MOE_ACT_SILU, 4>(O, rows, f, k, R, gu, dgu, (hipStream_t)stream)
+                             : launch_bwd<MOE_ACT_GELU, 4>(O, rows, f, k, R, gu, dgu, (hipStream_t)stream);
 }
 
 }  // namespace

@@ -307,10 +307,11 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(const T* __restrict
 // ------------------------------------------------------------------- plan
 
 constexpr int kPlanPairs = 256;       // pairs one wave ranks in the split form
-constexpr int kSmallPairs = 4096;     // the one-launch form: pairs, experts
+constexpr int kSmallSteps = 16;       // the one-launch form: steps of 64 pairs a wave keeps in registers, experts
 constexpr int kSmallExperts = 512;
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallPairs = kSmallThreads * kSmallSteps;
 
 __device__ __forceinline__ int expert_of(const int32_t* ids, int64_t p, int64_t end, int E) {
   const int e = p < end ? ids[p] : -1;
@@ -411,12 +412,15 @@ __global__ __launch_bounds__(kSmallThreads) void plan_small_kernel(const int32_t
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int share = (pairs + kSmallThreads - 1) / kSmallThreads * 64;  // pairs of a wave, whole steps
   const int p0 = wave * share, p1 = min(p0 + share, pairs);
+  int id[kSmallSteps];
+#pragma unroll
+  for (int i = 0; i < kSmallSteps; ++i)
+    if (p0 + 64 * i < p1) id[i] = expert_of(ids, p0 + 64 * i + lane, p1, E);
   for (int i = tid; i < kSmallWaves * E; i += kSmallThreads) hist[i] = 0;
   __syncthreads();
-  for (int p = p0; p < p1; p += 64) {
-    const int e = expert_of(ids, p + lane, p1, E);
-    if (e >= 0) atomicAdd(&hist[wave * E + e], 1);
-  }
+#pragma unroll
+  for (int i = 0; i < kSmallSteps; ++i)
+    if (p0 + 64 * i < p1 && id[i] >= 0) atomicAdd(&hist[wave * E + id[i]], 1);
   __syncthreads();
   for (int e = tid; e < E; e += kSmallThreads) {
     int acc = 0;
@@ -429,10 +433,12 @@ __global__ __launch_bounds__(kSmallThreads) void plan_small_kernel(const int32_t
   }
   __syncthreads();
   const int total = group_begins(cnt, E, begin, wtot);
-  for (int p = p0; p < p1; p += 64) {
-    const int e = expert_of(ids, p + lane, p1, E);
-    const int r = wave_rank(e, ebits, hist + wave * E);
-    if (p + lane < p1) write_pair(p + lane, e >= 0 ? begin[e] + r : -1, cap, rows, src);
+#pragma unroll
+  for (int i = 0; i < kSmallSteps; ++i) {
+    const int p = p0 + 64 * i;
+    if (p >= p1) break;
+    const int r = wave_rank(id[i], ebits, hist + wave * E);
+    if (p + lane < p1) write_pair(p + lane, id[i] >= 0 ? begin[id[i]] + r : -1, cap, rows, src);
   }
   fill_padding(0, 1, cap, E, total, begin, cnt, src);
   write_ends(E, begin, cnt, cap, total, offs, counts, status);

@@ -25,7 +25,6 @@ constexpr int kStepK = 256;     // contraction step of a wave
 constexpr int kTokenThreads = 512;
 constexpr int kTokenWaves = kTokenThreads / 64;
 constexpr int kTokenLds = 72 * 1024;  // of the 160 KB of a CU, so that two work-groups fit; twice that where one is enough
-constexpr int kCus = 256;
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 // s_waitcnt for at most n outstanding vector-memory operations.

@@ -51,7 +51,7 @@ def with_change(args, at, value):
 
 ROUTE = [FAKE, 0, 4, 8, 2, None, 0, 1, 1.0, FAKE, FAKE, None]
 ROUTE_BWD = [FAKE, 0, 4, 8, 2, FAKE, FAKE, 0, 1, 1.0, FAKE, None]
-PLAN = [FAKE, 5000, 8, 8192, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 20, None]
+PLAN = [FAKE, 50000, 8, 8192, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 20, None]
 DISPATCH = [FAKE, 4, 64, 2, FAKE, FAKE, FAKE, 8, 256, None, None, 0, FAKE, None, None]
 COMBINE = [FAKE, 0, 256, 4, 64, 2, FAKE, None, FAKE, None]
 TOKEN_GLU = [FAKE, 4, 64, 2, FAKE, FAKE, FAKE, FAKE, 32, 8, 0, FAKE, None]
@@ -119,7 +119,8 @@ def test_nothing_to_do_is_no_error(lib):
 
 
 def test_workspace_sizes(lib):
-    assert moe.moe_plan_workspace(4096, 512) == 0 and moe.moe_plan_workspace(4097, 512) > 0
+    assert moe.moe_plan_workspace(16384, 512) == 0 and moe.moe_plan_workspace(16385, 512) > 0
+    assert moe.moe_plan_workspace(5000, 513) > 0
     assert moe.moe_plan_workspace(0, 4096) > 0
     assert moe.lora_workspace(0, 64, 16, 8) == 0
     assert moe.lora_workspace(65, 64, 16, 8) >= 65 * 16 * 4
