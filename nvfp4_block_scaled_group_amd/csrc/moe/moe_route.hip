@@ -307,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(const T* __restrict
 // ------------------------------------------------------------------- plan
 
 constexpr int kPlanPairs = 256;       // pairs one wave ranks in the split form
-constexpr int kSmallSteps = 16;       // the one-launch form: steps of 64 pairs a wave keeps in registers, experts
+constexpr int kSmallSteps = 4;        // the one-launch form: steps of 64 pairs a wave keeps in registers (at 11 it took 20 us, the split form 15), experts
 constexpr int kSmallExperts = 512;
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallWaves = kSmallThreads / 64;
