@@ -14,19 +14,27 @@ namespace {
 
 using namespace moe;
 
-// Pairs of the leader's expert, in pair order, into list[]; returns their
-// number, or 0 if an earlier pair leads.  All threads of the work-group.
-__device__ int gather_pairs(const int32_t* ids, int pairs, int lead, int e, int32_t* list, int32_t* wcnt) {
+// Whether no pair before `lead` has its expert (each wave finds out by
+// itself).  mine: ids[lane], loaded beside e.
+__device__ __forceinline__ bool leads(const int32_t* ids, int lead, int e, int lane, int mine) {
+  bool earlier = lane < lead && mine == e;
+  for (int p = lane + 64; p < lead; p += 64) earlier |= ids[p] == e;
+  return !__any(earlier);
+}
+
+// Pairs of expert e, in pair order, into list[]; returns their number.  All
+// threads of the work-group; the list is there after the last barrier inside.
+// own: ids[thread], loaded beside e.  Done before the weights' first loads:
+// behind them it took 1 to 3% longer.
+__device__ __forceinline__ int gather_pairs(const int32_t* ids, int pairs, int e, int own, int32_t* list, int32_t* wcnt) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int at = 0;
-  bool earlier = false;
   for (int p0 = 0; p0 < pairs; p0 += kTokenThreads) {
     const int p = p0 + tid;
-    const bool mine = p < pairs && ids[p] == e;
-    earlier |= mine && p < lead;
+    const bool mine = p < pairs && (p0 ? ids[p] : own) == e;
     const uint64_t b = __ballot(mine);
     if (lane == 0) wcnt[wave] = __popcll(b);
-    if (__syncthreads_or(earlier)) return 0;
+    __syncthreads();
     int before = at;
     for (int w = 0; w < kTokenWaves; ++w) {
       if (w < wave) before += wcnt[w];
@@ -50,7 +58,7 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void token_kernel(
   constexpr int kCols = MODE == kModeGlu ? NL / 2 * 16 : NL * 16;   // output columns of a wave
   const int lane = threadIdx.x & 63, wave = uni((int32_t)(threadIdx.x >> 6));
   const int lead = uni((int32_t)blockIdx.y);
-  const int e = uni(ids[lead]);
+  const int mine = ids[min(lane, pairs - 1)], own = ids[min((int)threadIdx.x, pairs - 1)], e = uni(ids[lead]);
   const int64_t ocols = MODE == kModeGlu ? n / 2 : n;
   const int groups = kTokenWaves / P.ks, group = wave / P.ks, part = wave % P.ks;
   const int64_t first_col = (int64_t)blockIdx.x * groups * kCols, col0 = first_col + group * kCols;
@@ -65,13 +73,21 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void token_kernel(
   // The choices of a lone token are taken one by one (a token that names an
   // expert twice reads its weights twice), with nothing to gather.
   const bool lone = pairs <= per;
-  const int cnt = lone ? 1 : gather_pairs(ids, pairs, lead, e, list, wcnt);
-  if (cnt == 0) return;
+  if (!lone && !leads(ids, lead, e, lane, mine)) return;
+  const int cnt = lone ? 1 : gather_pairs(ids, pairs, e, own, list, wcnt);
   auto pair_at = [&](int i) { return lone ? lead : list[i]; };
   const int64_t line0 = (int64_t)e * n;
   TileLines<MODE, NL> W;
   W.init(b_data, b_scale, line0, col0, ocols, k, lane);
   f32x4* red = reinterpret_cast<f32x4*>(xlds);
+  // 2688 times the line factors of this lane's columns, loaded before anything waits
+  float sg[kCols / 16], su[kCols / 16];
+#pragma unroll
+  for (int c = 0; c < kCols / 16; ++c) {
+    const int64_t col = min<int64_t>(col0 + 16 * c, ocols - 16) + (lane & 15);
+    sg[c] = b_amax[line0 + col];
+    su[c] = MODE == kModeGlu ? b_amax[line0 + ocols + col] : 0.0f;
+  }
   for (int first = 0; first < cnt; first += P.rows) {
     f32x4 acc[MT][NL];
     if (first) __syncthreads();  // the last pass is done with the staged rows and the joined sums
@@ -95,8 +111,6 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void token_kernel(
         } else {
           a = P.ks > 1 ? joined<MT, NL>(red, group, P.ks, mt, c, lane) : acc[mt][c];
         }
-        const float s = b_amax[line0 + col] / 2688.0f;
-        const float su = MODE == kModeGlu ? b_amax[line0 + ocols + col] / 2688.0f : 0.0f;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int i = mt * 16 + 4 * (lane >> 4) + v;
@@ -104,10 +118,10 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void token_kernel(
           const int64_t p = pair_at(first + i);
           if (MODE == kModeGlu) {
             float dv;
-            const float g = a[v] * s, u = b[v] * su;
+            const float g = a[v] * (sg[c] / 2688.0f), u = b[v] * (su[c] / 2688.0f);
             reinterpret_cast<uint16_t*>(out)[p * ocols + col] = to_bf16(g * act_logistic<ACT>(g, &dv) * u);
           } else {
-            reinterpret_cast<float*>(out)[p * ocols + col] = a[v] * s;
+            reinterpret_cast<float*>(out)[p * ocols + col] = a[v] * (sg[c] / 2688.0f);
           }
         }
       }

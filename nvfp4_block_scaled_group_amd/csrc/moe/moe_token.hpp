@@ -51,12 +51,13 @@ struct TokenPlan {
 };
 
 // rows: the most rows of a pass; ks: waves that should split the contraction
-// (fewer where their staged rows would not fit); tiles: MFMA tiles a wave joins
-// through LDS; extra: bytes the epilogue wants beside them; groups: the
-// work-groups of the launch.
+// (fewer where their staged rows would not fit or a wave would have no step:
+// 23 tokens, 384 elements in two steps, 4 ways 24 us, 1 way 13); tiles: MFMA
+// tiles a wave joins through LDS; extra: bytes the epilogue wants beside them;
+// groups: the work-groups of the launch.
 inline TokenPlan token_plan(int64_t k, int rows, int ks, int tiles, int64_t extra, int64_t groups) {
   const int64_t limit = rows <= 16 && groups > kCus ? kTokenLds : 2 * kTokenLds, steps = (k + kStepK - 1) / kStepK;
-  while (ks > 1 && rows * (ks * 4 * kStepK + 16) > limit) ks /= 2;
+  while (ks > 1 && (rows * (ks * 4 * kStepK + 16) > limit || 2 * ks > steps + 1)) ks /= 2;
   const int64_t want = ((steps + ks - 1) / ks + 1) / 2 * 2;
   const int64_t room = (limit / rows - 16) / (2 * kStepK) / ks / 2 * 2;
   TokenPlan p;
