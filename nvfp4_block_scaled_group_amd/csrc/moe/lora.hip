@@ -237,33 +237,34 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void few_rows_kerne
 
 // ----------------------------------------------------- projection, many rows
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kIM = 4, kIN = 2;                     // 32 x 32 tiles of a wave: all 128 rows x 64 lines
+constexpr int kBM = 128, kBK = 64;
+constexpr int kIM = 4;                              // 32 x 32 tiles of a wave: all 128 rows x kIN blocks of lines
 constexpr uint32_t kXBytes = kBM * kBK * 2;         // 16 KB: 128 bytes a row
-constexpr uint32_t kWBytes = kBN * kBK / 2;         // 8 KB: 32 bytes a line
-constexpr uint32_t kStage = kXBytes + kWBytes;
+template <int IN>
+constexpr uint32_t kStageOf = kXBytes + 128 * IN * kBK / 2;  // and 32 bytes a line: 24 KB, 20 KB
 
 
-// Tile of 128 rows x 256 lines, or one of gridDim.y parts of its contraction
+// Tile of 128 rows x 128 kIN lines, or one of gridDim.y parts of its contraction
 // (SPLIT: fp32 sums to partial[blockIdx.y], for finish_kernel, which adds the
 // adapters).  Copies run one step ahead; with SPLIT, where a CU may
 // have one work-group alone and the latency sets the pace (2.3 us a step), two
-// (with many tiles the third stage costs 2%).  Wave w takes all rows and lines 64 w .. + 63,
+// (with many tiles the third stage costs 2%).  Wave w takes all rows and 32 kIN lines,
 // so no weight is decoded twice in a work-group.  Element granules (8 of x,
 // 16 bytes) and code granules are XOR-placed in LDS so that fragment reads of
 // 32 consecutive rows or lines spread over the banks.  Rows past the last and
 // elements past k read as zero (the weights' codes there, the next line's, are
 // finite and meet zeros).
-template <bool SPLIT>
+template <bool SPLIT, int kIN>
 __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
     const uint16_t* __restrict__ x, int64_t tokens, int64_t k, const uint8_t* __restrict__ w_data,
     const uint8_t* __restrict__ w_scale, const float* __restrict__ w_amax, int64_t n,
     const uint16_t* __restrict__ lora_b, int adapters, int rank, const int32_t* __restrict__ ids,
     const int32_t* __restrict__ order, const uint16_t* __restrict__ v, uint32_t ntm, uint32_t ntn, uint16_t* __restrict__ y, float* __restrict__ partial) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds0[kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds1[kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds2[SPLIT ? kStage : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[kStageOf<kIN>];
+  __shared__ __attribute__((aligned(16))) uint8_t lds1[kStageOf<kIN>];
+  __shared__ __attribute__((aligned(16))) uint8_t lds2[SPLIT ? kStageOf<kIN> : 16];
   __shared__ int32_t lrow[kBM];  // the tile's rows, counted from base0; past the last: -1
+  constexpr int kBN = 128 * kIN, kWave = 32 * kIN;  // lines of the tile, of a wave
   const int tid = threadIdx.x, wave = uni((int32_t)(tid >> 6)), lane = tid & 63, h = lane >> 5;
   // groups of 8 row tiles sweep the column tiles together, a run of tiles an XCD
   const uint32_t nb = gridDim.x, xcd = blockIdx.x % kNumXcd, q8 = nb / kNumXcd, r8 = nb % kNumXcd;
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   auto fetch_scales = [&](uint32_t ks, uint32_t (&sc)[kIN]) {
 #pragma unroll
     for (int in = 0; in < kIN; ++in)
-      sc[in] = __builtin_amdgcn_raw_buffer_load_b16(ws, (wave * 64 + in * 32 + (lane & 31)) * sp + 2 * h, ks * (kBK / 16),
+      sc[in] = __builtin_amdgcn_raw_buffer_load_b16(ws, (wave * kWave + in * 32 + (lane & 31)) * sp + 2 * h, ks * (kBK / 16),
                                                     0);
   };
 
@@ -341,7 +342,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
     u32x4 wq[kIN];
 #pragma unroll
     for (int in = 0; in < kIN; ++in) {
-      const uint32_t line = wave * 64 + in * 32 + (lane & 31);
+      const uint32_t line = wave * kWave + in * 32 + (lane & 31);
       wq[in] = *reinterpret_cast<const u32x4*>(base + kXBytes + 32 * line + 16 * (h ^ ((line >> 2) & 1)));
     }
     // Sub-step s, lane half h: the 8 elements of word 4h + s.  The next
@@ -403,7 +404,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
     if (ks < nk) step(ks, lds0, sc0, lds1, sc1);
   }
 
-  const uint32_t jw = wave * 64;  // first line of the wave in the tile
+  const uint32_t jw = wave * kWave;  // first line of the wave in the tile
   const uint32_t yp = (uint32_t)(2 * n);
   float lf[kIN];
 #pragma unroll
@@ -501,33 +502,29 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
 }
 
 // y[t] = the sum of the parts, in their order, plus the row's adapter, rounded
-// once.  A work-group takes kThreads * 8 columns of a row.
+// once.  A work-group takes kThreads * 2 columns of a row.
 __global__ __launch_bounds__(kThreads) void finish_kernel(const float* __restrict__ partial, int parts, int64_t tokens,
                                                           int64_t n, const uint16_t* __restrict__ lora_b,
                                                           const float* __restrict__ alpha, int adapters, int rank,
                                                           const int32_t* __restrict__ ids, const float* __restrict__ v,
                                                           int v_parts, uint16_t* __restrict__ y) {
   __shared__ __attribute__((aligned(16))) float lv[LORA_MAX_RANK];
-  const int64_t t = blockIdx.x, c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * 8;
+  const int64_t t = blockIdx.x, c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * 2;
   const int a = adapters ? uni(ids[t]) : -1;
   const bool adapted = (uint32_t)a < (uint32_t)adapters;
   if (adapted && (int)threadIdx.x < rank) lv[threadIdx.x] = row_v(v, v_parts, tokens, t, rank, threadIdx.x, a, alpha);
   __syncthreads();
   if (c >= n) return;
   const int64_t count = tokens * n, i = t * n + c;
-  f32x4 s0 = *reinterpret_cast<const f32x4*>(partial + i), s1 = *reinterpret_cast<const f32x4*>(partial + i + 4);
-  for (int p = 1; p < parts; ++p) {
-    s0 += *reinterpret_cast<const f32x4*>(partial + p * count + i);
-    s1 += *reinterpret_cast<const f32x4*>(partial + p * count + i + 4);
+  f32x2 s = *reinterpret_cast<const f32x2*>(partial + i);
+#pragma unroll 4
+  for (int p = 1; p < parts; ++p) s += *reinterpret_cast<const f32x2*>(partial + p * count + i);
+  if (adapted) {
+    const uint16_t* b = lora_b + ((int64_t)a * n + c) * rank;
+    s[0] += rank_dot(b, lv, rank);
+    s[1] += rank_dot(b + rank, lv, rank);
   }
-  float o[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    o[q] = q < 4 ? s0[q] : s1[q - 4];
-    if (adapted) o[q] += rank_dot(lora_b + ((int64_t)a * n + c + q) * rank, lv, rank);
-  }
-  *reinterpret_cast<u32x4*>(y + i) = u32x4{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                                          pack_bf16(o[6], o[7])};
+  *reinterpret_cast<uint32_t*>(y + i) = pack_bf16(s[0], s[1]);
 }
 
 // ------------------------------------------------------------- host side
@@ -540,35 +537,47 @@ int shrink_parts(int64_t tokens, int64_t k) {
   return (int)std::max<int64_t>(1, std::min(std::min(want, (steps + kShrinkWaves - 1) / kShrinkWaves), (int64_t)kMaxSplit));
 }
 
+constexpr int kWideLines = 256;  // lines of a wide tile of the projection
 constexpr int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 // Parts of the contraction of many rows: as many as give every CU two
-// work-groups where the tiles alone do not give it one, at least 8 steps each,
-// and their sums within kMaxWorkspace.
-constexpr int64_t kMaxWorkspace = 24 << 20;
-int project_parts(int64_t tokens, int64_t k, int64_t n) {
-  const int64_t tiles = ((tokens + kBM - 1) / kBM) * ((n + kBN - 1) / kBN);
+// work-groups where the tiles alone do not give it one, at least 4 steps each
+// (8 left the 7 tiles of 125 rows of a 1552 x 800 projection alone: 29 us
+// instead of 19), and all that is kept between the launches within kMaxWorkspace.
+constexpr int64_t kMaxWorkspace = 32 << 20;
+int project_parts(int64_t tokens, int64_t k, int64_t n, int rank) {
+  const int64_t tiles = ((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines);
   if (tokens <= kFewRows || tiles >= kCus) return 1;
-  const int64_t by_steps = (k + kBK - 1) / kBK / 8, by_room = kMaxWorkspace / (tokens * n * 4);
+  const int64_t other = round256(tokens * rank * 4 * shrink_parts(tokens, k)) + round256(tokens * 4);
+  const int64_t by_steps = (k + kBK - 1) / kBK / 4, by_room = (kMaxWorkspace - other) / (tokens * n * 4);
   return (int)std::max<int64_t>(1, std::min(std::min(2 * kCus / tiles, by_steps), by_room));
 }
 
-// Whether the rows are put in order first: worth a launch where tiles meet the
-// adapters (not in parts, where the last launch adds them row by row) and there
-// are several; a window's rows have to be within 31-bit offsets.
+// Whether the rows are put in order first: a launch of 6 us where every row is
+// another request's (4096 rows of 4 adapters, 7168 x 2048: 181 us instead of
+// 250); where they come in order already it is lost (5474 rows of 2 adapters,
+// 1376 x 352: 42 us instead of 35), which the host cannot see.  A window's
+// rows have to be within 31-bit offsets.
 bool ordered(int64_t tokens, int64_t k, int64_t n, int adapters) {
-  return tokens > kFewRows && project_parts(tokens, k, n) == 1 && adapters > 1 &&
-         adapters < (1 << 21) && kWindow * std::max(2 * k, 2 * n) <= INT32_MAX;
+  return tokens > kFewRows && adapters > 1 && adapters < (1 << 21) && kWindow * std::max(2 * k, 2 * n) <= INT32_MAX;
 }
 
-// Workspace: v (its parts, or its halves and the order), the projection's parts.
+// Adapters of a tile of the first launch that are taken side by side: as many
+// as a tile of rows in order meets if the adapters are equally frequent.
+int shrink_slots(int64_t tokens, int adapters, bool in_order) {
+  const int64_t run = std::min<int64_t>(tokens, kWindow);
+  const int64_t meets = in_order ? 1 + (kShrinkRows * (int64_t)adapters + run - 1) / run : kShrinkRows;
+  return (int)std::min(std::min(meets, (int64_t)adapters), std::min<int64_t>(tokens, kShrinkRows));
+}
+
+// Workspace: v (its parts, or its halves), the order, the projection's parts.
 struct Workspace {
   int64_t v, order, partial;
 };
 Workspace workspace_of(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
-  const int parts = project_parts(tokens, k, n);
+  const int parts = project_parts(tokens, k, n, rank);
   const bool halves = tokens > kFewRows && parts == 1;
   return {round256(halves ? tokens * round16(rank) * 4 : tokens * rank * 4 * shrink_parts(tokens, k)),
-          halves && rank ? round256(tokens * 4) : 0, parts > 1 ? parts * tokens * n * 4 : 0};
+          tokens > kFewRows && rank ? round256(tokens * 4) : 0, parts > 1 ? parts * tokens * n * 4 : 0};
 }
 
 template <class F>
@@ -619,8 +628,8 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
   const int64_t need = lora_workspace(tokens, k, n, num_adapters ? rank : 0);
   if (need && (!workspace || workspace_bytes < need)) return NVFP4G_EINVAL;
   const hipStream_t st = (hipStream_t)stream;
-  if (((tokens + kBM - 1) / kBM) * ((n + kBN - 1) / kBN) > (int64_t)INT32_MAX) return NVFP4G_EINVAL;
-  const int T = (int)tokens, r = num_adapters ? rank : 0, split = project_parts(tokens, k, n);
+  if (((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines) > (int64_t)INT32_MAX) return NVFP4G_EINVAL;
+  const int T = (int)tokens, r = num_adapters ? rank : 0, split = project_parts(tokens, k, n, r);
   const bool few = tokens <= kFewRows, halves = !few && split == 1;
   const int parts = halves ? 1 : shrink_parts(tokens, k);
   const Workspace w = workspace_of(tokens, k, n, r);
@@ -631,9 +640,7 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
     if (order)
       hipLaunchKernelGGL(order_kernel, dim3((uint32_t)((tokens + kOrderRows - 1) / kOrderRows)), dim3(kThreads), 0, st,
                          adapter_ids, T, num_adapters, order);
-    // adapters of a tile side by side: two where the rows are in order
-    const dim3 grid((uint32_t)((T + kShrinkRows - 1) / kShrinkRows), parts,
-                    std::min(order ? 2 : std::min(T, kShrinkRows), num_adapters));
+    const dim3 grid((uint32_t)((T + kShrinkRows - 1) / kShrinkRows), parts, shrink_slots(T, num_adapters, order));
     with_ranks(rank, [&](auto nr) {
       constexpr int NR = decltype(nr)::value;
       if (halves)
@@ -649,16 +656,23 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
     if (T <= 16) launch_few<1, 1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
     else launch_few<2, 1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
   } else {
-    const uint32_t ntm = (uint32_t)((tokens + kBM - 1) / kBM), ntn = (uint32_t)((n + kBN - 1) / kBN);
+    // half as wide tiles where neither the wide ones nor parts fill the device
+    const int64_t wide = ((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines);
+    const int lines = split == 1 && wide < kCus ? kWideLines / 2 : kWideLines;
+    const uint32_t ntm = (uint32_t)((tokens + kBM - 1) / kBM), ntn = (uint32_t)((n + lines - 1) / lines);
+    auto project = [&](auto kernel, const int32_t* rows_in) {
+      hipLaunchKernelGGL(kernel, dim3(ntm * ntn, split), dim3(kThreads), 0, st, x, tokens, k, w_data, w_scale, w_amax, n,
+                         lora_b, num_adapters, r, adapter_ids, rows_in, (const uint16_t*)v, ntm, ntn, y, partial);
+    };
     if (split > 1) {
-      hipLaunchKernelGGL((many_rows_kernel<true>), dim3(ntm * ntn, split), dim3(kThreads), 0, st, x, tokens, k, w_data,
-                         w_scale, w_amax, n, lora_b, num_adapters, r, adapter_ids, order, (const uint16_t*)v, ntm, ntn, y, partial);
-      hipLaunchKernelGGL(finish_kernel, dim3((uint32_t)tokens, (uint32_t)((n + 8 * kThreads - 1) / (8 * kThreads))),
+      project(many_rows_kernel<true, 2>, nullptr);
+      hipLaunchKernelGGL(finish_kernel, dim3((uint32_t)tokens, (uint32_t)((n + 2 * kThreads - 1) / (2 * kThreads))),
                          dim3(kThreads), 0, st, partial, split, tokens, n, lora_b, alpha, num_adapters, r, adapter_ids,
                          v, parts, y);
+    } else if (lines == kWideLines) {
+      project(many_rows_kernel<false, 2>, order);
     } else {
-      hipLaunchKernelGGL((many_rows_kernel<false>), dim3(ntm * ntn), dim3(kThreads), 0, st, x, tokens, k, w_data,
-                         w_scale, w_amax, n, lora_b, num_adapters, r, adapter_ids, order, (const uint16_t*)v, ntm, ntn, y, partial);
+      project(many_rows_kernel<false, 1>, order);
     }
   }
   return hip_status();
