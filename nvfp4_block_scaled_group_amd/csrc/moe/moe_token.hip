@@ -137,13 +137,22 @@ void launch(const uint16_t* x, int64_t k, int per, const int32_t* ids, int pairs
   constexpr int NL = 2, kCols = MODE == kModeGlu ? 16 : 32;
   const int64_t ocols = MODE == kModeGlu ? n / 2 : n, experts = std::min(pairs, E);
   auto tiles = [&](int ks) { return (ocols + kCols * (kTokenWaves / ks) - 1) / (kCols * (kTokenWaves / ks)); };
-  // Waves that split the contraction: as few as leave two work-groups a CU,
-  // with the experts that the pairs can reach.
-  int ks = 1;
-  while (ks < kTokenWaves && experts * tiles(ks) < 2 * kCus) ks *= 2;
   // an expert has at most one pair of a token, or takes more passes
   const int rows = std::min((pairs + per - 1) / per, 16 * MT);
-  const TokenPlan P = token_plan(k, rows, ks, MT * NL, 0, experts * tiles(ks));
+  // Waves that split the contraction: the fewest rounds of work-groups (two a
+  // CU where LDS and registers hold them, with the experts that the pairs can
+  // reach) times steps of a wave and a start that takes about three of them.
+  // 5 tokens, 5600 x 1824, 8 of 8 experts: 32 us 4 ways, 52 not split, 45 with
+  // 8; 24 pairs of 64 experts, 2048 x 7168: 97 us not split, 131 with 8.
+  TokenPlan P{};
+  int64_t best = INT64_MAX;
+  for (int ks = 1; ks <= kTokenWaves; ks *= 2) {
+    const TokenPlan q = token_plan(k, rows, ks, MT * NL, 0, experts * tiles(ks));
+    if (q.ks != ks) break;
+    const int64_t slots = (token_waves(MT) == 4 && q.lds <= kTokenLds ? 2 : 1) * kCus;
+    const int64_t cost = (experts * tiles(ks) + slots - 1) / slots * ((int64_t)q.per * q.chunks + 3);
+    if (cost < best) best = cost, P = q;
+  }
   hipLaunchKernelGGL((token_kernel<MODE, ACT, MT, NL>), dim3((uint32_t)tiles(P.ks), (uint32_t)pairs),
                      dim3(kTokenThreads), P.lds, st, x, k, per, ids, pairs, bd, bs, ba, n, E, P, out);
 }

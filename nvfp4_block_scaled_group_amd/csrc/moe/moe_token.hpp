@@ -8,7 +8,9 @@
 // MFMA layout neighbouring lanes hold different lines, so every lane of a load
 // is a request of its own.  Hence
 //  * a lane takes 64 consecutive elements of its line a step: two 16-byte
-//    loads of codes and one of four scale bytes, two steps in flight;
+//    loads of codes and one of four scale bytes, two steps in flight; the
+//    loads share cache lines, so the codes are not streamed past the caches
+//    (8 tokens, 5568 x 1504, 32 experts: 60 us instead of 76);
 //  * the tokens' rows are staged in LDS (first loads from memory in the MFMA
 //    layout cost four times the weights' requests: 23 us instead of 12 for 8
 //    rows of a 7168 x 7168 projection);
@@ -110,8 +112,8 @@ struct StepCodes {
     const uint32_t o0 = past | (s + 1 == steps ? cut[0] : 0u), o1 = past | (s + 1 == steps ? cut[1] : 0u);
 #pragma unroll
     for (int t = 0; t < NL; ++t) {
-      codes[t][0] = __builtin_amdgcn_raw_buffer_load_b128(w.data[t], w.doff | o0, s * (kStepK / 2), kLoadStream);
-      codes[t][1] = __builtin_amdgcn_raw_buffer_load_b128(w.data[t], (w.doff + 16) | o1, s * (kStepK / 2), kLoadStream);
+      codes[t][0] = __builtin_amdgcn_raw_buffer_load_b128(w.data[t], w.doff | o0, s * (kStepK / 2), 0);
+      codes[t][1] = __builtin_amdgcn_raw_buffer_load_b128(w.data[t], (w.doff + 16) | o1, s * (kStepK / 2), 0);
       if (w.dwords)
         scales[t] = __builtin_amdgcn_raw_buffer_load_b32(w.scale[t], w.soff | o0, s * (kStepK / 16), 0);
       else
