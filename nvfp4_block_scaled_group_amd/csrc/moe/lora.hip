@@ -154,27 +154,38 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const uint16_t* 
   }
 }
 
-// sum_r b[r] * v[r] in fp32; the loads of 32 ranks are in flight together.
-__device__ __forceinline__ float rank_dot(const uint16_t* b, const float* v, int rank) {
-  float d = 0.0f;
-  for (int i = 0; i < rank; i += 32) {
+// Ranks i .. i + 31 of a line of B (past the rank not read, and not used).
+__device__ __forceinline__ void rank_load(const uint16_t* b, int i, int rank, u32x4 (&q)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (i + 8 * j < rank) q[j] = *reinterpret_cast<const u32x4*>(b + i + 8 * j);
+}
+
+// d + the sum of up to 32 ranks q[r] * v[r], in their order, in fp32.
+__device__ __forceinline__ float rank_sum(const u32x4 (&q)[4], const float* v, int ranks, float d) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (8 * j >= ranks) break;
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(v + 8 * j), hi = *reinterpret_cast<const f32x4*>(v + 8 * j + 4);
+    d = __builtin_fmaf(bf16lo(q[j][0]), lo[0], d);
+    d = __builtin_fmaf(bf16hi(q[j][0]), lo[1], d);
+    d = __builtin_fmaf(bf16lo(q[j][1]), lo[2], d);
+    d = __builtin_fmaf(bf16hi(q[j][1]), lo[3], d);
+    d = __builtin_fmaf(bf16lo(q[j][2]), hi[0], d);
+    d = __builtin_fmaf(bf16hi(q[j][2]), hi[1], d);
+    d = __builtin_fmaf(bf16lo(q[j][3]), hi[2], d);
+    d = __builtin_fmaf(bf16hi(q[j][3]), hi[3], d);
+  }
+  return d;
+}
+
+// d + the ranks from `from` (a multiple of 32) on of a line of B times v; the
+// loads of 32 ranks are in flight together.
+__device__ __forceinline__ float rank_dot(const uint16_t* b, const float* v, int from, int rank, float d) {
+  for (int i = from; i < rank; i += 32) {
     u32x4 q[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i + 8 * j < rank) q[j] = *reinterpret_cast<const u32x4*>(b + i + 8 * j);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (i + 8 * j >= rank) break;
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(v + i + 8 * j), hi = *reinterpret_cast<const f32x4*>(v + i + 8 * j + 4);
-      d = __builtin_fmaf(bf16lo(q[j][0]), lo[0], d);
-      d = __builtin_fmaf(bf16hi(q[j][0]), lo[1], d);
-      d = __builtin_fmaf(bf16lo(q[j][1]), lo[2], d);
-      d = __builtin_fmaf(bf16hi(q[j][1]), lo[3], d);
-      d = __builtin_fmaf(bf16lo(q[j][2]), hi[0], d);
-      d = __builtin_fmaf(bf16hi(q[j][2]), hi[1], d);
-      d = __builtin_fmaf(bf16lo(q[j][3]), hi[2], d);
-      d = __builtin_fmaf(bf16hi(q[j][3]), hi[3], d);
-    }
+    rank_load(b, i, rank, q);
+    d = rank_sum(q, v + i, rank - i, d);
   }
   return d;
 }
@@ -189,7 +200,10 @@ __device__ __forceinline__ float row_v(const float* v, int parts, int64_t tokens
 
 // ------------------------------------------------------ projection, few rows
 
-template <int MT, int NL>
+// Wave part p of a tile finishes the outputs whose number (token tile, row of
+// four) is p, p + ks, ...  What its first one needs of B is loaded before the
+// weights, and v of all rows beside them.
+template <int MT>
 __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void few_rows_kernel(
     const uint16_t* __restrict__ x, int tokens, int64_t k, const uint8_t* __restrict__ w_data,
     const uint8_t* __restrict__ w_scale, const float* __restrict__ w_amax, int64_t n,
@@ -198,40 +212,41 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void few_rows_kerne
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = uni((int32_t)(threadIdx.x >> 6));
   const int groups = kTokenWaves / P.ks, group = wave / P.ks, part = wave % P.ks;
-  const int64_t col0 = ((int64_t)uni(blockIdx.x) * groups + group) * (NL * 16);
-  TileLines<kModeLinear, NL> W;
+  const int64_t col0 = ((int64_t)uni(blockIdx.x) * groups + group) * 16, col = col0 + (lane & 15);
+  auto row_of = [&](int item) { return 16 * (item >> 2) + 4 * (lane >> 4) + (item & 3); };
+  auto adapter_of = [&](int t) { return adapters && t < tokens && col0 < n ? ids[t] : -1; };
+  auto line_of = [&](int a) { return lora_b + ((int64_t)a * n + col) * rank; };
+  u32x4 first[4];
+  const int first_a = adapter_of(row_of(part));
+  if ((uint32_t)first_a < (uint32_t)adapters) rank_load(line_of(first_a), 0, rank, first);
+  const float factor = w_amax[min<int64_t>(col, n - 1)];
+  TileLines<kModeLinear, 1> W;
   W.init(w_data, w_scale, 0, col0, n, k, lane);
-  f32x4 acc[MT][NL];
-  token_multiply<MT, NL>(W, P, x, k, tokens, wave, lane, lds, [](int i) { return (int64_t)i; }, acc);
-  f32x4* red = reinterpret_cast<f32x4*>(lds);
-  float* lv = reinterpret_cast<float*>(lds + kTokenWaves * MT * NL * 1024);  // [tokens][rank]: alpha * v of every row
-  __syncthreads();
-  for (int i = threadIdx.x; i < tokens * rank; i += kTokenThreads) {
-    const int a = ids[i / rank];
-    lv[i] = (uint32_t)a < (uint32_t)adapters ? row_v(v, parts, tokens, i / rank, rank, i % rank, a, alpha) : 0.0f;
-  }
-  join_waves<MT, NL>(acc, red, wave, lane);
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    if (mt * 16 >= tokens) continue;
-#pragma unroll
-    for (int c = 0; c < NL; ++c) {
-      if ((mt * NL + c) % P.ks != part || col0 + 16 * c >= n) continue;
-      const int64_t col = col0 + 16 * c + (lane & 15);
-      const f32x4 sum = joined<MT, NL>(red, group, P.ks, mt, c, lane);
-      const float s = w_amax[col] / 2688.0f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int t = mt * 16 + 4 * (lane >> 4) + q;
-        if (t >= tokens) continue;
-        float r = sum[q] * s;
-        const int a = adapters ? ids[t] : -1;
-        if ((uint32_t)a < (uint32_t)adapters) {
-          r += rank_dot(lora_b + ((int64_t)a * n + col) * rank, lv + t * rank, rank);
-        }
-        y[(int64_t)t * n + col] = to_bf16(r);
-      }
+  f32x4 acc[MT][1];
+  float* lv = reinterpret_cast<float*>(lds + P.shared);  // [tokens][rank]: alpha * v of every row
+  token_multiply<MT, 1>(W, P, x, k, tokens, wave, lane, lds, [](int i) { return (int64_t)i; }, acc, [&] {
+    for (int i = threadIdx.x; i < tokens * rank; i += kTokenThreads) {
+      const int a = ids[i / rank];
+      lv[i] = (uint32_t)a < (uint32_t)adapters ? row_v(v, parts, tokens, i / rank, rank, i % rank, a, alpha) : 0.0f;
     }
+  });
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+  join_waves<MT, 1>(acc, red, wave, lane);
+  if (col0 >= n) return;
+  for (int item = part; item < 4 * MT; item += P.ks) {
+    const int t = row_of(item);
+    if (t >= tokens) continue;
+    const float* f = reinterpret_cast<const float*>(red + (group * P.ks * MT + (item >> 2)) * 64 + lane) + (item & 3);
+    float r = f[0];
+    for (int w = 1; w < P.ks; ++w) r += f[w * MT * 64 * 4];
+    r *= factor / 2688.0f;
+    const int a = item == part ? first_a : adapter_of(t);
+    if ((uint32_t)a < (uint32_t)adapters) {
+      const float* l = lv + t * rank;
+      r += item == part ? rank_dot(line_of(a), l, 32, rank, rank_sum(first, l, rank, 0.0f))
+                        : rank_dot(line_of(a), l, 0, rank, 0.0f);
+    }
+    y[(int64_t)t * n + col] = to_bf16(r);
   }
 }
 
@@ -521,8 +536,8 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(const float* __restric
   for (int p = 1; p < parts; ++p) s += *reinterpret_cast<const f32x2*>(partial + p * count + i);
   if (adapted) {
     const uint16_t* b = lora_b + ((int64_t)a * n + c) * rank;
-    s[0] += rank_dot(b, lv, rank);
-    s[1] += rank_dot(b + rank, lv, rank);
+    s[0] += rank_dot(b, lv, 0, rank, 0.0f);
+    s[1] += rank_dot(b + rank, lv, 0, rank, 0.0f);
   }
   *reinterpret_cast<uint32_t*>(y + i) = pack_bf16(s[0], s[1]);
 }
@@ -588,17 +603,19 @@ void with_ranks(int rank, F f) {
   else f(std::integral_constant<int, 8>());
 }
 
-template <int MT, int NL>
+template <int MT>
 void launch_few(const uint16_t* x, int tokens, int64_t k, const uint8_t* wd, const uint8_t* ws, const float* wa,
                 int64_t n, const uint16_t* b, const float* alpha, int adapters, int rank, const int32_t* ids,
                 const float* v, int parts, uint16_t* y, hipStream_t st) {
+  // Waves that split the contraction: as few as give most CUs a work-group (8
+  // rows, 7168 x 7168: 21 us 4 ways, 25 with 2, 34 not split; 17 rows: 25 us 4
+  // ways, 35 with 8).
+  auto tiles = [&](int ks) { return (n + 16 * (kTokenWaves / ks) - 1) / (16 * (kTokenWaves / ks)); };
   int ks = 1;
-  while (ks < 8 && (n + 16 * NL * (8 / ks) - 1) / (16 * NL * (8 / ks)) < 200) ks *= 2;
-  const TokenPlan P = token_plan(k, tokens, ks, MT * NL, adapters ? (int64_t)tokens * rank * 4 : 0,
-                                 (n + 16 * NL * (8 / ks) - 1) / (16 * NL * (8 / ks)));
-  const int cols = NL * 16 * (kTokenWaves / P.ks);
-  hipLaunchKernelGGL((few_rows_kernel<MT, NL>), dim3((uint32_t)((n + cols - 1) / cols)), dim3(kTokenThreads), P.lds, st, x,
-                     tokens, k, wd, ws, wa, n, b, alpha, adapters, adapters ? rank : 0, ids, v, parts, P, y);
+  while (ks < kTokenWaves && tiles(ks) < 200) ks *= 2;
+  const TokenPlan P = token_plan(k, tokens, ks, MT, adapters ? (int64_t)tokens * rank * 4 : 0, tiles(ks));
+  hipLaunchKernelGGL((few_rows_kernel<MT>), dim3((uint32_t)tiles(P.ks)), dim3(kTokenThreads), P.lds, st, x, tokens, k, wd,
+                     ws, wa, n, b, alpha, adapters, adapters ? rank : 0, ids, v, parts, P, y);
 }
 
 }  // namespace
@@ -653,8 +670,8 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
   }
   if (few) {
     // one 16-line tile a work-group: the most work-groups a projection gives
-    if (T <= 16) launch_few<1, 1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
-    else launch_few<2, 1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
+    if (T <= 16) launch_few<1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
+    else launch_few<2>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
   } else {
     // half as wide tiles where neither the wide ones nor parts fill the device
     const int64_t wide = ((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines);

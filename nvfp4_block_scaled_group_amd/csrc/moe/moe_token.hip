@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void token_kernel(
     if (first) __syncthreads();  // the last pass is done with the staged rows and the joined sums
     const int rows = min(cnt - first, P.rows);
     token_multiply<MT, NL>(W, P, x, k, rows, wave, lane, xlds,
-                           [&](int i) { return (int64_t)(pair_at(first + i) / per); }, acc);
+                           [&](int i) { return (int64_t)(pair_at(first + i) / per); }, acc, [] {});
     if (P.ks > 1) join_waves<MT, NL>(acc, red, wave, lane);
     // each wave finishes its share: with split waves the tiles whose number
     // is its part's

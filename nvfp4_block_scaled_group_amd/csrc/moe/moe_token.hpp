@@ -49,16 +49,17 @@ struct TokenPlan {
   int32_t chunks;
   int32_t rows;    // rows of a pass at most
   int32_t pitch;   // bytes of a staged row
+  int32_t shared;  // bytes of the staged rows, then of the waves' sums
   int32_t lds;     // bytes of dynamic LDS
 };
 
 // rows: the most rows of a pass; ks: waves that should split the contraction
 // (fewer where their staged rows would not fit or a wave would have no step:
 // 23 tokens, 384 elements in two steps, 4 ways 24 us, 1 way 13); tiles: MFMA
-// tiles a wave joins through LDS; extra: bytes the epilogue wants beside them;
+// tiles a wave joins through LDS; extra: bytes the caller wants beside them;
 // groups: the work-groups of the launch.
 inline TokenPlan token_plan(int64_t k, int rows, int ks, int tiles, int64_t extra, int64_t groups) {
-  const int64_t limit = rows <= 16 && groups > kCus ? kTokenLds : 2 * kTokenLds, steps = (k + kStepK - 1) / kStepK;
+  const int64_t limit = (rows <= 16 && groups > kCus ? kTokenLds : 2 * kTokenLds) - extra, steps = (k + kStepK - 1) / kStepK;
   while (ks > 1 && (rows * (ks * 4 * kStepK + 16) > limit || 2 * ks > steps + 1)) ks /= 2;
   const int64_t want = ((steps + ks - 1) / ks + 1) / 2 * 2;
   const int64_t room = (limit / rows - 16) / (2 * kStepK) / ks / 2 * 2;
@@ -68,8 +69,9 @@ inline TokenPlan token_plan(int64_t k, int rows, int ks, int tiles, int64_t extr
   p.per = (int32_t)(want < room ? want : room);
   p.chunks = (int32_t)((steps + (int64_t)p.per * ks - 1) / ((int64_t)p.per * ks));
   p.pitch = p.per * ks * 2 * kStepK + 16;
-  const int64_t x = (int64_t)rows * p.pitch, join = kTokenWaves * tiles * 1024 + extra;
-  p.lds = (int32_t)(x > join ? x : join);
+  const int64_t x = (int64_t)rows * p.pitch, join = kTokenWaves * tiles * 1024;
+  p.shared = (int32_t)((x > join ? x : join) + 15) / 16 * 16;
+  p.lds = (int32_t)(p.shared + extra);
   return p;
 }
 
@@ -126,12 +128,13 @@ struct StepCodes {
 
 // acc[m][t] = the rows of token tile m times the lines of tile t, over this
 // wave's part of the contraction.  row_of(i): x's row of the i-th of `rows`
-// rows.  All threads of the work-group; xlds is free again on return only
-// after the caller's next barrier.
-template <int MT, int NL, class W, class RowOf>
+// rows; beside(): work of the caller while the first x is on its way.  All
+// threads of the work-group; xlds is free again on return only after the
+// caller's next barrier.
+template <int MT, int NL, class W, class RowOf, class Beside>
 __device__ __forceinline__ void token_multiply(const W& w, const TokenPlan& P, const uint16_t* x, int64_t k,
                                                int rows, int wave, int lane, uint8_t* xlds, RowOf row_of,
-                                               f32x4 (&acc)[MT][NL]) {
+                                               f32x4 (&acc)[MT][NL], Beside beside) {
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -183,6 +186,7 @@ __device__ __forceinline__ void token_multiply(const W& w, const TokenPlan& P, c
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xs, (lds_ptr_t)(xlds + r * P.pitch + 1024 * p), 16, 16 * lane + 1024 * p, 0, 0,
                                                0);
     }
+    if (c == 0) beside();
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
     const uint8_t* xs = xlds + part * P.per * (2 * kStepK);
