@@ -10,8 +10,15 @@
 //   few rows (at most 32)  the weight is read once and bounds it; every
 //                          16-line tile adds its rows' B_a v in fp32;
 //   more rows              128 x 256 tiles, MFMA 32x32x16; each adapter present
-//                          in the tile adds rank/16 MFMA steps of v B_a^T to
-//                          the scaled accumulators, rows of other adapters 0.
+//                          in 32 rows of the tile adds rank/16 MFMA steps of
+//                          v B_a^T to its own rows of the scaled accumulators;
+//                          where tiles are few, parts of the contraction, and
+//                          a last launch that adds them and the adapters.
+// 32 rows are one pass over the weight in the first form: 17 rows of 7168 x 7168
+// take 24 us, 32 rows 28; in the second 36 and 37.
+// Measured: 8 rows, 7168 x 7168, 6 adapters of rank 16: 19 us (1.6 TB/s; the
+// latency of a wave's seven steps after the first launch's 5 us); 4095 rows,
+// 7168 x 2048, 8 adapters of rank 32: 162 us (0.75 PFLOP/s; MFMA and decode).
 // v is kept in fp32 (few rows), or as two bf16 halves, v = hi + lo, which
 // leaves it 16 significant bits: the adapter's part then has the precision of
 // the bf16 result to spare.
@@ -74,7 +81,8 @@ __global__ __launch_bounds__(kThreads) void order_kernel(const int32_t* __restri
 // adapter are not written.  The waves take a share of the part each and join
 // in LDS.  A step's loads are in flight together; parts and adapters are
 // work-groups of their own because the chain of steps, not the bytes, is what
-// takes the time.
+// takes the time: 5 us for 8 rows of 7168, 16 for 4095 rows of 2048 (two
+// bytes an element of x: 1.0 TB/s).
 template <int NR, bool HALVES>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const uint16_t* __restrict__ x, int tokens, int64_t k,
                                                           const uint16_t* __restrict__ lora_a,
@@ -200,6 +208,8 @@ __device__ __forceinline__ float row_v(const float* v, int parts, int64_t tokens
 
 // ------------------------------------------------------ projection, few rows
 
+// The weight is read once (15 us for 7168 x 7168 and 8 rows, 1.9 TB/s: a wave has
+// seven steps of it, and the start and the end are half of the time).
 // Wave part p of a tile finishes the outputs whose number (token tile, row of
 // four) is p, p + ks, ...  What its first one needs of B is loaded before the
 // weights, and v of all rows beside them.
@@ -258,15 +268,16 @@ constexpr uint32_t kXBytes = kBM * kBK * 2;         // 16 KB: 128 bytes a row
 template <int IN>
 constexpr uint32_t kStageOf = kXBytes + 128 * IN * kBK / 2;  // and 32 bytes a line: 24 KB, 20 KB
 
-
 // Tile of 128 rows x 128 kIN lines, or one of gridDim.y parts of its contraction
 // (SPLIT: fp32 sums to partial[blockIdx.y], for finish_kernel, which adds the
-// adapters).  Copies run one step ahead; with SPLIT, where a CU may
-// have one work-group alone and the latency sets the pace (2.3 us a step), two
-// (with many tiles the third stage costs 2%).  Wave w takes all rows and 32 kIN lines,
-// so no weight is decoded twice in a work-group.  Element granules (8 of x,
-// 16 bytes) and code granules are XOR-placed in LDS so that fragment reads of
-// 32 consecutive rows or lines spread over the banks.  Rows past the last and
+// adapters).  Copies run one step ahead; with SPLIT, where a CU may have one
+// work-group alone and the latency sets the pace (2.3 us a step), two (with
+// many tiles the third stage costs 2%).  Wave w takes all rows and 32 kIN lines,
+// so no weight is decoded twice in a work-group.  What bounds it is the MFMAs
+// and the decode between them: 4095 rows, 7168 x 2048 in 150 us, 0.8 PFLOP/s.
+// Element granules (8 of x, 16 bytes) and code granules are XOR-placed in LDS so
+// that fragment reads of 32 consecutive rows or lines spread over the banks.
+// Rows past the last and
 // elements past k read as zero (the weights' codes there, the next line's, are
 // finite and meet zeros).
 template <bool SPLIT, int kIN>
@@ -673,9 +684,11 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
     if (T <= 16) launch_few<1>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
     else launch_few<2>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
   } else {
-    // half as wide tiles where neither the wide ones nor parts fill the device
+    // Half as wide tiles where neither parts nor the wide ones, two a CU, fill
+    // the device: 1500 rows, 7168 x 4096 (336 wide tiles) 129 us wide, 123
+    // narrow; 2048 rows, 7168 x 2048 (448) 85 and 96; 700 rows in parts stay wide.
     const int64_t wide = ((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines);
-    const int lines = split == 1 && wide < kCus ? kWideLines / 2 : kWideLines;
+    const int lines = split == 1 && wide < 3 * kCus / 2 ? kWideLines / 2 : kWideLines;
     const uint32_t ntm = (uint32_t)((tokens + kBM - 1) / kBM), ntn = (uint32_t)((n + lines - 1) / lines);
     auto project = [&](auto kernel, const int32_t* rows_in) {
       hipLaunchKernelGGL(kernel, dim3(ntm * ntn, split), dim3(kThreads), 0, st, x, tokens, k, w_data, w_scale, w_amax, n,
