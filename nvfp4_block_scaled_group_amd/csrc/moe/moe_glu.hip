@@ -18,6 +18,12 @@
 // elements in the same lane (its first two MFMA columns are gate lines, the
 // other two the matching up lines): the activation and the product need no
 // exchange, and neither g nor u goes through memory.
+//
+// What bounds it: at large sizes the power of MFMAs and decode together
+// (forward, 65536 rows, 7168 x 2 x 2048: 3.0 ms, 1.28 PFLOP/s at a clock of
+// 1.6 GHz, MFMAs busy 68% of it); with few steps a tile the start and the
+// epilogue too (backward, 16384 rows of 64 experts, 2048 x 1040: 113 us, 0.62
+// PFLOP/s; the same with 1024 columns, a whole number of tiles, 94 us).
 #include <algorithm>
 
 #include "moe_common.hpp"

@@ -9,8 +9,8 @@
 // ordered finite double, so that one maximum or minimum instruction compares
 // both.  Each lane sorts its patterns once; then topk rounds take the maximum
 // of the lanes' heads (log2 LANES exchanges) and the lane that had it drops its
-// head.  32768 x 256, 8 chosen: 28 us with one token a wave and the keys
-// searched every round.
+// head.  32768 x 256, 8 chosen, sigmoid: 16 us (2.3 TB/s); 28 us with one token a
+// wave and the keys searched every round.
 //
 // Plan.  A stable counting sort of the pairs by expert without atomics that
 // decide an order: a wave ranks 64 pairs at a time by matching expert
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const T* __restrict__ l
 //   sigmoid            dl_j = g_j s_j (1 - s_j)
 //   sigmoid normalised dl_j = (g_j - sum_i q_i g_i) q_j (1 - s_j)
 // The choices' values are scattered into the token's row in LDS and the row
-// is written once, densely.
+// is written once, densely: 8191 x 64 of bf16 in 4.5 us, a launch.
 template <class T, int VPL>
 __global__ __launch_bounds__(kThreads) void route_bwd_kernel(const T* __restrict__ logits, int64_t tokens, int E,
                                                              int topk, const int32_t* __restrict__ ids,
@@ -307,7 +307,9 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(const T* __restrict
 // ------------------------------------------------------------------- plan
 
 constexpr int kPlanSteps = 4;         // steps of 64 pairs a wave ranks in the split form
-constexpr int kSmallSteps = 4;        // the one-launch form: steps of 64 pairs a wave keeps in registers (at 11 it took 20 us, the split form 15), experts
+// The one-launch form: steps of 64 pairs a wave keeps in registers, experts.
+// With more steps the three launches are faster (at 11: 20 us and 15).
+constexpr int kSmallSteps = 4;
 constexpr int kSmallExperts = 512;
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallWaves = kSmallThreads / 64;
@@ -399,7 +401,8 @@ __device__ __forceinline__ void write_pair(int64_t p, int row, int64_t cap, int3
   if (fits) src[row] = (int32_t)p;
 }
 
-// Few pairs: one work-group does it all (a launch costs more than the work).
+// Few pairs: one work-group does it all (a launch costs more than the work):
+// 5.6 us for 8 pairs.
 __global__ __launch_bounds__(kSmallThreads) void plan_small_kernel(const int32_t* __restrict__ ids, int pairs, int E,
                                                                    int ebits, int64_t cap, int32_t* offs,
                                                                    int32_t* counts, int32_t* rows, int32_t* src,

@@ -11,9 +11,9 @@
 //    loads of codes and one of four scale bytes, two steps in flight; the
 //    loads share cache lines, so the codes are not streamed past the caches
 //    (8 tokens, 5568 x 1504, 32 experts: 60 us instead of 76);
-//  * the tokens' rows are staged in LDS (first loads from memory in the MFMA
-//    layout cost four times the weights' requests: 23 us instead of 12 for 8
-//    rows of a 7168 x 7168 projection);
+//  * the tokens' rows are staged in LDS (loads in the MFMA layout from memory
+//    cost four times the weights' requests: 25 us instead of 22 for 8 rows of a
+//    7168 x 7168 projection with adapters);
 //  * the eight waves of a work-group split the contraction KS ways and the
 //    lines 8 / KS ways, and join their sums in LDS in a fixed order.
 #pragma once
