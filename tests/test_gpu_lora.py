@@ -113,3 +113,22 @@ def test_offsets_past_32_bits():
     want, err = expect(w, v, a, b, [0] * len(rows), alpha.astype(np.float64), K, r)
     R.check(y[rows], want, err, "y")
     assert float(y.float().abs().sum()) == float(y[rows].float().abs().sum())
+
+
+FORMS = [  # T, N, K, rank, adapters
+    (1030, 11024, 64, 24, 9),    # whole wide tiles, over the end of a window of row order
+    (2100, 48, 96, 16, 50),      # half as wide tiles, three windows
+    (100, 48, 4160, 40, 28),     # parts of the contraction, rows in order, an adapter in every other row
+    (140, 272, 1312, 128, 3),
+    (32, 1040, 4128, 72, 32),    # every row of the first form, more than one chunk of x, ranks past one load
+]
+
+
+@pytest.mark.parametrize("T,N,K,r,A", FORMS)
+def test_lora_forms(T, N, K, r, A):
+    log(f"lora T={T} N={N} K={K} r={r} A={A}")
+    rng, w, xt, x, at, a, bt, b, alpha = make(T + K + 1, T, N, K, r, A)
+    ids = rng.integers(-1, A, T)
+    got = call(w, xt, at, bt, ids, alpha, T, N, K, r)
+    want, err = expect(w, x, a, b, ids, alpha.astype(np.float64), K, r)
+    R.check(got, want, err, "y")
