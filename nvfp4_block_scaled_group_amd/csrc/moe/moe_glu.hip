@@ -22,8 +22,8 @@
 // What bounds it: at large sizes the power of MFMAs and decode together
 // (forward, 65536 rows, 7168 x 2 x 2048: 3.0 ms, 1.28 PFLOP/s at a clock of
 // 1.6 GHz, MFMAs busy 68% of it); with few steps a tile the start and the
-// epilogue too (backward, 16384 rows of 64 experts, 2048 x 1040: 113 us, 0.62
-// PFLOP/s; the same with 1024 columns, a whole number of tiles, 94 us).
+// epilogue too (backward, 16384 rows of 64 experts, 2048 x 1040: 111 to 115 us, 0.6
+// PFLOP/s; the same with 1024 columns, a whole number of tiles, 91 us).
 #include <algorithm>
 
 #include "moe_common.hpp"
@@ -431,13 +431,15 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
       const uint32_t j0 = wn * (kCols / 2) + in0 * 32;
       const bool write = j0 + c < cols;
       const int64_t at0 = (row0 + wm * (kWM * 32) + im * 32 + srow) * 2 * f + col0 + j0 + c;
+      // through the caches: rows of 2f columns start inside a cache line (past
+      // them 1 to 4% slower); two blocks' loads at once were 8% slower
       u32x4 gq[kPasses], uq[kPasses];
 #pragma unroll
       for (int r = 0; r < kPasses; ++r) {
         gq[r] = uq[r] = u32x4{0, 0, 0, 0};
         if (write) {
-          gq[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(gu + at0 + 2 * kRows * r * f));
-          uq[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(gu + at0 + 2 * kRows * r * f + f));
+          gq[r] = *reinterpret_cast<const u32x4*>(gu + at0 + 2 * kRows * r * f);
+          uq[r] = *reinterpret_cast<const u32x4*>(gu + at0 + 2 * kRows * r * f + f);
         }
       }
 #pragma unroll
