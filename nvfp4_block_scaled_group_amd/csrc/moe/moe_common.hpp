@@ -72,6 +72,16 @@ __device__ __forceinline__ float act_logistic(float g, float* dv) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
 }
 
+// Work-groups of kThreads in a line.  A dimension of a launch holds fewer than
+// 2^32 threads (past that the number wraps: with 2^24 + 2^20 work-groups 2^20
+// ran, and the call succeeded), so more than 2^23 take a second dimension.  Its
+// last row may hold work-groups past the last one asked for.
+inline dim3 line_grid(uint32_t groups) {
+  constexpr uint32_t kLine = 1u << 23;
+  return groups <= kLine ? dim3(groups) : dim3(kLine, (groups - 1) / kLine + 1);
+}
+__device__ __forceinline__ uint32_t line_index() { return uni(blockIdx.y * gridDim.x + blockIdx.x); }
+
 inline bool valid_type(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
 
 }  // namespace moe

@@ -72,7 +72,8 @@ __device__ __forceinline__ void zero_padding(int64_t piece, int64_t width, const
 }
 
 // Dispatch.  Work-groups 0 .. units/4-1: a wave takes a token and `span`
-// columns of it; the others zero the padding among kPadRows rows.
+// columns of it; the others zero the padding among kPadRows rows (those past
+// the last row find none).
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(const uint16_t* __restrict__ x, int64_t tokens,
                                                             int64_t width, int topk, int32_t span, int32_t spans,
                                                             const int32_t* __restrict__ rows,
@@ -80,12 +81,13 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(const uint16_t* __re
                                                             const int32_t* __restrict__ offs, int E, int64_t cap,
                                                             const float* __restrict__ weights, uint32_t token_groups,
                                                             uint16_t* __restrict__ out) {
-  if (blockIdx.x >= token_groups) {
-    zero_padding(blockIdx.x - token_groups, width, src, offs[E - 1], cap, out);
+  const uint32_t group = line_index();
+  if (group >= token_groups) {
+    zero_padding(group - token_groups, width, src, offs[E - 1], cap, out);
     return;
   }
   const int lane = threadIdx.x & 63;
-  const int64_t unit = (int64_t)uni(blockIdx.x) * (kThreads / 64) + uni((uint32_t)(threadIdx.x >> 6));
+  const int64_t unit = (int64_t)group * (kThreads / 64) + uni((uint32_t)(threadIdx.x >> 6));
   const int64_t t = unit / spans;
   if (t >= tokens) return;
   const int64_t c0 = (unit - t * spans) * span, c1 = min<int64_t>(c0 + span, width);
@@ -123,12 +125,13 @@ __global__ __launch_bounds__(kThreads) void dispatch_dot_kernel(const uint16_t* 
                                                                 uint16_t* __restrict__ out,
                                                                 float* __restrict__ dweights) {
   __shared__ float part[kThreads / 64][KMAX];
-  if (blockIdx.x >= token_groups) {
-    zero_padding(blockIdx.x - token_groups, width, src, offs[E - 1], cap, out);
+  const uint32_t group = line_index();
+  if (group >= token_groups) {
+    zero_padding(group - token_groups, width, src, offs[E - 1], cap, out);
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = uni(blockIdx.x);
+  const int64_t t = group;
   float acc[KMAX], w[KMAX];
   int64_t r[KMAX];
 #pragma unroll
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const void* __restric
                                                            const float* __restrict__ weights,
                                                            uint16_t* __restrict__ out) {
   const int lane = threadIdx.x & 63;
-  const int64_t unit = (int64_t)uni(blockIdx.x) * (kThreads / 64) + uni((uint32_t)(threadIdx.x >> 6));
+  const int64_t unit = (int64_t)line_index() * (kThreads / 64) + uni((uint32_t)(threadIdx.x >> 6));
   const int64_t t = unit / pieces, c = (unit - t * pieces) * kRowCols + lane * kLaneCols;
   if (t >= tokens) return;
   int64_t r[KMAX];
@@ -260,14 +263,15 @@ int moe_dispatch(const uint16_t* x, int64_t tokens, int64_t width, int32_t topk,
   if (y && dweights) {
     const uint32_t groups = (uint32_t)tokens;
     if (groups + tiles == 0) return NVFP4G_OK;
+    const dim3 grid = line_grid(groups + tiles);
     with_choices(topk, [&](auto v) {
       constexpr int KMAX = decltype(v)::value;
       if (y_type == MOE_F32)
-        hipLaunchKernelGGL((dispatch_dot_kernel<true, KMAX>), dim3(groups + tiles), dim3(kThreads), 0, st, x, tokens,
-                           width, topk, rows, src, offs, num_experts, m_capacity, weights, y, groups, out, dweights);
+        hipLaunchKernelGGL((dispatch_dot_kernel<true, KMAX>), grid, dim3(kThreads), 0, st, x, tokens, width,
+                           topk, rows, src, offs, num_experts, m_capacity, weights, y, groups, out, dweights);
       else
-        hipLaunchKernelGGL((dispatch_dot_kernel<false, KMAX>), dim3(groups + tiles), dim3(kThreads), 0, st, x, tokens,
-                           width, topk, rows, src, offs, num_experts, m_capacity, weights, y, groups, out, dweights);
+        hipLaunchKernelGGL((dispatch_dot_kernel<false, KMAX>), grid, dim3(kThreads), 0, st, x, tokens, width,
+                           topk, rows, src, offs, num_experts, m_capacity, weights, y, groups, out, dweights);
     });
     return hip_status();
   }
@@ -276,8 +280,8 @@ int moe_dispatch(const uint16_t* x, int64_t tokens, int64_t width, int32_t topk,
   if (want + tiles > (int64_t)INT32_MAX) return NVFP4G_EINVAL;
   const uint32_t groups = (uint32_t)want;
   if (groups + tiles == 0) return NVFP4G_OK;
-  hipLaunchKernelGGL(dispatch_kernel, dim3(groups + tiles), dim3(kThreads), 0, st, x, tokens, width, topk, span, spans,
-                     rows, src, offs, num_experts, m_capacity, weights, groups, out);
+  hipLaunchKernelGGL(dispatch_kernel, line_grid(groups + tiles), dim3(kThreads), 0, st, x, tokens, width, topk, span,
+                     spans, rows, src, offs, num_experts, m_capacity, weights, groups, out);
   return hip_status();
 }
 
@@ -291,7 +295,7 @@ int moe_combine(const void* y, int32_t y_type, int64_t m_capacity, int64_t token
   if (!aligned(y, 16) || !aligned(out, 16) || !aligned(rows, 4) || !aligned(weights, 4)) return NVFP4G_EALIGN;
   const int32_t pieces = (int32_t)((width + kRowCols - 1) / kRowCols);
   if ((tokens * pieces + 3) / 4 > (int64_t)INT32_MAX) return NVFP4G_EINVAL;
-  const dim3 grid((uint32_t)((tokens * pieces + 3) / 4));
+  const dim3 grid = line_grid((uint32_t)((tokens * pieces + 3) / 4));
   with_choices(topk, [&](auto v) {
     constexpr int KMAX = decltype(v)::value;
     if (y_type == MOE_F32)

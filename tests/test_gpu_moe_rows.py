@@ -200,3 +200,43 @@ def test_another_stream():
     moe.moe_combine(out, rows, back, stream=s)
     s.synchronize()
     assert torch.equal(back, x)
+
+
+def test_gradient_of_more_than_2_to_24_work_groups():
+    """The most tokens there may be, one choice each, and as many rows."""
+    T, H = moe.MAX_PAIRS, 16
+    x = torch.ones((T, H), dtype=torch.bfloat16, device="cuda:0")
+    y = torch.full((T, H), 0.5, dtype=torch.bfloat16, device="cuda:0")
+    rows = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda:0").view(T, 1)   # in reverse
+    rows[T - 7] = -1                                                                     # row 6 is padding
+    src = (T - 1 - torch.arange(T, dtype=torch.int32, device="cuda:0")).contiguous()
+    src[6] = -1
+    x[T - 1] = 3.0
+    offs = torch.tensor([T], dtype=torch.int32, device="cuda:0")
+    w = torch.full((T, 1), 2.0, device="cuda:0")
+    out = torch.full((T, H), 9.0, dtype=torch.bfloat16, device="cuda:0")
+    dw = torch.full((T, 1), 9.0, device="cuda:0")
+    moe.moe_dispatch(x, rows, src, offs, out, weights=w, y=y, dweights=dw)
+    torch.cuda.synchronize()
+    want = torch.full((T, H), 2.0, dtype=torch.bfloat16, device="cuda:0")
+    want[0], want[6] = 6.0, 0.0
+    assert torch.equal(out, want)
+    want = torch.full((T, 1), 8.0, device="cuda:0")
+    want[T - 1], want[T - 7] = 24.0, 0.0
+    assert torch.equal(dw, want)
+
+
+def test_combine_of_more_than_2_to_24_work_groups():
+    """2^24 tokens of four pieces each: 51 GB of output, most of it zeros."""
+    T, H, cap = moe.MAX_PAIRS, 1552, 128
+    y = torch.randn((cap, H), device="cuda:0").to(torch.bfloat16)
+    rows = torch.full((T, 1), -1, dtype=torch.int32, device="cuda:0")
+    some = [0, 1, T // 2, T - 2, T - 1]
+    rows[some, 0] = torch.tensor([5, 0, 127, 64, 3], dtype=torch.int32, device="cuda:0")
+    out = torch.full((T, H), 9.0, dtype=torch.bfloat16, device="cuda:0")
+    moe.moe_combine(y, rows, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out[some], y[[5, 0, 127, 64, 3]])
+    out[some] = 0
+    for part in out.split(1 << 20):
+        assert not part.any()
