@@ -662,7 +662,7 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
   const int64_t need = lora_workspace(tokens, k, n, num_adapters ? rank : 0);
   if (need && (!workspace || workspace_bytes < need)) return NVFP4G_EINVAL;
   const hipStream_t st = (hipStream_t)stream;
-  if (((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines) > (int64_t)INT32_MAX) return NVFP4G_EINVAL;
+  if (((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines) > kMaxGroups) return NVFP4G_EINVAL;
   const int T = (int)tokens, r = num_adapters ? rank : 0, split = project_parts(tokens, k, n, r);
   const bool few = tokens <= kFewRows, halves = !few && split == 1;
   const int parts = halves ? 1 : shrink_parts(tokens, k);

@@ -72,10 +72,13 @@ __device__ __forceinline__ float act_logistic(float g, float* dv) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
 }
 
-// Work-groups of kThreads in a line.  A dimension of a launch holds fewer than
-// 2^32 threads (past that the number wraps: with 2^24 + 2^20 work-groups 2^20
-// ran, and the call succeeded), so more than 2^23 take a second dimension.  Its
-// last row may hold work-groups past the last one asked for.
+// A dimension of a launch holds fewer than 2^32 threads; past that the number
+// wraps: with 2^24 + 2^20 work-groups of kThreads 2^20 ran, and the call
+// succeeded.
+constexpr int64_t kMaxGroups = (1ll << 32) / kThreads - 1;
+
+// Work-groups of kThreads in a line: more than 2^23 take a second dimension.
+// Its last row may hold work-groups past the last one asked for.
 inline dim3 line_grid(uint32_t groups) {
   constexpr uint32_t kLine = 1u << 23;
   return groups <= kLine ? dim3(groups) : dim3(kLine, (groups - 1) / kLine + 1);

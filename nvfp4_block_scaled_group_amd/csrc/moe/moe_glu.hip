@@ -478,11 +478,12 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
 
 constexpr int64_t kMaxF = 1 << 19;  // 2f lines within the grouped GEMM's 2^20
 
+// cols_per_tile: the wide tile's columns (narrow ones are for few tiles).
 int check_glu(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, int32_t act, int cols_per_tile) {
   if (k <= 0 || k % kBK != 0 || k > kMaxK || f <= 0 || f % 16 != 0 || f > kMaxF) return NVFP4G_EINVAL;
   if (rows < 0 || rows > kMaxRows || E < 1) return NVFP4G_EINVAL;
   if (act != MOE_ACT_SILU && act != MOE_ACT_GELU) return NVFP4G_EINVAL;
-  if ((rows / kBM) * ((f + cols_per_tile - 1) / cols_per_tile) > (int64_t)INT32_MAX) return NVFP4G_EINVAL;
+  if ((rows / kBM) * ((f + cols_per_tile - 1) / cols_per_tile) > kMaxGroups) return NVFP4G_EINVAL;
   if (!O.b_data || !O.b_scale || !O.b_amax || (rows && (!O.a_data || !O.a_scale || !O.a_amax))) return NVFP4G_EINVAL;
   if (!aligned(O.a_data, 16) || !aligned(O.b_data, 16) || !aligned(O.a_scale, 4) || !aligned(O.b_scale, 4) ||
       !aligned(O.a_amax, 4) || !aligned(O.b_amax, 4))
@@ -527,7 +528,7 @@ int launch_bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Rout
 
 int fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
         const int32_t* d_offs, int32_t* d_status, bool graph, int32_t act, uint16_t* h, uint16_t* gu, void* stream) {
-  int rc = check_glu(O, rows, f, k, E, act, 64);
+  int rc = check_glu(O, rows, f, k, E, act, 128);
   if (rc) return rc;
   if (rows && !h) return NVFP4G_EINVAL;
   if (!aligned(h, 16) || !aligned(gu, 16)) return NVFP4G_EALIGN;
@@ -545,7 +546,7 @@ int fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const 
 int bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
         const int32_t* d_offs, int32_t* d_status, bool graph, const uint16_t* gu, int32_t act, uint16_t* dgu,
         void* stream) {
-  int rc = check_glu(O, rows, f, k, E, act, 128);
+  int rc = check_glu(O, rows, f, k, E, act, 256);
   if (rc) return rc;
   if (rows && (!gu || !dgu)) return NVFP4G_EINVAL;
   if (!aligned(gu, 16) || !aligned(dgu, 16)) return NVFP4G_EALIGN;

@@ -216,3 +216,17 @@ def test_capacity_holds_any_choice():
         for parts in range(1, min(n, E) + 1):
             worst = max(worst, (parts - 1) * 128 + (n - parts + 1 + 127) // 128 * 128)
         assert worst <= cap
+
+
+def test_launches_past_the_limit_are_refused(lib):
+    """Tiles that a launch cannot hold (2^24 work-groups of 256 threads)."""
+    rows, ops = 1 << 24, [FAKE] * 6
+    sp = (ctypes.c_int64 * 1)(rows)
+    assert lib.moe_glu(*ops, rows, 1 << 14, 128, 1, sp, 0, FAKE, None, None) == -1
+    assert lib.moe_glu(*ops, rows, 1 << 19, 128, 1, sp, 0, FAKE, FAKE, None) == -1
+    assert lib.moe_glu_graphsafe(*ops, rows, 1 << 14, 128, 1, FAKE, 0, FAKE, None, FAKE, None) == -1
+    assert lib.moe_glu_bwd(*ops, rows, 1 << 15, 128, 1, sp, FAKE, 0, FAKE, None) == -1
+    assert lib.moe_glu_bwd_graphsafe(*ops, rows, 1 << 15, 128, 1, FAKE, FAKE, 0, FAKE, FAKE, None) == -1
+    no_adapters = [FAKE, rows, 64, FAKE, FAKE, FAKE, 1 << 15, None, None, None, 0, 8, None, FAKE, FAKE, 1 << 25, None]
+    assert lib.lora_linear(*no_adapters) == -1
+    assert lib.lora_linear(*with_change(no_adapters, 6, 1 << 20)) == -1
