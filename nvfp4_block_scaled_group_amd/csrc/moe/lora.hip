@@ -283,9 +283,9 @@ constexpr uint32_t kStageOf = kXBytes + 128 * IN * kBK / 2;  // and 32 bytes a l
 // and the decode between them: 4095 rows, 7168 x 2048 in 150 us, 0.8 PFLOP/s.
 // Element granules (8 of x, 16 bytes) and code granules are XOR-placed in LDS so
 // that fragment reads of 32 consecutive rows or lines spread over the banks.
-// Rows past the last and
-// elements past k read as zero (the weights' codes there, the next line's, are
-// finite and meet zeros).
+// Rows past the last and elements past k read as zero.  The weights' codes past
+// k, in the second half of a last step, are the next line's; their scales, which
+// may not be numbers, read as zero.
 template <bool SPLIT, int kIN>
 __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
     const uint16_t* __restrict__ x, int64_t tokens, int64_t k, const uint8_t* __restrict__ w_data,
@@ -341,12 +341,15 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   };
   // Scales of a step, two bytes a line for each lane half (blocks 2h, 2h + 1),
   // fetched with the step's copies: a line's scales may start on any even byte.
+  // In the last step a lane half past k is moved out of the buffer's range.
+  const uint32_t spast = (steps - 1) * kBK + 32 * h < (uint32_t)k ? 0u : kOutOfRange;
   uint32_t sc0[kIN], sc1[kIN], sc2[kIN];
   auto fetch_scales = [&](uint32_t ks, uint32_t (&sc)[kIN]) {
+    const uint32_t cut = ks + 1 == steps ? spast : 0u;
 #pragma unroll
     for (int in = 0; in < kIN; ++in)
-      sc[in] = __builtin_amdgcn_raw_buffer_load_b16(ws, (wave * kWave + in * 32 + (lane & 31)) * sp + 2 * h, ks * (kBK / 16),
-                                                    0);
+      sc[in] = __builtin_amdgcn_raw_buffer_load_b16(ws, ((wave * kWave + in * 32 + (lane & 31)) * sp + 2 * h) | cut,
+                                                    ks * (kBK / 16), 0);
   };
 
   f32x16 acc[kIM][kIN];

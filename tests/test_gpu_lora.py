@@ -132,3 +132,26 @@ def test_lora_forms(T, N, K, r, A):
     got = call(w, xt, at, bt, ids, alpha, T, N, K, r)
     want, err = expect(w, x, a, b, ids, alpha.astype(np.float64), K, r)
     R.check(got, want, err, "y")
+
+
+@pytest.mark.parametrize("T,N,K", [
+    (8, 48, 96),          # few rows
+    (40, 48, 96),         # half as wide tiles
+    (40, 48, 1056),       # parts of the contraction
+    (1030, 11024, 96),    # wide tiles
+])
+def test_a_scale_that_is_not_a_number_stays_in_its_line(T, N, K):
+    """K is an odd multiple of 32: the last contraction step of a line reaches
+    the scales of the next one."""
+    log(f"lora NaN scale T={T} N={N} K={K}")
+    r, A = 8, 1
+    rng, w, xt, x, at, a, bt, b, alpha = make(9, T, N, K, r, A)
+    ids = np.full(T, -1)
+    ref = call(w, xt, at, bt, ids, alpha, T, N, K, r).clone()
+    bad = [1, 17, N - 1]                    # lines with a first and a second block that are no numbers
+    w[1][bad, 0], w[1][bad, 1] = 0x7F, 0xFF
+    got = call(w, xt, at, bt, ids, alpha, T, N, K, r)
+    keep = torch.ones(N, dtype=torch.bool, device="cuda:0")
+    keep[bad] = False
+    assert torch.equal(got[:, keep], ref[:, keep])
+    assert torch.isnan(got[:, ~keep].float()).all()
