@@ -19,9 +19,8 @@
 // Measured: 8 rows, 7168 x 7168, 6 adapters of rank 16: 19 us (1.6 TB/s; the
 // latency of a wave's seven steps after the first launch's 5 us); 4095 rows,
 // 7168 x 2048, 8 adapters of rank 32: 162 us (0.75 PFLOP/s; MFMA and decode).
-// v is kept in fp32 (few rows), or as two bf16 halves, v = hi + lo, which
-// leaves it 16 significant bits: the adapter's part then has the precision of
-// the bf16 result to spare.
+// v is kept in fp32, or, where the second launch multiplies it by MFMA, as three
+// bf16 pieces of 8 significant bits whose sum is the fp32 value.
 #include "moe_token.hpp"
 
 namespace {
@@ -35,6 +34,8 @@ constexpr int kShrinkRows = 16;   // rows of a work-group of the first launch
 constexpr int kMaxSplit = 8;      // parts of the contraction over work-groups (few rows)
 constexpr int kShrinkThreads = 512, kShrinkWaves = kShrinkThreads / 64;
 constexpr int kShrinkStep = 128;  // contraction step of a wave of the first launch
+
+constexpr int kPieces = 3;        // bf16 pieces of an fp32 value: 24 significant bits
 
 constexpr int round16(int r) { return (r + 15) / 16 * 16; }
 
@@ -76,14 +77,14 @@ __global__ __launch_bounds__(kThreads) void order_kernel(const int32_t* __restri
 
 // blockIdx = (tile of 16 rows in `order`, or as they are if that is NULL, part
 // of the contraction, first of the tile's adapters that it takes).  v [parts][tokens][rank]
-// fp32, or with HALVES (one part) alpha * v as two bf16 halves hi, then lo,
-// [tokens][rank rounded up to 16] each, zeros past the rank.  Rows without an
-// adapter are not written.  The waves take a share of the part each and join
+// fp32, or with PIECES (one part) alpha * v as kPieces bf16 tables [tokens][rank
+// rounded up to 16], zeros past the rank.  Rows without an adapter are not
+// written.  The waves take a share of the part each and join
 // in LDS.  A step's loads are in flight together; parts and adapters are
 // work-groups of their own because the chain of steps, not the bytes, is what
 // takes the time: 5 us for 8 rows of 7168, 16 for 4095 rows of 2048 (two
 // bytes an element of x: 1.0 TB/s).
-template <int NR, bool HALVES>
+template <int NR, bool PIECES>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const uint16_t* __restrict__ x, int tokens, int64_t k,
                                                           const uint16_t* __restrict__ lora_a,
                                                           const float* __restrict__ alpha, int adapters, int rank,
@@ -151,14 +152,18 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const uint16_t* 
 #pragma unroll
         for (int w = 1; w < kShrinkWaves; ++w) sum += f[w * NR * 64 * 4];
         const int c = 16 * r + col;
-        if (HALVES) {
+        if (PIECES) {
           const int r16 = round16(rank);
           if (c >= r16) break;
-          const float w = c < rank ? sum * alpha[a] : 0.0f;
-          const uint16_t hi = to_bf16(w);
+          float w = c < rank ? sum * alpha[a] : 0.0f;
           uint16_t* o = reinterpret_cast<uint16_t*>(v) + (int64_t)token[row] * r16 + c;
-          o[0] = hi;
-          o[(int64_t)tokens * r16] = to_bf16(w - __uint_as_float((uint32_t)hi << 16));
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i, o += (int64_t)tokens * r16) {
+            // cut off, not rounded: the rest is exact and nothing overflows
+            const uint32_t top = __float_as_uint(w) & 0xFFFF0000u;
+            *o = (uint16_t)(top >> 16);
+            w = __builtin_isfinite(w) ? w - __uint_as_float(top) : 0.0f;
+          }
         } else if (c < rank) {
           reinterpret_cast<float*>(v)[((int64_t)blockIdx.y * tokens + token[row]) * rank + c] = sum;
         }
@@ -471,8 +476,9 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   // must not reach them either: each adapter's product is formed apart and
   // added to its own rows alone.  The loads of 32 ranks are in flight together.
   const uint32_t r16 = round16(rank);
-  const rsrc_t vh = range_rsrc(v + base0 * r16, span * r16 * 2);
-  const rsrc_t vl = range_rsrc(v + (tokens + base0) * r16, span * r16 * 2);
+  rsrc_t vs[kPieces];
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) vs[p] = range_rsrc(v + (p * tokens + base0) * r16, span * r16 * 2);
   const rsrc_t ys = range_rsrc(y + base0 * n + col0, (span - 1) * yp + 2 * cols);
   const bool odd = lane & 1;
 #pragma unroll
@@ -495,7 +501,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
       for (int in = 0; in < kIN; ++in) part[in] = f32x16{};
 #pragma unroll 1
       for (uint32_t r = 0; r < r16; r += 32) {
-        u32x4 b[2][kIN], hi[2], lo[2];
+        u32x4 b[2][kIN], vq[2][kPieces];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t rr = r + 16 * i, bin = rr + 8 * h < (uint32_t)rank ? 0u : kOutOfRange;
@@ -504,16 +510,17 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
             b[i][in] = __builtin_amdgcn_raw_buffer_load_b128(
                 bs, ((jw + in * 32 + (lane & 31)) * rank * 2 + 16 * h + 2 * rr) | bin, 0, 0);
           const uint32_t vo = rr < r16 ? voff + 2 * rr : kOutOfRange;
-          hi[i] = __builtin_amdgcn_raw_buffer_load_b128(vh, vo, 0, 0);
-          lo[i] = __builtin_amdgcn_raw_buffer_load_b128(vl, vo, 0, 0);
+#pragma unroll
+          for (int p = 0; p < kPieces; ++p) vq[i][p] = __builtin_amdgcn_raw_buffer_load_b128(vs[p], vo, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int in = 0; in < kIN; ++in) {
             const bf16x8 bf = __builtin_bit_cast(bf16x8, b[i][in]);
-            part[in] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, hi[i]), bf, part[in], 0, 0, 0);
-            part[in] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, lo[i]), bf, part[in], 0, 0, 0);
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p)
+              part[in] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vq[i][p]), bf, part[in], 0, 0, 0);
           }
       }
 #pragma unroll
@@ -604,14 +611,14 @@ int shrink_slots(int64_t tokens, int adapters, bool in_order) {
   return (int)std::min(std::min(meets, (int64_t)adapters), std::min<int64_t>(tokens, kShrinkRows));
 }
 
-// Workspace: v (its parts, or its halves), the order, the projection's parts.
+// Workspace: v (its parts, or its pieces), the order, the projection's parts.
 struct Workspace {
   int64_t v, order, partial;
 };
 Workspace workspace_of(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
   const int parts = project_parts(tokens, k, n, rank);
-  const bool halves = tokens > kFewRows && parts == 1;
-  return {round256(halves ? tokens * round16(rank) * 4 : tokens * rank * 4 * shrink_parts(tokens, k)),
+  const bool pieces = tokens > kFewRows && parts == 1;
+  return {round256(pieces ? tokens * round16(rank) * 2 * kPieces : tokens * rank * 4 * shrink_parts(tokens, k)),
           tokens > kFewRows && rank ? round256(tokens * 4) : 0, parts > 1 ? parts * tokens * n * 4 : 0};
 }
 
@@ -667,8 +674,8 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
   const hipStream_t st = (hipStream_t)stream;
   if (((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines) > kMaxGroups) return NVFP4G_EINVAL;
   const int T = (int)tokens, r = num_adapters ? rank : 0, split = project_parts(tokens, k, n, r);
-  const bool few = tokens <= kFewRows, halves = !few && split == 1;
-  const int parts = halves ? 1 : shrink_parts(tokens, k);
+  const bool few = tokens <= kFewRows, pieces = !few && split == 1;
+  const int parts = pieces ? 1 : shrink_parts(tokens, k);
   const Workspace w = workspace_of(tokens, k, n, r);
   float* v = (float*)workspace;
   int32_t* order = ordered(tokens, k, n, num_adapters) ? (int32_t*)((char*)workspace + w.v) : nullptr;
@@ -680,7 +687,7 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
     const dim3 grid((uint32_t)((T + kShrinkRows - 1) / kShrinkRows), parts, shrink_slots(T, num_adapters, order));
     with_ranks(rank, [&](auto nr) {
       constexpr int NR = decltype(nr)::value;
-      if (halves)
+      if (pieces)
         hipLaunchKernelGGL((shrink_kernel<NR, true>), grid, dim3(kShrinkThreads), 0, st, x, T, k, lora_a, alpha, num_adapters,
                            rank, adapter_ids, order, v);
       else

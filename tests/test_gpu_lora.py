@@ -155,3 +155,30 @@ def test_a_scale_that_is_not_a_number_stays_in_its_line(T, N, K):
     keep[bad] = False
     assert torch.equal(got[:, keep], ref[:, keep])
     assert torch.isnan(got[:, ~keep].float()).all()
+
+
+@pytest.mark.parametrize("T,N,K", [
+    (8, 16, 64),          # few rows
+    (40, 16, 64),         # half as wide tiles
+    (40, 16, 1024),       # parts of the contraction
+    (1030, 11024, 64),    # wide tiles
+])
+def test_inner_product_is_kept_in_fp32(T, N, K):
+    """Two inner products that differ in their twentieth bit, with factors 1
+    and -1 (every other sum on the way is exact); and a scaled inner product
+    above bf16's largest value whose factor brings it back into range."""
+    log(f"lora fp32 inner product T={T} N={N} K={K}")
+    r = 8
+    w = (np.zeros((N, K // 2), np.uint8), np.full((N, K // 16), 0x38, np.uint8), np.ones(N, np.float32))
+    x, a, b = torch.zeros((T, K)), torch.zeros((2, r, K)), torch.zeros((2, N, r))
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 2.0 ** -10, 2.0 ** -20
+    a[0, 0, :3] = 1.0
+    a[0, 1, :2] = 1.0
+    b[0, :, 0], b[0, :, 1] = 1.0, -1.0
+    a[1, 0, 0], b[1, :, 0] = 1.0, 2.0 ** -100
+    alpha = np.array([1.0, R.FLT_MAX], np.float32)
+    ids = np.arange(T) % 3 - 1
+    got = call(w, *(t.to(torch.bfloat16) for t in (x, a, b)), ids, alpha, T, N, K, r)
+    want = torch.tensor([0.0, 2.0 ** -20, R.FLT_MAX * 2.0 ** -100], dtype=torch.float64)
+    want = want.to(torch.bfloat16)[torch.from_numpy(ids + 1)].to("cuda:0")
+    assert torch.equal(got, want[:, None].expand(T, N))
