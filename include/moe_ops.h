@@ -201,11 +201,14 @@ int moe_token_linear(const uint16_t* x, int64_t pairs, int64_t k,
  * (w_data [n, k/2], w_scale [n, k/16], w_amax [n]); lora_a [num_adapters,
  * rank, k] and lora_b [num_adapters, n, rank] bf16, alpha [num_adapters]
  * fp32; y [tokens, n] bf16, rounded once from fp32.  The inner product A_a x
- * is kept in fp32 between the two steps.  adapter_ids may be in any order.  k: a positive
- * multiple of 32, n of 16, rank of 8 up to LORA_MAX_RANK; num_adapters 0 (with
- * NULL lora_a, lora_b, alpha) is the projection alone.  workspace: at least
- * lora_workspace(tokens, k, n, rank) bytes (rank 0 without adapters), 16-byte
- * aligned; about 24 MiB at most beside the adapters' inner products. */
+ * is kept in fp32 between the two steps.  adapter_ids may be in any order.  k: a
+ * positive multiple of 32, n of 16, rank of 8 up to LORA_MAX_RANK; num_adapters
+ * 0 (with NULL lora_a, lora_b, alpha, adapter_ids) is the projection alone.
+ * workspace: lora_workspace(tokens, k, n, rank) bytes, 16-byte aligned, which
+ * also serve every call with the same k and n, up to as many tokens and up to
+ * that rank (or no adapters: rank 0).  It is at most 32 MiB or, if that is
+ * more, 6 bytes a token and rank (rounded up to 16) and 4 a token, in multiples
+ * of 256 bytes. */
 #define LORA_MAX_RANK 128
 int64_t lora_workspace(int64_t tokens, int64_t k, int64_t n, int32_t rank);
 int lora_linear(const uint16_t* x, int64_t tokens, int64_t k,

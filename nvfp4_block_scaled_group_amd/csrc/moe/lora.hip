@@ -611,15 +611,36 @@ int shrink_slots(int64_t tokens, int adapters, bool in_order) {
   return (int)std::min(std::min(meets, (int64_t)adapters), std::min<int64_t>(tokens, kShrinkRows));
 }
 
-// Workspace: v (its parts, or its pieces), the order, the projection's parts.
+// Workspace of a call: v (its parts, or its pieces), the order, the projection's
+// parts.
 struct Workspace {
   int64_t v, order, partial;
+  int64_t bytes() const { return v + order + partial; }
 };
 Workspace workspace_of(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
   const int parts = project_parts(tokens, k, n, rank);
   const bool pieces = tokens > kFewRows && parts == 1;
   return {round256(pieces ? tokens * round16(rank) * 2 * kPieces : tokens * rank * 4 * shrink_parts(tokens, k)),
           tokens > kFewRows && rank ? round256(tokens * 4) : 0, parts > 1 ? parts * tokens * n * 4 : 0};
+}
+
+// What any batch of up to `tokens` rows and any rank up to `rank` needs.  Without
+// parts of the projection the need grows with both.  With parts it does not, as
+// fewer tiles get more of them: the most that the parts of each number of row
+// tiles take, which never passes kMaxWorkspace.
+int64_t workspace_bound(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
+  const int64_t few = std::min<int64_t>(tokens, kFewRows);
+  int64_t most = workspace_of(few, k, n, rank).bytes();
+  if (tokens <= kFewRows) return most;
+  most = std::max(most, round256(tokens * round16(rank) * 2 * kPieces) + (rank ? round256(tokens * 4) : 0));
+  const int64_t ntn = (n + kWideLines - 1) / kWideLines, by_steps = (k + kBK - 1) / kBK / 4;
+  for (int64_t ntm = 1; ntm * ntn < kCus && (ntm - 1) * kBM < tokens; ++ntm) {
+    const int64_t parts = std::min(2 * kCus / (ntm * ntn), by_steps), t = std::min(tokens, ntm * kBM);
+    if (parts < 2) continue;
+    const int64_t v = round256(t * rank * 4 * shrink_parts(few, k));  // few rows have the most parts of v
+    most = std::max(most, std::min(kMaxWorkspace, v + round256(t * 4) + parts * t * n * 4));
+  }
+  return most;
 }
 
 template <class F>
@@ -651,8 +672,7 @@ extern "C" {
 
 int64_t lora_workspace(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
   if (tokens <= 0 || k <= 0 || n <= 0 || rank < 0) return 0;
-  const Workspace w = workspace_of(tokens, k, n, rank);
-  return w.v + w.order + w.partial;
+  return workspace_bound(tokens, k, n, rank);
 }
 
 int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_data, const uint8_t* w_scale,
@@ -669,14 +689,14 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
       !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(alpha, 4) || !aligned(adapter_ids, 4) ||
       !aligned(workspace, 16))
     return NVFP4G_EALIGN;
-  const int64_t need = lora_workspace(tokens, k, n, num_adapters ? rank : 0);
+  const Workspace w = workspace_of(tokens, k, n, num_adapters ? rank : 0);
+  const int64_t need = w.bytes();
   if (need && (!workspace || workspace_bytes < need)) return NVFP4G_EINVAL;
   const hipStream_t st = (hipStream_t)stream;
   if (((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines) > kMaxGroups) return NVFP4G_EINVAL;
   const int T = (int)tokens, r = num_adapters ? rank : 0, split = project_parts(tokens, k, n, r);
   const bool few = tokens <= kFewRows, pieces = !few && split == 1;
   const int parts = pieces ? 1 : shrink_parts(tokens, k);
-  const Workspace w = workspace_of(tokens, k, n, r);
   float* v = (float*)workspace;
   int32_t* order = ordered(tokens, k, n, num_adapters) ? (int32_t*)((char*)workspace + w.v) : nullptr;
   float* partial = (float*)((char*)workspace + w.v + w.order);

@@ -303,7 +303,7 @@ def moe_token_linear(x, ids, b_data, b_scale, b_amax, out, stream=None):
 # ----------------------------------------------------------------- adapters
 
 def lora_workspace(tokens: int, k: int, n: int, rank: int) -> int:
-    """Bytes of workspace that lora_linear needs (rank 0: no adapters)."""
+    """Bytes of workspace that lora_linear needs for up to ``tokens`` rows and ranks up to ``rank`` (0: no adapters)."""
     return int(load_library().lora_workspace(int(tokens), int(k), int(n), int(rank)))
 
 

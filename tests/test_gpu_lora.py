@@ -182,3 +182,23 @@ def test_inner_product_is_kept_in_fp32(T, N, K):
     want = torch.tensor([0.0, 2.0 ** -20, R.FLT_MAX * 2.0 ** -100], dtype=torch.float64)
     want = want.to(torch.bfloat16)[torch.from_numpy(ids + 1)].to("cuda:0")
     assert torch.equal(got, want[:, None].expand(T, N))
+
+
+def test_a_workspace_serves_smaller_batches_and_ranks():
+    """One workspace, sized for the largest batch and rank, for every smaller
+    one and for no adapters."""
+    N, K, r = 528, 2048, 16
+    rng, w, xt, x, at, a, bt, b, alpha = make(12, 600, N, K, r, 2)
+    ids = rng.integers(-1, 2, 600)
+    dev = [R.to_dev(v) for v in w]
+    ws = torch.empty(moe.lora_workspace(20000, K, N, r), dtype=torch.uint8, device="cuda:0")
+    for T in (1, 33, 100, 128, 400, 600):
+        for rank, adapters in ((r, 2), (8, 2), (r, 0)):
+            y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda:0")
+            la, lb = at[:adapters, :rank].contiguous(), bt[:adapters, :, :rank].contiguous()
+            moe.lora_linear(xt[:T].to("cuda:0"), *dev, la.to("cuda:0"), lb.to("cuda:0"), R.to_dev(ids[:T].astype(np.int32)),
+                            R.to_dev(alpha[:adapters]), y, ws)
+            torch.cuda.synchronize()
+            la64, lb64 = la.double().numpy(), lb.double().numpy()
+            want, err = expect(w, x[:T], la64, lb64, ids[:T], alpha.astype(np.float64), K, rank)
+            R.check(y, want, err, f"y of {T} rows, rank {rank}, {adapters} adapters")

@@ -230,3 +230,18 @@ def test_launches_past_the_limit_are_refused(lib):
     no_adapters = [FAKE, rows, 64, FAKE, FAKE, FAKE, 1 << 15, None, None, None, 0, 8, None, FAKE, FAKE, 1 << 25, None]
     assert lib.lora_linear(*no_adapters) == -1
     assert lib.lora_linear(*with_change(no_adapters, 6, 1 << 20)) == -1
+
+
+@pytest.mark.parametrize("k,n", [(32, 16), (2048, 528), (7168, 7168), (4896, 7168), (7168, 256), (4096, 1 << 16)])
+def test_lora_workspace_serves_smaller_calls(lib, k, n):
+    """It grows with the rows and with the rank, and keeps to its bound."""
+    ranks = (0, 8, 16, 24, 64, 128)
+    before = dict.fromkeys(ranks, 0)
+    for tokens in sorted({*range(1, 300), *range(300, 9000, 61), 16384, 32768, 32769, 1 << 20}):
+        last = 0
+        for rank in ranks:
+            size = moe.lora_workspace(tokens, k, n, rank)
+            r16 = (rank + 15) // 16 * 16
+            kept = (tokens * r16 * 6 + 255) // 256 * 256 + (tokens * 4 + 255) // 256 * 256
+            assert last <= size and before[rank] <= size <= max(32 << 20, kept), (tokens, rank)
+            last = before[rank] = size
