@@ -99,7 +99,8 @@ int moe_plan(const int32_t* ids, int64_t pairs, int32_t num_experts,
  * topk], also dweights[p] = sum_c x[t, c] * y[rows[p], c] (fp32; 0 where the
  * pair has no row): with x the gradient of moe_combine's output this is the
  * gradient of moe_combine in y (out) and in its weights (dweights).
- * width: a positive multiple of 16, at most NVFP4G_MAX_K. */
+ * width: a positive multiple of 16, at most NVFP4G_MAX_K; x, y and out are
+ * 16-byte aligned (in moe_combine too). */
 int moe_dispatch(const uint16_t* x, int64_t tokens, int64_t width,
                  int32_t topk, const int32_t* rows, const int32_t* src,
                  const int32_t* offs, int32_t num_experts, int64_t m_capacity,
@@ -176,7 +177,8 @@ int moe_glu_bwd_graphsafe(const uint8_t* a_data, const uint8_t* a_scale,
  * with x [tokens, k] bf16 unquantised, b as in moe_glu, h [pairs, f] bf16;
  * an id outside 0 .. E-1 gives a row of zeros.  Each chosen expert's weights
  * are read once for up to 16 pairs that share it.  Meant for decoding: pairs
- * <= MOE_MAX_TOKEN_PAIRS.  k: a positive multiple of 32, f of 16. */
+ * <= MOE_MAX_TOKEN_PAIRS.  k: a positive multiple of 32, f of 16; alignment
+ * of b as in nvfp4_group_gemm, x and h 16-byte aligned. */
 #define MOE_MAX_TOKEN_PAIRS 1024
 int moe_token_glu(const uint16_t* x, int64_t tokens, int64_t k, int32_t topk,
                   const int32_t* ids, const uint8_t* b_data,
@@ -187,7 +189,8 @@ int moe_token_glu(const uint16_t* x, int64_t tokens, int64_t k, int32_t topk,
  * every pair p with expert e = ids[p]; x [pairs, k] bf16, b_data [E, n, k/2]
  * as in nvfp4_group_gemm, out fp32 [pairs, n]; rows of zeros for pairs
  * without an expert.  moe_combine with rows[p] = p joins the pairs of a
- * token.  k: a positive multiple of 32, n of 16. */
+ * token.  k: a positive multiple of 32, n of 16; alignment as in
+ * moe_token_glu, out 16-byte aligned. */
 int moe_token_linear(const uint16_t* x, int64_t pairs, int64_t k,
                      const int32_t* ids, const uint8_t* b_data,
                      const uint8_t* b_scale, const float* b_amax, int64_t n,
@@ -204,6 +207,7 @@ int moe_token_linear(const uint16_t* x, int64_t pairs, int64_t k,
  * is kept in fp32 between the two steps.  adapter_ids may be in any order.  k: a
  * positive multiple of 32, n of 16, rank of 8 up to LORA_MAX_RANK; num_adapters
  * 0 (with NULL lora_a, lora_b, alpha, adapter_ids) is the projection alone.
+ * x, w_data, lora_a, lora_b and y are 16-byte aligned, the others 4-byte.
  * workspace: lora_workspace(tokens, k, n, rank) bytes, 16-byte aligned, which
  * also serve every call with the same k and n, up to as many tokens and up to
  * that rank (or no adapters: rank 0).  It is at most 32 MiB or, if that is

@@ -685,7 +685,7 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
   if (tokens == 0) return NVFP4G_OK;
   if (!x || !w_data || !w_scale || !w_amax || !y) return NVFP4G_EINVAL;
   if (num_adapters && (!lora_a || !lora_b || !alpha || !adapter_ids)) return NVFP4G_EINVAL;
-  if (!aligned(x, 16) || !aligned(w_data, 16) || !aligned(w_scale, 16) || !aligned(w_amax, 4) || !aligned(y, 16) ||
+  if (!aligned(x, 16) || !aligned(w_data, 16) || !aligned(w_scale, 4) || !aligned(w_amax, 4) || !aligned(y, 16) ||
       !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(alpha, 4) || !aligned(adapter_ids, 4) ||
       !aligned(workspace, 16))
     return NVFP4G_EALIGN;

@@ -202,3 +202,21 @@ def test_a_workspace_serves_smaller_batches_and_ranks():
             la64, lb64 = la.double().numpy(), lb.double().numpy()
             want, err = expect(w, x[:T], la64, lb64, ids[:T], alpha.astype(np.float64), K, rank)
             R.check(y, want, err, f"y of {T} rows, rank {rank}, {adapters} adapters")
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 48, 192), (5, 48, 96), (40, 48, 192), (40, 48, 1056)])
+def test_scales_on_any_dword(T, N, K):
+    log(f"lora scales on a dword T={T} N={N} K={K}")
+    r, A = 8, 2
+    rng, w, xt, x, at, a, bt, b, alpha = make(13, T, N, K, r, A)
+    ids = rng.integers(-1, A, T)
+    ref = call(w, xt, at, bt, ids, alpha, T, N, K, r)
+    room = torch.full((w[1].size + 16,), 0x7F, dtype=torch.uint8, device="cuda:0")
+    scale = room[4:4 + w[1].size].view(w[1].shape)
+    scale.copy_(R.to_dev(w[1]))
+    assert scale.data_ptr() % 16 == 4
+    y = torch.empty_like(ref)
+    ws = torch.empty(moe.lora_workspace(T, K, N, r), dtype=torch.uint8, device="cuda:0")
+    moe.lora_linear(xt.to("cuda:0"), R.to_dev(w[0]), scale, R.to_dev(w[2]), at.to("cuda:0"), bt.to("cuda:0"),
+                    R.to_dev(ids.astype(np.int32)), R.to_dev(alpha), y, ws)
+    assert torch.equal(y, ref)

@@ -245,3 +245,10 @@ def test_lora_workspace_serves_smaller_calls(lib, k, n):
             kept = (tokens * r16 * 6 + 255) // 256 * 256 + (tokens * 4 + 255) // 256 * 256
             assert last <= size and before[rank] <= size <= max(32 << 20, kept), (tokens, rank)
             last = before[rank] = size
+
+
+def test_lora_scales_are_four_byte_aligned(lib):
+    """As the scales of every other product; the small workspace stops the call."""
+    small = with_change(with_change(LORA, 15, 0), 4, FAKE + 4)
+    assert lib.lora_linear(*small) == -1
+    assert lib.lora_linear(*with_change(small, 4, FAKE + 2)) == -3
