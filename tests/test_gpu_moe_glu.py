@@ -256,3 +256,77 @@ def test_token_and_grouped_forms_agree():
     gu, err = products(tuple(rows), b, [128], 2 * f, k)
     bound = 2 * R.glu_bound(gu[:T, :f], gu[:T, f:], err[:T, :f], err[:T, f:], "silu")
     R.check(h2, h1[:T].double().cpu().numpy(), bound, "h")
+
+
+# ------------------------------------------- wide tiles (more than 128 of them)
+
+# rows, columns, contraction: with 128 (forward) or 256 (backward) columns a
+# tile, at least 129 tiles, the last column of them 16 wide; empty experts; one
+# case of several scale blocks, one of more than 512 tiles (their XCD order).
+WIDE = {"forward": [([1024, 0, 1536, 128, 384], 656, 640), ([16384, 0, 128, 16512], 144, 128)],
+        "backward": [([2048, 0, 3072, 128, 384], 528, 640), ([16384, 0, 128, 16512], 272, 128)]}
+
+
+@pytest.mark.parametrize("at", [0, 1])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_forward_wide_tiles(at, kind):
+    splits, f, k = WIDE["forward"][at]
+    assert sum(splits) // 128 * -(-f // 128) > 128 * (1 + 3 * at)
+    test_forward(splits, f, k, kind)
+
+
+@pytest.mark.parametrize("at", [0, 1])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_backward_wide_tiles(at, kind):
+    splits, f, k = WIDE["backward"][at]
+    assert sum(splits) // 128 * -(-f // 256) > 128 * (1 + 3 * at)
+    test_backward(splits, f, k, kind)
+
+
+@pytest.mark.parametrize("direction", ["forward", "backward"])
+def test_device_routing_wide_tiles(direction):
+    """The host-split call's bits in the routed rows, nothing in the others."""
+    splits, f, k = WIDE[direction][0]
+    spare = 640
+    lines = 2 * f if direction == "forward" else f
+    rng, M, E, a, b = case(17, splits, f, k, lines)
+    cap = M + spare
+    pad = [np.concatenate([v, np.full((spare, *v.shape[1:]), 0x7F, v.dtype)]) for v in a]
+    dev, exact = on_device(pad, b, E, lines), on_device(a, b, E, lines)
+    offs = torch.tensor(B.offsets_from_splits(splits), dtype=torch.int32, device="cuda:0")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    width = f if direction == "forward" else 2 * f
+    out = Guarded(2 * cap * width, torch.bfloat16, (cap, width))
+    gu = Guarded(4 * cap * f, torch.bfloat16, (cap, 2 * f))
+    want = torch.empty((M, width), dtype=torch.bfloat16, device="cuda:0")
+    if direction == "forward":
+        want_gu = torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0")
+        moe.moe_glu_graphsafe(*dev, offs, out.t, status, gu=gu.t)
+        moe.moe_glu(*exact, splits, want, gu=want_gu)
+        torch.cuda.synchronize()
+        assert gu.guards_intact() and torch.equal(gu.t[:M], want_gu)
+        assert (gu.t[M:].contiguous().view(torch.uint8) == CANARY).all()
+    else:
+        gu.t.copy_(R.bf16_round(rng.standard_normal((cap, 2 * f)))[0])
+        moe.moe_glu_bwd_graphsafe(*dev, offs, gu.t, out.t, status)
+        moe.moe_glu_bwd(*exact, splits, gu.t[:M].contiguous(), want)
+        torch.cuda.synchronize()
+    assert int(status) == 0 and out.guards_intact() and torch.equal(out.t[:M], want)
+    assert (out.t[M:].contiguous().view(torch.uint8) == CANARY).all()
+
+
+# --------------------------------------- two token tiles (17 to 32 rows a pass)
+
+TWO_TILES = [(24, 2, 1, 64, 48), (24, 2, 1, 2080, 32), (20, 2, 2, 544, 80), (40, 2, 1, 1056, 16), (29, 1, 1, 7168, 32),
+             (32, 16, 8, 96, 1040)]
+
+
+@pytest.mark.parametrize("T,E,topk,k,f", TWO_TILES)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_token_glu_two_tiles(T, E, topk, k, f, kind):
+    test_token_glu(T, E, topk, k, f, kind)
+
+
+@pytest.mark.parametrize("T,E,topk,k,f", TWO_TILES)
+def test_token_linear_two_tiles(T, E, topk, k, f):
+    test_token_linear(T, E, topk, k, f)
