@@ -211,3 +211,26 @@ def test_route_and_plan_replay_in_a_graph():
         for a, b in zip(got, (ids, w, p["d_offs"], p["counts"], p["rows"], p["src"])):
             assert torch.equal(a, b)
     assert int(p["d_status"]) == 0
+
+
+# Up to 8 of 65-128, 257-512 and 513-1024 experts: three more ways to share a
+# wave among tokens.
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("T,E,k,kind,dtype,biased", [
+    (131, 65, 8, "masks", torch.float32, True), (97, 128, 6, "ties", torch.bfloat16, False),
+    (67, 257, 8, "masks", torch.bfloat16, True), (129, 384, 6, "ties", torch.float32, False), (65, 512, 8, "masks", torch.float32, True),
+    (35, 513, 8, "ties", torch.bfloat16, False), (33, 1000, 3, "masks", torch.float32, True), (9, 1024, 8, "ties", torch.float32, True),
+])
+def test_route_more_experts(T, E, k, kind, dtype, biased, score, normalize):
+    test_route(T, E, k, kind, dtype, biased, score, normalize)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("T,E,k,kind,dtype", [
+    (131, 129, 8, "masks", torch.bfloat16), (66, 256, 6, "ties", torch.float32), (35, 513, 8, "masks", torch.float32),
+    (17, 1000, 5, "normal", torch.bfloat16), (9, 1024, 16, "masks", torch.bfloat16), (33, 384, 8, "ties", torch.bfloat16),
+])
+def test_route_gradient_more_experts(T, E, k, kind, dtype, score, normalize):
+    test_route_gradient_follows_the_formula(T, E, k, kind, dtype, score, normalize)
