@@ -220,3 +220,38 @@ def test_scales_on_any_dword(T, N, K):
     moe.lora_linear(xt.to("cuda:0"), R.to_dev(w[0]), scale, R.to_dev(w[2]), at.to("cuda:0"), bt.to("cuda:0"),
                     R.to_dev(ids.astype(np.int32)), R.to_dev(alpha), y, ws)
     assert torch.equal(y, ref)
+
+
+MORE_FORMS = [  # T, N, K, rank, adapters
+    (1030, 11024, 288, 72, 5),    # wide tiles, five steps of which the last is half, ranks past 64
+    (1030, 11024, 160, 16, 1),    # the same with one adapter: rows as they come
+    (300, 528, 352, 104, 6),      # half as wide tiles, six steps, ranks past 64
+    (150, 272, 416, 128, 1),
+]
+
+
+@pytest.mark.parametrize("T,N,K,r,A", MORE_FORMS)
+def test_lora_more_forms(T, N, K, r, A):
+    test_lora_forms(T, N, K, r, A)
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 48, 96), (20, 272, 544), (40, 144, 96), (40, 144, 1056), (1030, 11024, 96)])
+def test_projection_alone(T, N, K):
+    """No adapters: through the binding with empty tensors, and from C with
+    NULL pointers, which give the same bits."""
+    log(f"lora without adapters T={T} N={N} K={K}")
+    rng, w, xt, x, *_ = make(14, T, N, K, 8, 1)
+    xd, wd = xt.to("cuda:0"), [R.to_dev(v) for v in w]
+    y, again = Guarded(2 * T * N, torch.bfloat16, (T, N)), Guarded(2 * T * N, torch.bfloat16, (T, N))
+    size = moe.lora_workspace(T, K, N, 0)
+    ws = torch.full((max(16, size),), 0xFF, dtype=torch.uint8, device="cuda:0")
+    none = torch.empty((0, 8, K), dtype=torch.bfloat16, device="cuda:0"), torch.empty((0, N, 8), dtype=torch.bfloat16, device="cuda:0")
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda:0")       # no adapter has this number
+    moe.lora_linear(xd, *wd, *none, ids, torch.empty(0, device="cuda:0"), y.t, ws)
+    rc = moe.load_library().lora_linear(xd.data_ptr(), T, K, *[t.data_ptr() for t in wd], N, None, None, None, 0, 0, None,
+                                        again.t.data_ptr(), ws.data_ptr() if size else None, size,
+                                        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0 and y.guards_intact() and again.guards_intact() and torch.equal(y.t, again.t)
+    want, err = expect(w, x, np.zeros((0, 8, K)), np.zeros((0, N, 8)), [-1] * T, np.zeros(0), K, 8)
+    R.check(y.t, want, err, "y")
