@@ -128,3 +128,91 @@ def test_a_decoding_step_replays_in_a_graph(made):
         step()
         torch.cuda.synchronize()
         assert torch.equal(got, y)
+
+
+def replays(step, refresh, outputs):
+    """Captures step, then replays it on new inputs with eager work between;
+    every replay gives the eager call's bits."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        refresh()
+        for t in outputs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outputs]
+        for t in outputs:
+            t.zero_()
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, outputs):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert any(t.any() for t in got)
+
+
+def test_training_calls_replay_in_a_graph(made):
+    """Plan, dispatch, block, its backward pass, combine and their gradients
+    under a routing that changes between the replays."""
+    L, g, w, layer = made
+    m, dev = L.moe, "cuda:0"
+    plan = m.alloc_plan(T, K, E)
+    cap, offs, status = plan["src"].numel(), plan["d_offs"], plan["d_status"]
+
+    def b16(*shape):
+        return torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+
+    logits, ids, wt = torch.empty((T, E), device=dev), torch.zeros((T, K), dtype=torch.int32, device=dev), torch.zeros((T, K), device=dev)
+    x, packed, hid, gu, y = b16(T, H), b16(cap, H), b16(cap, F), b16(cap, 2 * F), b16(T, H)
+    out = torch.zeros((cap, H), device=dev)
+    d_out, dw, dlogits, dgu, dx = b16(cap, H), torch.zeros((T, K), device=dev), torch.zeros((T, E), device=dev), b16(cap, 2 * F), b16(T, H)
+    cast = [L.B.alloc_outputs(cap, n, E, True, False, device=dev) for n in (H, F, H)]
+
+    def rows(c, t):
+        L.B.nvfp4_group_quantize_graphsafe(t, E, offs, status, **c)
+        return c["row_data"], c["row_scale"], c["row_amax"]
+
+    def step():
+        m.moe_route(logits, ids, wt)
+        m.moe_plan(ids, **plan)
+        m.moe_dispatch(x, plan["rows"], plan["src"], offs, packed)
+        m.moe_glu_graphsafe(*rows(cast[0], packed), *layer.gu_lines, offs, hid, status, gu=gu)
+        L.B.nvfp4_group_gemm_graphsafe(*rows(cast[1], hid), *layer.down_lines, offs, out, status)
+        m.moe_combine(out, plan["rows"], y, weights=wt)
+        m.moe_dispatch(x, plan["rows"], plan["src"], offs, d_out, weights=wt, y=out, dweights=dw)
+        m.moe_route_bwd(logits, ids, dw, dlogits)
+        m.moe_glu_bwd_graphsafe(*rows(cast[2], d_out), *layer.down_turned, offs, gu, dgu, status)
+        m.moe_combine(d_out, plan["rows"], dx)
+
+    def refresh():
+        x.copy_(rand(g, T, H))
+        logits.copy_(x.float() @ layer.router.t() + 2 * torch.randn(E, generator=g, device=dev))
+
+    refresh()
+    replays(step, refresh, [ids, wt, plan["rows"], plan["src"], plan["d_offs"], plan["counts"], packed, hid, gu, out, y, d_out, dw,
+                            dlogits, dgu, dx])
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("rows,k", [(7, 256), (200, 256), (60, 2048)])
+def test_adapted_projection_replays_in_a_graph(made, rows, k):
+    L, g, _, _ = made
+    n, r, a = 512, 16, 5
+    p = L.AdaptedProjection(rand(g, n, k, scale=k ** -0.5), rand(g, a, r, k, scale=k ** -0.5), rand(g, a, n, r, scale=0.25),
+                            torch.linspace(0.5, 2.0, a, device="cuda:0"))
+    x, y = torch.empty((rows, k), dtype=torch.bfloat16, device="cuda:0"), torch.empty((rows, n), dtype=torch.bfloat16, device="cuda:0")
+    ids = torch.empty(rows, dtype=torch.int32, device="cuda:0")
+    ws = torch.empty(L.moe.lora_workspace(rows, k, n, r), dtype=torch.uint8, device="cuda:0")
+
+    def refresh():
+        x.copy_(rand(g, rows, k))
+        ids.copy_(torch.randint(-1, a, (rows,), generator=g, device="cuda:0"))
+
+    refresh()
+    replays(lambda: L.moe.lora_linear(x, *p.w, *p.lora, ids, p.alpha, y, ws), refresh, [y])
