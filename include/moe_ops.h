@@ -50,11 +50,13 @@ extern "C" {
  * A logit of -inf or NaN masks that expert for that token; +inf counts as
  * the largest finite value.  Per token the topk experts with the largest
  * logit + select_bias[e] (fp32 sum; select_bias may be NULL) are chosen, in
- * descending order, equal keys by the lower index.  ids [tokens, topk] gets
- * them, -1 where fewer than topk experts are unmasked; weights [tokens, topk]
- * (fp32) gets scale * s_j, or with normalize scale * s_j / sum_i s_i over the
- * chosen, where s is the score of the logit without the bias; 0 for -1 (and
- * for every choice when the chosen scores sum to 0).  1 <= topk <= E. */
+ * descending order, equal keys by the lower index; a sum of -inf or NaN is not
+ * chosen (its logit still counts in the softmax over the unmasked).  ids
+ * [tokens, topk] gets them, -1 where fewer than topk are left; weights
+ * [tokens, topk] (fp32) gets scale * s_j, or with normalize scale * s_j / sum_i
+ * s_i over the chosen, where s is the fp32 score of the logit without the bias;
+ * 0 for -1 (and for every choice when the chosen scores sum to 0).
+ * 1 <= topk <= E. */
 int moe_route(const void* logits, int32_t logits_type, int64_t tokens,
               int32_t num_experts, int32_t topk, const float* select_bias,
               int32_t score, int32_t normalize, float scale, int32_t* ids,
@@ -176,7 +178,8 @@ int moe_glu_bwd_graphsafe(const uint8_t* a_data, const uint8_t* a_scale,
  *     h[p, j] = act(sum_c x[t, c] xb_e[j, c]) * (sum_c x[t, c] xb_e[f+j, c])
  * with x [tokens, k] bf16 unquantised, b as in moe_glu, h [pairs, f] bf16;
  * an id outside 0 .. E-1 gives a row of zeros.  Each chosen expert's weights
- * are read once for up to 16 pairs that share it.  Meant for decoding: pairs
+ * are read once for up to 16 pairs that share it (32 or 64 where the pairs are
+ * that many an expert; for each pair of a lone token).  Meant for decoding: pairs
  * <= MOE_MAX_TOKEN_PAIRS.  k: a positive multiple of 32, f of 16; alignment
  * of b as in nvfp4_group_gemm, x and h 16-byte aligned. */
 #define MOE_MAX_TOKEN_PAIRS 1024
@@ -205,8 +208,9 @@ int moe_token_linear(const uint16_t* x, int64_t pairs, int64_t k,
  * rank, k] and lora_b [num_adapters, n, rank] bf16, alpha [num_adapters]
  * fp32; y [tokens, n] bf16, rounded once from fp32.  The inner product A_a x
  * is kept in fp32 between the two steps.  adapter_ids may be in any order.  k: a
- * positive multiple of 32, n of 16, rank of 8 up to LORA_MAX_RANK; num_adapters
- * 0 (with NULL lora_a, lora_b, alpha, adapter_ids) is the projection alone.
+ * positive multiple of 32 up to NVFP4G_MAX_K, n of 16 up to 2^20, rank of 8 up
+ * to LORA_MAX_RANK; tokens up to NVFP4G_MAX_ROWS; num_adapters 0 (with NULL
+ * lora_a, lora_b, alpha, adapter_ids) is the projection alone.
  * x, w_data, lora_a, lora_b and y are 16-byte aligned, the others 4-byte.
  * workspace: lora_workspace(tokens, k, n, rank) bytes, 16-byte aligned, which
  * also serve every call with the same k and n, up to as many tokens and up to

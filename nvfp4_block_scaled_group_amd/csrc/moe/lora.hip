@@ -18,9 +18,10 @@
 // take 24 us, 32 rows 28; in the second 36 and 37.
 // Measured: 8 rows, 7168 x 7168, 6 adapters of rank 16: 19 us (1.6 TB/s; the
 // latency of a wave's seven steps after the first launch's 5 us); 4095 rows,
-// 7168 x 2048, 8 adapters of rank 32: 162 us (0.75 PFLOP/s; MFMA and decode).
+// 7168 x 2048, 8 adapters of rank 32: 167 to 171 us (0.73 PFLOP/s; MFMA and decode).
 // v is kept in fp32, or, where the second launch multiplies it by MFMA, as three
-// bf16 pieces of 8 significant bits whose sum is the fp32 value.
+// bf16 pieces of 8 significant bits whose sum is the fp32 value (4096 rows of 32
+// adapters of rank 64: 223 us; with two pieces, 16 bits, 214).
 #include "moe_token.hpp"
 
 namespace {
@@ -82,8 +83,8 @@ __global__ __launch_bounds__(kThreads) void order_kernel(const int32_t* __restri
 // written.  The waves take a share of the part each and join
 // in LDS.  A step's loads are in flight together; parts and adapters are
 // work-groups of their own because the chain of steps, not the bytes, is what
-// takes the time: 5 us for 8 rows of 7168, 16 for 4095 rows of 2048 (two
-// bytes an element of x: 1.0 TB/s).
+// takes the time: 5 us for 8 rows of 7168, 17 to 19 for 4095 rows of 2048 (two
+// bytes an element of x: 0.9 TB/s).
 template <int NR, bool PIECES>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const uint16_t* __restrict__ x, int tokens, int64_t k,
                                                           const uint16_t* __restrict__ lora_a,
@@ -281,11 +282,14 @@ constexpr uint32_t kStageOf = kXBytes + 128 * IN * kBK / 2;  // and 32 bytes a l
 
 // Tile of 128 rows x 128 kIN lines, or one of gridDim.y parts of its contraction
 // (SPLIT: fp32 sums to partial[blockIdx.y], for finish_kernel, which adds the
-// adapters).  Copies run one step ahead; with SPLIT, where a CU may have one
-// work-group alone and the latency sets the pace (2.3 us a step), two (with
-// many tiles the third stage costs 2%).  Wave w takes all rows and 32 kIN lines,
-// so no weight is decoded twice in a work-group.  What bounds it is the MFMAs
-// and the decode between them: 4095 rows, 7168 x 2048 in 150 us, 0.8 PFLOP/s.
+// adapters).  Copies run one step ahead.  With SPLIT, where a CU may have one
+// work-group alone and the latency sets the pace (2.3 us a step), a third stage
+// lets them be asked for two steps ahead; but the barrier of a step waits for
+// all copies into LDS that are out, those of the next step too, so that they
+// still get one step's time (with many tiles the third stage costs 2%).  Wave w
+// takes all rows and 32 kIN lines, so no weight is decoded twice in a work-group.
+// What bounds it is the MFMAs and the decode between them: 4095 rows, 7168 x
+// 2048 in 152 us, 0.8 PFLOP/s (174 over and over, as the clock falls).
 // Element granules (8 of x, 16 bytes) and code granules are XOR-placed in LDS so
 // that fragment reads of 32 consecutive rows or lines spread over the banks.
 // Rows past the last and elements past k read as zero.  The weights' codes past
@@ -365,7 +369,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_rows_kernel(
   constexpr uint32_t kAhead = SPLIT ? 2 : 1;
   constexpr int kCopies = kBM / 32 + kBN / 128 + kIN;  // vector-memory operations of a step
   auto step = [&](uint32_t ks, const uint8_t* base, const uint32_t (&sc)[kIN], uint8_t* next, uint32_t (&next_sc)[kIN]) {
-    // this step's own copies: those of the next step, if under way, may go on
+    // this step's own copies (the barrier waits for the next step's as well)
     if (SPLIT && ks + 1 < nk) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kCopies));
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
@@ -584,7 +588,7 @@ constexpr int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 // Parts of the contraction of many rows: as many as give every CU two
 // work-groups where the tiles alone do not give it one, at least 4 steps each
 // (8 left the 7 tiles of 125 rows of a 1552 x 800 projection alone: 29 us
-// instead of 19), and all that is kept between the launches within kMaxWorkspace.
+// instead of 21), and all that is kept between the launches within kMaxWorkspace.
 constexpr int64_t kMaxWorkspace = 32 << 20;
 int project_parts(int64_t tokens, int64_t k, int64_t n, int rank) {
   const int64_t tiles = ((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines);
@@ -595,9 +599,9 @@ int project_parts(int64_t tokens, int64_t k, int64_t n, int rank) {
 }
 
 // Whether the rows are put in order first: a launch of 6 us where every row is
-// another request's (4096 rows of 4 adapters, 7168 x 2048: 181 us instead of
-// 250); where they come in order already it is lost (5474 rows of 2 adapters,
-// 1376 x 352: 42 us instead of 35), which the host cannot see.  A window's
+// another request's (4096 rows of 4 adapters, 7168 x 2048: 192 us instead of
+// 266); where they come in order already it is lost (5474 rows of 2 adapters,
+// 1376 x 352: 39 us instead of 34), which the host cannot see.  A window's
 // rows have to be within 31-bit offsets.
 bool ordered(int64_t tokens, int64_t k, int64_t n, int adapters) {
   return tokens > kFewRows && adapters > 1 && adapters < (1 << 21) && kWindow * std::max(2 * k, 2 * n) <= INT32_MAX;
@@ -721,8 +725,9 @@ int lora_linear(const uint16_t* x, int64_t tokens, int64_t k, const uint8_t* w_d
     else launch_few<2>(x, T, k, w_data, w_scale, w_amax, n, lora_b, alpha, num_adapters, rank, adapter_ids, v, parts, y, st);
   } else {
     // Half as wide tiles where neither parts nor the wide ones, two a CU, fill
-    // the device: 1500 rows, 7168 x 4096 (336 wide tiles) 129 us wide, 123
-    // narrow; 2048 rows, 7168 x 2048 (448) 85 and 96; 700 rows in parts stay wide.
+    // the device: 700 rows, 7168 x 7168 (168 wide tiles) 147 us wide, 128 narrow;
+    // 1500 rows, 7168 x 4096 (336) 135 and 128; 2048 rows, 7168 x 2048 (448) 86
+    // and 102; parts stay wide.
     const int64_t wide = ((tokens + kBM - 1) / kBM) * ((n + kWideLines - 1) / kWideLines);
     const int lines = split == 1 && wide < 3 * kCus / 2 ? kWideLines / 2 : kWideLines;
     const uint32_t ntm = (uint32_t)((tokens + kBM - 1) / kBM), ntn = (uint32_t)((n + lines - 1) / lines);

@@ -22,8 +22,8 @@
 // What bounds it: at large sizes the power of MFMAs and decode together
 // (forward, 65536 rows, 7168 x 2 x 2048: 3.0 ms, 1.28 PFLOP/s at a clock of
 // 1.6 GHz, MFMAs busy 68% of it); with few steps a tile the start and the
-// epilogue too (backward, 16384 rows of 64 experts, 2048 x 1040: 111 to 115 us, 0.6
-// PFLOP/s; the same with 1024 columns, a whole number of tiles, 91 us).
+// epilogue too (backward, 16384 rows of 64 experts, 2048 x 1040: 112 to 120 us, 0.6
+// PFLOP/s; the same with 1024 columns, a whole number of tiles, 91 to 93 us).
 #include <algorithm>
 
 #include "moe_common.hpp"
@@ -504,7 +504,8 @@ int make_routing(const int64_t* h_splits, const int32_t* d_offs, int32_t* d_stat
 // Half as wide tiles where the wide ones leave at least half of the CUs idle:
 // they decode a third more for an MFMA, but there are twice as many.  Forward,
 // 7168 x 2 x 2048: 1024 rows (128 wide tiles) 93 us wide, 70 narrow; 2944 rows
-// of 4096 x 2 x 1024 (184) 64 and 66; 65536 rows 3.03 and 3.32 ms.
+// of 4096 x 2 x 1024 (184) 64 and 66; 65536 rows 3.03 and 3.32 ms.  Device
+// routing counts the capacity's tiles: the host does not know the rows.
 bool narrow(int64_t wide_tiles) { return wide_tiles <= kCus / 2; }
 
 template <int ACT, bool KEEP, int NW>

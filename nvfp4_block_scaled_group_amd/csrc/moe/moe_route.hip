@@ -184,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const T* __restrict__ l
     for (int i = 0; i < VPL; ++i) s += expf(l[i] - top);
     sum = group_sum<LANES>(s);
   }
-  if (bias) {  // a masked logit stays -inf: the bias is finite
+  if (bias) {  // a masked logit stays -inf, whatever its bias; a sum of -inf or NaN is not chosen either
     float b[VPL];
     load_row<float, VPL>(bias, E, li, wide_bias, b);
 #pragma unroll

@@ -6,7 +6,7 @@
 // of work is one token times a run of columns; a lane moves 16 bytes of bf16
 // (8 columns) at a time.  HBM bounds all of it once there are tokens enough:
 // dispatch of 8192 x 7168 to 8 experts each in 210 us, 5.0 TB/s (a large copy
-// reaches 4.8); the gradient of combine, 4095 x 2048, 6 each, fp32 results, in
+// reaches 5.85, a large fill 5.4); the gradient of combine, 4095 x 2048, 6 each, fp32 results, in
 // 63 us, 5.0 TB/s; combine of 33 x 2064 in 4 us, a launch.
 #include "moe_common.hpp"
 
@@ -178,8 +178,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_dot_kernel(const uint16_t* 
 
 // Combine.  A wave takes a token and 512 columns; the loads of KMAX choices are
 // in flight together, the sum runs in the order of the choices.  One piece of a
-// row a wave: 8192 x 7168, 8 choices of fp32 in 360 us, 5.5 TB/s (four pieces
-// one after another 411).
+// row a wave: 8192 x 7168, 8 choices of fp32 in 360 to 374 us, 5.4 TB/s (four
+// pieces one after another 411).
 template <bool F32, int KMAX>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const void* __restrict__ y, int64_t cap, int64_t tokens,
                                                            int64_t width, int topk, int32_t pieces,

@@ -234,3 +234,18 @@ def test_route_more_experts(T, E, k, kind, dtype, biased, score, normalize):
 ])
 def test_route_gradient_more_experts(T, E, k, kind, dtype, score, normalize):
     test_route_gradient_follows_the_formula(T, E, k, kind, dtype, score, normalize)
+
+
+@pytest.mark.parametrize("E,k", [(12, 8), (256, 6), (600, 16)])
+def test_route_with_a_bias_that_is_not_finite(E, k):
+    """+inf comes first (among several the lower index), -inf and NaN never."""
+    rng = np.random.default_rng(E)
+    l = logits_for(rng, 9, E, "masks")
+    bias = rng.standard_normal(E).astype(np.float32)
+    bias[rng.permutation(E)[:E // 2]] = -np.inf
+    bias[rng.permutation(E)[:3]] = np.inf
+    bias[0], bias[E - 1] = np.nan, np.inf
+    for score in SCORES:
+        clean, ids, w = run_route(l, k, bias, score, True, 1.0, torch.float32)
+        want = R.select(clean, k, bias)
+        assert np.array_equal(ids, want) and (want < 0).any() and (w[ids < 0] == 0).all()
