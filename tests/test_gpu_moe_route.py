@@ -249,3 +249,16 @@ def test_route_with_a_bias_that_is_not_finite(E, k):
         clean, ids, w = run_route(l, k, bias, score, True, 1.0, torch.float32)
         want = R.select(clean, k, bias)
         assert np.array_equal(ids, want) and (want < 0).any() and (w[ids < 0] == 0).all()
+
+
+# the element type that the cases above leave out of a shape
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,dtype", [(40, 200, 8, torch.bfloat16), (33, 100, 10, torch.float32)])
+def test_route_other_type(T, E, k, dtype, score):
+    test_route(T, E, k, "masks", dtype, True, score, True)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,dtype", [(20, 100, 8, torch.bfloat16), (17, 400, 8, torch.float32), (3, 2000, 8, torch.bfloat16)])
+def test_route_gradient_other_type(T, E, k, dtype, score):
+    test_route_gradient_follows_the_formula(T, E, k, "masks", dtype, score, False)
