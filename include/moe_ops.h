@@ -2,8 +2,9 @@
  * moe_ops.h -- C ABI of the operators around the grouped NVFP4 path in
  * libnvfp4g.so: routing of tokens to experts, movement of rows into and out
  * of the packed 128-row expert groups, the experts' gated feed-forward block
- * with its backward pass and its single-token form, and low-rank adapters of
- * many requests beside a shared projection.
+ * with its backward pass and its single-token form, the router's balance loss
+ * with its gradient, and low-rank adapters of many requests beside a shared
+ * projection.
  *
  * Conventions are those of nvfp4_group.h: every pointer except h_splits is a
  * device pointer owned by the caller, `stream` is a hipStream_t, calls only
@@ -70,6 +71,49 @@ int moe_route_bwd(const void* logits, int32_t logits_type, int64_t tokens,
                   int32_t num_experts, int32_t topk, const int32_t* ids,
                   const float* dweights, int32_t score, int32_t normalize,
                   float scale, void* dlogits, void* stream);
+
+/* Balance loss of a router, sequence by sequence, with the counts it is made
+ * of.  The rows of logits [tokens, E] are cut into num_seqs sequences by
+ * seq_ends [num_seqs], device row ends in non-decreasing order (NULL: one
+ * sequence of all rows); rows at or past the last end count nowhere.  With
+ *     p[t, e]      softmax over the token's unmasked experts, or with
+ *                  MOE_SCORE_SIGMOID s_e / sum_i s_i of the sigmoids (0 where
+ *                  that sum underflows); masked logits as in moe_route
+ *     counts[s, e] pairs of sequence s whose id is e (an id outside 0 .. E-1
+ *                  is no choice)
+ *     seq_tokens[s] tokens n_s of s with at least one unmasked expert
+ *     probs[s, e]  sum of p[t, e] over the tokens of s
+ * the loss is
+ *     coef / num_seqs * sum_s E / (topk n_s^2) * sum_e counts[s, e] probs[s, e]
+ * (0 for a sequence with n_s = 0): coef where all experts get the same.  All
+ * four are written; sums are fp32 or wider in a fixed order.  Ends that
+ * decrease or leave 0 .. tokens make the loss NaN (nothing outside the buffers
+ * is touched; counts, probs and gradients are then of no use).
+ * num_seqs <= MOE_MAX_SEQS, tokens times topk <= MOE_MAX_PAIRS.  workspace:
+ * moe_balance_workspace(tokens, E, num_seqs) bytes, 4-byte aligned. */
+#define MOE_MAX_SEQS 65535
+int64_t moe_balance_workspace(int64_t tokens, int32_t num_experts,
+                              int32_t num_seqs);
+int moe_balance(const void* logits, int32_t logits_type, int64_t tokens,
+                int32_t num_experts, int32_t topk, const int32_t* ids,
+                int32_t score, const int32_t* seq_ends, int32_t num_seqs,
+                float coef, float* loss, int32_t* counts, float* probs,
+                int32_t* seq_tokens, void* workspace, int64_t workspace_bytes,
+                void* stream);
+
+/* Gradient of moe_balance's loss in the logits, with the counts held constant:
+ * dlogits [tokens, E] in the type of the logits, fully written (0 at masked
+ * experts and past the last end), times *dloss (device fp32; NULL: 1), plus
+ * add [tokens, E] (the type of the logits, may be dlogits itself; NULL: none),
+ * rounded once.  counts and seq_tokens as moe_balance wrote them; those of
+ * several ranks may be summed first, and the gradient is then that of the loss
+ * of all their tokens. */
+int moe_balance_bwd(const void* logits, int32_t logits_type, int64_t tokens,
+                    int32_t num_experts, int32_t topk, int32_t score,
+                    const int32_t* seq_ends, int32_t num_seqs, float coef,
+                    const int32_t* counts, const int32_t* seq_tokens,
+                    const float* dloss, const void* add, void* dlogits,
+                    void* stream);
 
 /* Plan of the packed rows.  ids: [pairs] expert of each pair; an id outside
  * 0 .. E-1 is no choice.  Expert e's group holds its pairs in pair order,
@@ -172,6 +216,52 @@ int moe_glu_bwd_graphsafe(const uint8_t* a_data, const uint8_t* a_scale,
                           int32_t num_experts, const int32_t* d_offs,
                           const uint16_t* gu, int32_t act, uint16_t* dgu,
                           int32_t* d_status, void* stream);
+
+/* The gated block with its checkpoint in 8 bits: moe_glu, with g and u kept
+ * for the backward call as whole numbers of a scale that 32 columns of a row
+ * share (16 where f ends inside a group):
+ *     S = bf16(max |v| / 127),   code = v / S to the nearest (ties to even),
+ * value code * S, off by at most S / 2 (and two fp32 roundings).  A group whose
+ * largest magnitude is below 2^-112 is kept as zeros, one with a value that is
+ * not finite as S = NaN and codes 0.  gu8 [sum_m, 2f] with g first; gu_scale
+ * [2 * ceil(f / 32), sum_m], the groups of g first (m_capacity in place of
+ * sum_m in the graph-safe form): 1.06 bytes a value in place of 2.  h is
+ * moe_glu's, from the values before they are kept.  gu8 16-byte, gu_scale 4-byte
+ * aligned. */
+#define MOE_KEEP8_GROUP 32
+int moe_glu_keep8(const uint8_t* a_data, const uint8_t* a_scale,
+                  const float* a_amax, const uint8_t* b_data,
+                  const uint8_t* b_scale, const float* b_amax, int64_t sum_m,
+                  int64_t f, int64_t k, int32_t num_experts,
+                  const int64_t* h_splits, int32_t act, uint16_t* h,
+                  int8_t* gu8, uint16_t* gu_scale, void* stream);
+int moe_glu_keep8_graphsafe(const uint8_t* a_data, const uint8_t* a_scale,
+                            const float* a_amax, const uint8_t* b_data,
+                            const uint8_t* b_scale, const float* b_amax,
+                            int64_t m_capacity, int64_t f, int64_t k,
+                            int32_t num_experts, const int32_t* d_offs,
+                            int32_t act, uint16_t* h, int8_t* gu8,
+                            uint16_t* gu_scale, int32_t* d_status,
+                            void* stream);
+
+/* moe_glu_bwd on the values that moe_glu_keep8 kept.  h [sum_m, f] bf16, if
+ * not NULL, gets act(g) * u of the kept values, for the weight gradient of the
+ * down projection: the forward pass's h need not be kept then. */
+int moe_glu_bwd_keep8(const uint8_t* a_data, const uint8_t* a_scale,
+                      const float* a_amax, const uint8_t* b_data,
+                      const uint8_t* b_scale, const float* b_amax,
+                      int64_t sum_m, int64_t f, int64_t k, int32_t num_experts,
+                      const int64_t* h_splits, const int8_t* gu8,
+                      const uint16_t* gu_scale, int32_t act, uint16_t* dgu,
+                      uint16_t* h, void* stream);
+int moe_glu_bwd_keep8_graphsafe(const uint8_t* a_data, const uint8_t* a_scale,
+                                const float* a_amax, const uint8_t* b_data,
+                                const uint8_t* b_scale, const float* b_amax,
+                                int64_t m_capacity, int64_t f, int64_t k,
+                                int32_t num_experts, const int32_t* d_offs,
+                                const int8_t* gu8, const uint16_t* gu_scale,
+                                int32_t act, uint16_t* dgu, uint16_t* h,
+                                int32_t* d_status, void* stream);
 
 /* Single-token form of the gated block: bf16 tokens, NVFP4 weights, no
  * packed groups.  For every pair p of token t with expert e = ids[p],

@@ -1,0 +1,454 @@
+// moe_balance.hip -- balance loss of a router over the sequences of a batch,
+// with the counts it is made of, and its gradient, behind the C ABI of
+// include/moe_ops.h.
+//
+//   p[t, e]  softmax of the unmasked logits, or s_e / sum_i s_i of sigmoids
+//   loss     coef / S * sum_s E / (k n_s^2) * sum_e counts[s, e] probs[s, e]
+//   a[s, e]  its derivative in p[t, e]: coef / S * E / (k n_s^2) * counts[s, e]
+//   dl[t, e] p_e (a_e - sum_i p_i a_i), with sigmoids times 1 - s_e
+//
+// Forward: a work-group takes a chunk of rows, LANES lanes a token with VPL
+// experts each, and keeps the sums of its experts in registers from token to
+// token; a sequence that ends (or the chunk's end) joins the groups in LDS in a
+// fixed order and writes one slot.  The pair (chunk, sequence) goes up in one
+// of the two or in both from slot to slot, so slot chunk + sequence is its own
+// without any list.  A second launch adds the slots of each sequence in order,
+// a third the sequences.  No float is added by an atomic.
+#include <algorithm>
+
+#include "moe_logits.hpp"
+
+namespace {
+
+using namespace moe;
+
+constexpr int kFwdThreads = 1024;
+// Threads of the forward pass: many experts a lane need the registers of many waves.
+constexpr int fwd_threads(int vpl) { return vpl <= 16 ? kFwdThreads : kFwdThreads / 4; }
+constexpr int kChunks = 256;    // chunks of a large batch: one for each CU
+constexpr int kJoinCols = 32;   // columns of a joining work-group
+
+// The first sequence whose end is above row t (num_seqs if none): the row's
+// sequence.  Whatever the ends hold, the result is in 0 .. num_seqs.
+__device__ __forceinline__ int sequence_of(const int32_t* ends, int num_seqs, int64_t t) {
+  if (!ends) return 0;
+  int lo = 0, hi = num_seqs;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > t) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Probabilities of a token's experts from its logits (masked ones -inf, which
+// get 0), l replaced; with sigmoids slope gets 1 - s.  Returns whether any
+// expert is unmasked.
+template <int LANES, int VPL, bool SIGMOID>
+__device__ __forceinline__ bool probabilities(float (&l)[VPL], float (&slope)[SIGMOID ? VPL : 1]) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+  m = group_fmax<LANES>(m);
+  const bool any = m > kNegInf;
+  float sum = 0.0f;
+  if constexpr (SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      // s = 1 / (1 + e^-l) and 1 - s = s e^-l, which keeps its digits near s = 1
+      const float e = __expf(-l[i]), s = __builtin_amdgcn_rcpf(1.0f + e);  // e^inf = inf: s = 0 where masked
+      slope[i] = s > 0.0f ? s * e : 1.0f;
+      l[i] = s;
+      sum += s;
+    }
+  } else {
+    const float top = fmaxf(m, -FLT_MAX);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      l[i] = __expf(l[i] - top);
+      sum += l[i];
+    }
+  }
+  sum = group_sum<LANES>(sum);
+  const float inv = sum >= FLT_MIN ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) l[i] *= inv;
+  return any;
+}
+
+struct Slots {
+  float* probs;     // [slots, E]
+  int32_t* counts;  // [slots, E]
+  int32_t* tokens;  // [slots]
+};
+struct Results {
+  float* loss;
+  int32_t* counts;
+  float* probs;
+  int32_t* tokens;
+};
+
+// coef / S * E / (k n^2): the weight of a sequence with n tokens.
+__device__ __forceinline__ float sequence_weight(float coef, int num_seqs, int E, int topk, int n) {
+  return n > 0 ? coef / (float)num_seqs * (float)E / (float)topk / ((float)n * (float)n) : 0.0f;
+}
+
+// Sum over the work-group's threads, in a fixed order, in thread 0.  lred: one
+// float a wave.
+__device__ __forceinline__ float block_sum(float v, float* lred, int waves) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) lred[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.0f;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < waves; ++w) s += lred[w];
+  return s;
+}
+
+// whole: the launch is one work-group and one sequence, and writes the results
+// themselves.
+template <class T, int LANES, int VPL, bool SIGMOID>
+__global__ __launch_bounds__(fwd_threads(VPL)) void balance_kernel(const T* __restrict__ logits, int64_t tokens, int E,
+                                                              int topk, const int32_t* __restrict__ ids,
+                                                              const int32_t* __restrict__ ends, int num_seqs,
+                                                              int64_t rows, bool wide, bool whole, float coef, Slots P,
+                                                              Results out) {
+  constexpr int kFwd = fwd_threads(VPL);
+  extern __shared__ float lds[];  // E sums, E counts
+  __shared__ int32_t lany;
+  __shared__ float lred[kFwd / 64];
+  float* lsum = lds;
+  int32_t* lcount = reinterpret_cast<int32_t*>(lds + E);
+  constexpr int kPass = kFwd / LANES;  // tokens at a time
+  const int tid = threadIdx.x, li = tid & (LANES - 1), wave = tid >> 6;
+  const int64_t c0 = (int64_t)blockIdx.x * rows, c1 = min(c0 + rows, tokens);
+  int64_t at = c0;
+  for (int s = sequence_of(ends, num_seqs, c0); s < num_seqs && at < c1; ++s) {
+    const int64_t to = ends ? min<int64_t>(ends[s], c1) : c1;
+    if (to <= at) continue;
+    for (int e = tid; e < E; e += kFwd) lcount[e] = 0;
+    if (tid == 0) lany = 0;
+    __syncthreads();
+    float acc[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
+    int n = 0;
+    const int64_t t0 = at + tid / LANES;
+    float l[VPL];
+    load_logits<T, VPL>(logits + min(t0, tokens - 1) * E, E, li, wide, l);
+    for (int64_t t = t0; t - tid / LANES < to; t += kPass) {
+      float next[VPL], slope[SIGMOID ? VPL : 1];
+      load_logits<T, VPL>(logits + min(t + kPass, tokens - 1) * E, E, li, wide, next);
+      const bool any = probabilities<LANES, VPL, SIGMOID>(l, slope);
+      if (t < to) {
+        n += any;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] += l[i];
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] = next[i];
+    }
+    for (int64_t p = at * topk + tid; p < to * topk; p += kFwd) {
+      const int e = ids[p];
+      if ((uint32_t)e < (uint32_t)E) atomicAdd(&lcount[e], 1);
+    }
+    if (li == 0 && n) atomicAdd(&lany, n);
+    // groups of a wave, then the waves in order
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      float v = acc[i];
+      if constexpr (LANES <= 8) v += __uint_as_float(exchange<3>(__float_as_uint(v)));
+      if constexpr (LANES <= 16) v += __uint_as_float(exchange<4>(__float_as_uint(v)));
+      if constexpr (LANES <= 32) v += __uint_as_float(exchange<5>(__float_as_uint(v)));
+      acc[i] = v;
+    }
+    for (int w = 0; w < kFwd / 64; ++w) {
+      if (wave == w && (tid & 63) < LANES) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const int e = li * VPL + i;
+          if (e < E) lsum[e] = w ? lsum[e] + acc[i] : acc[i];
+        }
+      }
+      __syncthreads();
+    }
+    if (whole) {
+      float v = 0.0f;
+      for (int e = tid; e < E; e += kFwd) {
+        out.probs[e] = lsum[e];
+        out.counts[e] = lcount[e];
+        v += (float)lcount[e] * lsum[e];
+      }
+      v = block_sum(v, lred, kFwd / 64);
+      if (tid == 0) {
+        *out.tokens = lany;
+        const bool good = !ends || (ends[0] >= 0 && ends[0] <= tokens);
+        *out.loss = good ? v * sequence_weight(coef, 1, E, topk, lany) : __uint_as_float(0x7FC00000u);
+      }
+      return;
+    }
+    const int64_t slot = (int64_t)blockIdx.x + s;
+    for (int e = tid; e < E; e += kFwd) {
+      P.probs[slot * E + e] = lsum[e];
+      P.counts[slot * E + e] = lcount[e];
+    }
+    if (tid == 0) P.tokens[slot] = lany;
+    __syncthreads();
+    at = to;
+  }
+  // one work-group and an empty sequence
+  if (whole) {
+    for (int e = tid; e < E; e += kFwd) {
+      out.probs[e] = 0.0f;
+      out.counts[e] = 0;
+    }
+    if (tid == 0) {
+      *out.tokens = 0;
+      *out.loss = !ends || ends[0] == 0 ? 0.0f : __uint_as_float(0x7FC00000u);
+    }
+  }
+}
+
+// The slots of a sequence, in order: work-group (s, b) has kJoinCols columns.
+// lossp [num_seqs, blocks] gets its share of the loss.
+__global__ __launch_bounds__(kFwdThreads) void balance_join_kernel(Slots P, int64_t tokens, int E, int topk,
+                                                                   const int32_t* __restrict__ ends, int num_seqs,
+                                                                   int64_t rows, float coef, float* __restrict__ lossp,
+                                                                   Results out) {
+  constexpr int kParts = kFwdThreads / kJoinCols;
+  __shared__ float lsum[kParts][kJoinCols + 1];
+  __shared__ int32_t lcount[kParts][kJoinCols + 1];
+  __shared__ int32_t ltok[kParts];
+  const int s = blockIdx.y, tid = threadIdx.x, part = tid / kJoinCols, c = tid % kJoinCols;
+  const int64_t from = ends && s ? ends[s - 1] : 0, to = ends ? ends[s] : tokens;
+  const bool good = from >= 0 && to >= from && to <= tokens;
+  const int64_t b = min(max(from, (int64_t)0), tokens), e = min(max(to, b), tokens);
+  const int64_t first = b / rows, last = e > b ? (e - 1) / rows : first - 1;
+  const int col = blockIdx.x * kJoinCols + c;
+  float sum = 0.0f;
+  int cnt = 0, tok = 0;
+  if (col < E)
+    for (int64_t j = first + part; j <= last; j += kParts) {
+      sum += P.probs[(j + s) * E + col];
+      cnt += P.counts[(j + s) * E + col];
+    }
+  if (c == 0)
+    for (int64_t j = first + part; j <= last; j += kParts) tok += P.tokens[j + s];
+  lsum[part][c] = sum;
+  lcount[part][c] = cnt;
+  if (c == 0) ltok[part] = tok;
+  __syncthreads();
+  if (tid >= 64) return;
+  float v = 0.0f;
+  tok = 0;
+  for (int p = 0; p < kParts; ++p) tok += ltok[p];
+  if (tid < kJoinCols && col < E) {
+    sum = 0.0f;
+    cnt = 0;
+    for (int p = 0; p < kParts; ++p) {
+      sum += lsum[p][c];
+      cnt += lcount[p][c];
+    }
+    out.probs[(int64_t)s * E + col] = sum;
+    out.counts[(int64_t)s * E + col] = cnt;
+    v = (float)cnt * sum;
+  }
+  v = wave_sum(v);
+  if (tid == 0) {
+    if (blockIdx.x == 0) out.tokens[s] = tok;
+    lossp[(int64_t)s * gridDim.x + blockIdx.x] =
+        good ? v * sequence_weight(coef, num_seqs, E, topk, tok) : __uint_as_float(0x7FC00000u);
+  }
+}
+
+__global__ __launch_bounds__(kFwdThreads) void balance_loss_kernel(const float* __restrict__ lossp, int64_t n,
+                                                                   float* __restrict__ loss) {
+  __shared__ float lred[kFwdThreads / 64];
+  float v = 0.0f;
+  for (int64_t i = threadIdx.x; i < n; i += kFwdThreads) v += lossp[i];
+  v = block_sum(v, lred, kFwdThreads / 64);
+  if (threadIdx.x == 0) *loss = v;
+}
+
+template <class T, int LANES, int VPL, bool SIGMOID>
+__global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const T* __restrict__ logits, int64_t tokens, int E,
+                                                               int topk, const int32_t* __restrict__ ends,
+                                                               int num_seqs, float coef,
+                                                               const int32_t* __restrict__ counts,
+                                                               const int32_t* __restrict__ seq_tokens,
+                                                               const float* __restrict__ dloss, const T* add,
+                                                               bool wide, bool wide_counts, T* dlogits) {
+  const int li = threadIdx.x & (LANES - 1);
+  const int64_t t = (int64_t)line_index() * (kThreads / LANES) + threadIdx.x / LANES;
+  const bool live = t < tokens;  // the others work on the last token and write nothing: exchanges need all lanes
+  const int64_t tt = live ? t : tokens - 1;
+  float l[VPL], slope[SIGMOID ? VPL : 1], extra[VPL], a[VPL];
+  load_logits<T, VPL>(logits + tt * E, E, li, wide, l);
+  if (add) load_row<T, VPL>(add + tt * E, E, li, wide, extra);
+  const int s = sequence_of(ends, num_seqs, tt);
+  const bool in = s < num_seqs;
+  const int row = in ? s : 0;
+  load_row<int32_t, VPL>(counts + (int64_t)row * E, E, li, wide_counts, a);
+  const float w = in ? sequence_weight(coef, num_seqs, E, topk, seq_tokens[row]) * (dloss ? *dloss : 1.0f) : 0.0f;
+  probabilities<LANES, VPL, SIGMOID>(l, slope);
+  float inner = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) inner += l[i] * a[i];
+  inner = group_sum<LANES>(inner);
+  float d[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    d[i] = l[i] * (a[i] - inner) * w;
+    if constexpr (SIGMOID) d[i] *= slope[i];
+    d[i] = in && l[i] > 0.0f ? d[i] : 0.0f;
+    if (add) d[i] += extra[i];
+  }
+  const int e0 = li * VPL;
+  if (!live) return;
+  T* o = dlogits + t * E;
+  if (wide) {
+    constexpr int kPer = 16 / (int)sizeof(T) < VPL ? 16 / (int)sizeof(T) : VPL;
+    if (e0 < E) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += kPer) {
+        typedef T vec_t __attribute__((ext_vector_type(kPer)));
+        vec_t v;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          if constexpr (sizeof(T) == 4) v[q] = d[i + q];
+          else v[q] = to_bf16(d[i + q]);
+        }
+        *reinterpret_cast<vec_t*>(o + e0 + i) = v;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e0 + i < E) {
+        if constexpr (sizeof(T) == 4) o[e0 + i] = d[i];
+        else o[e0 + i] = to_bf16(d[i]);
+      }
+  }
+}
+
+// ------------------------------------------------------------- host side
+
+int64_t chunk_rows(int64_t tokens) { return std::max<int64_t>(128, (tokens + kChunks - 1) / kChunks); }
+int64_t chunk_count(int64_t tokens) { return (tokens + chunk_rows(tokens) - 1) / chunk_rows(tokens); }
+bool one_group(int64_t tokens, int num_seqs) { return num_seqs == 1 && chunk_count(tokens) <= 1; }
+int64_t join_blocks(int E) { return (E + kJoinCols - 1) / kJoinCols; }
+
+int check_balance(const void* logits, int32_t type, int64_t tokens, int32_t E, int32_t topk, int32_t score,
+                  const int32_t* ends, int32_t num_seqs) {
+  if (!valid_type(type) || (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID)) return NVFP4G_EINVAL;
+  if (E < 1 || E > MOE_MAX_EXPERTS || topk < 1 || topk > MOE_MAX_TOPK || topk > E) return NVFP4G_EINVAL;
+  if (tokens < 0 || tokens > MOE_MAX_PAIRS / topk || num_seqs < 1 || num_seqs > MOE_MAX_SEQS) return NVFP4G_EINVAL;
+  if (tokens && !logits) return NVFP4G_EINVAL;
+  if (num_seqs > 1 && !ends) return NVFP4G_EINVAL;
+  if (!aligned(logits, type == MOE_F32 ? 4 : 2) || !aligned(ends, 4)) return NVFP4G_EALIGN;
+  return NVFP4G_OK;
+}
+
+// Calls f with the lanes of a token and the experts of a lane.
+template <class F>
+void by_experts(int E, F f) {
+  if (E <= 32) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+  else if (E <= 64) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
+  else if (E <= 128) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+  else if (E <= 256) f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+  else if (E <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
+  else if (E <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
+  else if (E <= 2048) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 32>{});
+  else f(std::integral_constant<int, 64>{}, std::integral_constant<int, 64>{});
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t moe_balance_workspace(int64_t tokens, int32_t num_experts, int32_t num_seqs) {
+  if (tokens < 0 || tokens > MOE_MAX_PAIRS || num_experts < 1 || num_experts > MOE_MAX_EXPERTS || num_seqs < 1 ||
+      num_seqs > MOE_MAX_SEQS)
+    return NVFP4G_EINVAL;
+  if (one_group(tokens, num_seqs)) return 0;
+  return (chunk_count(tokens) + num_seqs) * (8 * (int64_t)num_experts + 4) + 4 * num_seqs * join_blocks(num_experts);
+}
+
+int moe_balance(const void* logits, int32_t logits_type, int64_t tokens, int32_t num_experts, int32_t topk,
+                const int32_t* ids, int32_t score, const int32_t* seq_ends, int32_t num_seqs, float coef, float* loss,
+                int32_t* counts, float* probs, int32_t* seq_tokens, void* workspace, int64_t workspace_bytes,
+                void* stream) {
+  const int rc = check_balance(logits, logits_type, tokens, num_experts, topk, score, seq_ends, num_seqs);
+  if (rc) return rc;
+  if ((tokens && !ids) || !loss || !counts || !probs || !seq_tokens) return NVFP4G_EINVAL;
+  const int64_t need = moe_balance_workspace(tokens, num_experts, num_seqs);
+  if (need && (!workspace || workspace_bytes < need)) return NVFP4G_EINVAL;
+  if (!aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(probs, 4) || !aligned(seq_tokens, 4) ||
+      !aligned(workspace, 4))
+    return NVFP4G_EALIGN;
+  const hipStream_t st = (hipStream_t)stream;
+  const int E = num_experts;
+  const int64_t rows = chunk_rows(tokens), chunks = chunk_count(tokens), slots = chunks + num_seqs;
+  const bool whole = one_group(tokens, num_seqs);
+  const Results R{loss, counts, probs, seq_tokens};
+  Slots P{(float*)workspace, (int32_t*)workspace + slots * E, (int32_t*)workspace + 2 * slots * E};
+  if (chunks || whole) {
+    const int size = logits_type == MOE_F32 ? 4 : 2;
+    by_experts(E, [&](auto lanes, auto vpl) {
+      constexpr int L = decltype(lanes)::value, V = decltype(vpl)::value;
+      const bool wide = wide_rows(logits, E, V, size);
+      auto go = [&](auto* kernel, auto* p) {
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)std::max<int64_t>(chunks, 1)), dim3(fwd_threads(V)), 8 * E, st, p,
+                           tokens, E, topk, ids, seq_ends, num_seqs, rows, wide, whole, coef, P, R);
+      };
+      if (logits_type == MOE_F32) {
+        if (score == MOE_SCORE_SIGMOID) go(balance_kernel<float, L, V, true>, (const float*)logits);
+        else go(balance_kernel<float, L, V, false>, (const float*)logits);
+      } else {
+        if (score == MOE_SCORE_SIGMOID) go(balance_kernel<uint16_t, L, V, true>, (const uint16_t*)logits);
+        else go(balance_kernel<uint16_t, L, V, false>, (const uint16_t*)logits);
+      }
+    });
+    if (whole) return hip_status();
+  }
+  const int64_t blocks = join_blocks(E);
+  float* lossp = (float*)(P.tokens + slots);
+  hipLaunchKernelGGL(balance_join_kernel, dim3((uint32_t)blocks, (uint32_t)num_seqs), dim3(kFwdThreads), 0, st, P,
+                     tokens, E, topk, seq_ends, num_seqs, rows, coef, lossp, R);
+  hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFwdThreads), 0, st, lossp, blocks * num_seqs, loss);
+  return hip_status();
+}
+
+int moe_balance_bwd(const void* logits, int32_t logits_type, int64_t tokens, int32_t num_experts, int32_t topk,
+                    int32_t score, const int32_t* seq_ends, int32_t num_seqs, float coef, const int32_t* counts,
+                    const int32_t* seq_tokens, const float* dloss, const void* add, void* dlogits, void* stream) {
+  const int rc = check_balance(logits, logits_type, tokens, num_experts, topk, score, seq_ends, num_seqs);
+  if (rc) return rc;
+  if (tokens && (!counts || !seq_tokens || !dlogits)) return NVFP4G_EINVAL;
+  const int size = logits_type == MOE_F32 ? 4 : 2;
+  if (!aligned(counts, 4) || !aligned(seq_tokens, 4) || !aligned(dloss, 4) || !aligned(add, size) ||
+      !aligned(dlogits, size))
+    return NVFP4G_EALIGN;
+  if (tokens == 0) return NVFP4G_OK;
+  const int E = num_experts;
+  by_experts(E, [&](auto lanes, auto vpl) {
+    constexpr int L = decltype(lanes)::value, V = decltype(vpl)::value;
+    const bool wide = wide_rows(logits, E, V, size) && wide_rows(dlogits, E, V, size) && wide_rows(add, E, V, size);
+    const int64_t groups = (tokens + kThreads / L - 1) / (kThreads / L);
+    auto go = [&](auto* kernel, auto* p) {
+      using P = decltype(p);
+      hipLaunchKernelGGL(kernel, line_grid((uint32_t)groups), dim3(kThreads), 0, (hipStream_t)stream, p, tokens, E,
+                         topk, seq_ends, num_seqs, coef, counts, seq_tokens, dloss, (P)add, wide,
+                         wide_rows(counts, E, V, 4), const_cast<std::remove_const_t<std::remove_pointer_t<P>>*>((P)dlogits));
+    };
+    if (logits_type == MOE_F32) {
+      if (score == MOE_SCORE_SIGMOID) go(balance_bwd_kernel<float, L, V, true>, (const float*)logits);
+      else go(balance_bwd_kernel<float, L, V, false>, (const float*)logits);
+    } else {
+      if (score == MOE_SCORE_SIGMOID) go(balance_bwd_kernel<uint16_t, L, V, true>, (const uint16_t*)logits);
+      else go(balance_bwd_kernel<uint16_t, L, V, false>, (const uint16_t*)logits);
+    }
+  });
+  return hip_status();
+}
+
+}  // extern "C"

@@ -26,6 +26,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ uint16_t to_bf16(float a) { return __builtin_bit_cast(uint16_t, (__bf16)a); }
 
+// Four int8 codes of four fp32 values below 127.5 in magnitude:
+// adding 1.5 * 2^23 rounds to the nearest whole number, ties to even, and
+// leaves it in the low byte.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  constexpr float kMagic = 12582912.0f;
+  const uint32_t p = __builtin_amdgcn_perm(__float_as_uint(b + kMagic), __float_as_uint(a + kMagic), 0x0c0c0400u);
+  const uint32_t q = __builtin_amdgcn_perm(__float_as_uint(d + kMagic), __float_as_uint(c + kMagic), 0x04000c0cu);
+  return p | q;
+}
+
 // Reductions over the 64 lanes of a wave, the result in every lane: five
 // lane exchanges inside and across 16-lane rows, then the two halves.
 template <class Op>

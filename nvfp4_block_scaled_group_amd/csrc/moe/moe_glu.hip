@@ -296,11 +296,45 @@ __device__ __forceinline__ float glu(float g, float u) {
   return g * act_logistic<ACT>(g, &dv) * u;
 }
 
+// What the forward pass keeps for the backward one.
+enum Keep { kKeepNone, kKeepBf16, kKeep8 };
+// g and u in 8 bits: codes [rows, 2f] and scales [2 * ceil(f / 32), rows], so
+// that the scales of a tile's rows lie side by side.
+struct Kept {
+  int8_t* q;
+  uint16_t* s;
+  int64_t rows;
+};
+constexpr int kGroup = MOE_KEEP8_GROUP;  // columns of a scale: four lanes hold 8 each
+static_assert(kGroup == 32, "the reductions below are over four lanes");
+
+// Codes of a lane's 8 values and the scale (bf16 bits) of its group.
+__device__ __forceinline__ u32x2 keep8(const float (&v)[8], uint16_t* scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);  // NaN above inf above the rest
+  m = max(m, dpp_x1(m));
+  m = max(m, dpp_x2(m));
+  if (m >= 0x7F800000u || m < __float_as_uint(0x1p-112f)) {
+    *scale = m >= 0x7F800000u ? 0x7FC0 : 0;
+    return u32x2{0, 0};
+  }
+  *scale = to_bf16(__uint_as_float(m) / 127.0f);
+  // at most 127 (1 + 2^-8) / (1 - 2^-9) < 127.5: a code never passes 127
+  const float inv = 1.0f / __uint_as_float((uint32_t)*scale << 16);
+  return u32x2{codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+}
+// The value of byte i of a lane's codes, exact: (code + 128) s - 128 s.
+__device__ __forceinline__ float kept(u32x2 q, int i, float s) {
+  const uint32_t w = q[i >> 2] ^ 0x80808080u;
+  return __builtin_fmaf((float)((w >> (8 * (i & 3))) & 0xFFu), s, -128.0f * s);
+}
+
 // Forward: tiles of 128 packed rows x 32 NW columns (64 NW lines).
-template <int ACT, bool KEEP, int NW>
+template <int ACT, Keep KEEP, int NW>
 __global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_t f, int64_t k, Routing R,
                                                               uint32_t ntm, uint32_t ntn, uint16_t* __restrict__ h,
-                                                              uint16_t* __restrict__ gu) {
+                                                              uint16_t* __restrict__ gu, Kept K8) {
   constexpr int kCols = 32 * NW;
   __shared__ __attribute__((aligned(16))) uint8_t lds0[Tile<NW>::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t lds1[Tile<NW>::kStageBytes];
@@ -368,7 +402,29 @@ __global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_
       wave_sync();
     };
     put_rows(h, f);
-    if (KEEP) {
+    if (KEEP == kKeep8) {
+      const int64_t groups = (f + kGroup - 1) / kGroup;
+#pragma unroll
+      for (int up = 0; up < 2; ++up) {
+#pragma unroll
+        for (int in = 0; in < BLK; ++in)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) stage.put(in, v, lane, up ? u[in][v] : g[in][v]);
+        wave_sync();
+        uint16_t* scales = K8.s + (up * groups + (col0 + j0 + c) / kGroup) * K8.rows + out0;
+#pragma unroll
+        for (int r = 0; r < 32; r += Stage<BLK>::kRows) {
+          float v[8];
+          stage.get(r + srow, c, v);
+          uint16_t s;
+          const u32x2 q = keep8(v, &s);
+          if (write) *reinterpret_cast<u32x2*>(K8.q + (out0 + r) * 2 * f + up * f + col0 + j0 + c) = q;
+          if (write && (lane & 3) == 0) scales[r] = s;
+        }
+        wave_sync();
+      }
+    }
+    if (KEEP == kKeepBf16) {
 #pragma unroll
       for (int in = 0; in < BLK; ++in)
 #pragma unroll
@@ -383,12 +439,14 @@ __global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_
   }
 }
 
-// Backward: tiles of 128 packed rows x 64 NW columns of dh.
-template <int ACT, int NW>
+// Backward: tiles of 128 packed rows x 64 NW columns of dh.  With KEEP8 g and u
+// come from 8 bits, and act(g) * u goes to `again` if that is not null.
+template <int ACT, bool KEEP8, int NW>
 __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_t f, int64_t k, Routing R,
                                                               uint32_t ntm, uint32_t ntn,
-                                                              const uint16_t* __restrict__ gu,
-                                                              uint16_t* __restrict__ dgu) {
+                                                              const uint16_t* __restrict__ gu, Kept K8,
+                                                              uint16_t* __restrict__ dgu,
+                                                              uint16_t* __restrict__ again) {
   constexpr int kCols = Tile<NW>::kLines;
   __shared__ __attribute__((aligned(16))) uint8_t lds0[Tile<NW>::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t lds1[Tile<NW>::kStageBytes];
@@ -434,8 +492,23 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
       // through the caches: rows of 2f columns start inside a cache line (past
       // them 1 to 4% slower); two blocks' loads at once were 8% slower
       u32x4 gq[kPasses], uq[kPasses];
+      u32x2 g8[kPasses], u8[kPasses];
+      uint16_t gs[kPasses], us[kPasses];
+      const int64_t groups = (f + kGroup - 1) / kGroup, grow0 = row0 + wm * (kWM * 32) + im * 32 + srow;
+      const uint16_t* scales = KEEP8 ? K8.s + (col0 + j0 + c) / kGroup * K8.rows + grow0 : nullptr;
 #pragma unroll
       for (int r = 0; r < kPasses; ++r) {
+        if (KEEP8) {
+          g8[r] = u8[r] = u32x2{0, 0};
+          gs[r] = us[r] = 0;
+          if (write) {
+            g8[r] = *reinterpret_cast<const u32x2*>(K8.q + at0 + 2 * kRows * r * f);
+            u8[r] = *reinterpret_cast<const u32x2*>(K8.q + at0 + 2 * kRows * r * f + f);
+            gs[r] = scales[kRows * r];
+            us[r] = scales[groups * K8.rows + kRows * r];
+          }
+          continue;
+        }
         gq[r] = uq[r] = u32x4{0, 0, 0, 0};
         if (write) {
           gq[r] = *reinterpret_cast<const u32x4*>(gu + at0 + 2 * kRows * r * f);
@@ -454,17 +527,22 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
       wave_sync();
 #pragma unroll
       for (int r = 0; r < kPasses; ++r) {
-        float dh[8], dg[8], du[8];
+        float dh[8], dg[8], du[8], hh[8];
         stage.get(kRows * r + srow, c, dh);
+        const float sg = KEEP8 ? __uint_as_float((uint32_t)gs[r] << 16) : 0.0f;
+        const float su = KEEP8 ? __uint_as_float((uint32_t)us[r] << 16) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float g = i & 1 ? bf16hi(gq[r][i >> 1]) : bf16lo(gq[r][i >> 1]);
-          const float u = i & 1 ? bf16hi(uq[r][i >> 1]) : bf16lo(uq[r][i >> 1]);
+          const float g = KEEP8 ? kept(g8[r], i, sg) : i & 1 ? bf16hi(gq[r][i >> 1]) : bf16lo(gq[r][i >> 1]);
+          const float u = KEEP8 ? kept(u8[r], i, su) : i & 1 ? bf16hi(uq[r][i >> 1]) : bf16lo(uq[r][i >> 1]);
           float dv;
           const float q = act_logistic<ACT>(g, &dv), a = g * q;
           du[i] = dh[i] * a;
           dg[i] = dh[i] * u * __builtin_fmaf(a * (1.0f - q), dv, q);
+          if (KEEP8) hh[i] = a * u;
         }
+        if (KEEP8 && again && write)
+          *reinterpret_cast<u32x4*>(again + (grow0 + kRows * r) * f + col0 + j0 + c) = pack8(hh);
         if (write) {
           *reinterpret_cast<u32x4*>(dgu + at0 + 2 * kRows * r * f) = pack8(dg);
           *reinterpret_cast<u32x4*>(dgu + at0 + 2 * kRows * r * f + f) = pack8(du);
@@ -508,54 +586,77 @@ int make_routing(const int64_t* h_splits, const int32_t* d_offs, int32_t* d_stat
 // routing counts the capacity's tiles: the host does not know the rows.
 bool narrow(int64_t wide_tiles) { return wide_tiles <= kCus / 2; }
 
-template <int ACT, bool KEEP, int NW>
+template <int ACT, Keep KEEP, int NW>
 int launch_fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Routing& R, uint16_t* h, uint16_t* gu,
-               hipStream_t st) {
+               const Kept& K8, hipStream_t st) {
   const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + 32 * NW - 1) / (32 * NW));
-  if (NW == 4 && narrow((int64_t)ntm * ntn)) return launch_fwd<ACT, KEEP, 2>(O, rows, f, k, R, h, gu, st);
+  if (NW == 4 && narrow((int64_t)ntm * ntn)) return launch_fwd<ACT, KEEP, 2>(O, rows, f, k, R, h, gu, K8, st);
   hipLaunchKernelGGL((glu_fwd_kernel<ACT, KEEP, NW>), dim3(ntm * ntn), dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h,
-                     gu);
+                     gu, K8);
   return hip_status();
 }
 
-template <int ACT, int NW>
+template <int ACT, bool KEEP8, int NW>
 int launch_bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Routing& R, const uint16_t* gu,
-               uint16_t* dgu, hipStream_t st) {
+               const Kept& K8, uint16_t* dgu, uint16_t* again, hipStream_t st) {
   const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + 64 * NW - 1) / (64 * NW));
-  if (NW == 4 && narrow((int64_t)ntm * ntn)) return launch_bwd<ACT, 2>(O, rows, f, k, R, gu, dgu, st);
-  hipLaunchKernelGGL((glu_bwd_kernel<ACT, NW>), dim3(ntm * ntn), dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, gu, dgu);
+  if (NW == 4 && narrow((int64_t)ntm * ntn)) return launch_bwd<ACT, KEEP8, 2>(O, rows, f, k, R, gu, K8, dgu, again, st);
+  hipLaunchKernelGGL((glu_bwd_kernel<ACT, KEEP8, NW>), dim3(ntm * ntn), dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, gu,
+                     K8, dgu, again);
   return hip_status();
 }
 
-int fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
-        const int32_t* d_offs, int32_t* d_status, bool graph, int32_t act, uint16_t* h, uint16_t* gu, void* stream) {
+// How a call's rows are routed: by h_splits, or with `graph` by d_offs.
+struct Route {
+  const int64_t* h_splits;
+  const int32_t* d_offs;
+  int32_t* d_status;
+  bool graph;
+};
+
+template <Keep KEEP>
+int fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const Route& W, int32_t act, uint16_t* h,
+        uint16_t* gu, const Kept& K8, void* stream) {
   int rc = check_glu(O, rows, f, k, E, act, 128);
   if (rc) return rc;
-  if (rows && !h) return NVFP4G_EINVAL;
-  if (!aligned(h, 16) || !aligned(gu, 16)) return NVFP4G_EALIGN;
+  if (rows && (!h || (KEEP == kKeep8 && (!K8.q || !K8.s)))) return NVFP4G_EINVAL;
+  if (!aligned(h, 16) || !aligned(gu, 16) || !aligned(K8.q, 16) || !aligned(K8.s, 4)) return NVFP4G_EALIGN;
   Routing R;
-  if ((rc = make_routing(h_splits, d_offs, d_status, rows, E, graph, &R))) return rc;
+  if ((rc = make_routing(W.h_splits, W.d_offs, W.d_status, rows, E, W.graph, &R))) return rc;
   if (rows == 0) return NVFP4G_OK;
   const hipStream_t st = (hipStream_t)stream;
-  if (act == MOE_ACT_SILU)
-    return gu ? launch_fwd<MOE_ACT_SILU, true, 4>(O, rows, f, k, R, h, gu, st)
-              : launch_fwd<MOE_ACT_SILU, false, 4>(O, rows, f, k, R, h, gu, st);
-  return gu ? launch_fwd<MOE_ACT_GELU, true, 4>(O, rows, f, k, R, h, gu, st)
-            : launch_fwd<MOE_ACT_GELU, false, 4>(O, rows, f, k, R, h, gu, st);
+  return act == MOE_ACT_SILU ? launch_fwd<MOE_ACT_SILU, KEEP, 4>(O, rows, f, k, R, h, gu, K8, st)
+                             : launch_fwd<MOE_ACT_GELU, KEEP, 4>(O, rows, f, k, R, h, gu, K8, st);
+}
+int fwd_bf16(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const Route& W, int32_t act,
+             uint16_t* h, uint16_t* gu, void* stream) {
+  const Kept none{nullptr, nullptr, 0};
+  return gu ? fwd<kKeepBf16>(O, rows, f, k, E, W, act, h, gu, none, stream)
+            : fwd<kKeepNone>(O, rows, f, k, E, W, act, h, gu, none, stream);
 }
 
-int bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
-        const int32_t* d_offs, int32_t* d_status, bool graph, const uint16_t* gu, int32_t act, uint16_t* dgu,
-        void* stream) {
+template <bool KEEP8>
+int bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const Route& W, const uint16_t* gu,
+        const Kept& K8, int32_t act, uint16_t* dgu, uint16_t* again, void* stream) {
   int rc = check_glu(O, rows, f, k, E, act, 256);
   if (rc) return rc;
-  if (rows && (!gu || !dgu)) return NVFP4G_EINVAL;
-  if (!aligned(gu, 16) || !aligned(dgu, 16)) return NVFP4G_EALIGN;
+  if (rows && ((KEEP8 ? !K8.q || !K8.s : !gu) || !dgu)) return NVFP4G_EINVAL;
+  if (!aligned(gu, 16) || !aligned(dgu, 16) || !aligned(again, 16) || !aligned(K8.q, 16) || !aligned(K8.s, 4))
+    return NVFP4G_EALIGN;
   Routing R;
-  if ((rc = make_routing(h_splits, d_offs, d_status, rows, E, graph, &R))) return rc;
+  if ((rc = make_routing(W.h_splits, W.d_offs, W.d_status, rows, E, W.graph, &R))) return rc;
   if (rows == 0) return NVFP4G_OK;
-  return act == MOE_ACT_SILU ? launch_bwd<MOE_ACT_SILU, 4>(O, rows, f, k, R, gu, dgu, (hipStream_t)stream)
-                             : launch_bwd<MOE_ACT_GELU, 4>(O, rows, f, k, R, gu, dgu, (hipStream_t)stream);
+  const hipStream_t st = (hipStream_t)stream;
+  return act == MOE_ACT_SILU ? launch_bwd<MOE_ACT_SILU, KEEP8, 4>(O, rows, f, k, R, gu, K8, dgu, again, st)
+                             : launch_bwd<MOE_ACT_GELU, KEEP8, 4>(O, rows, f, k, R, gu, K8, dgu, again, st);
+}
+int bwd_bf16(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const Route& W, const uint16_t* gu,
+             int32_t act, uint16_t* dgu, void* stream) {
+  return bwd<false>(O, rows, f, k, E, W, gu, Kept{nullptr, nullptr, 0}, act, dgu, nullptr, stream);
+}
+// The backward pass only reads what was kept.
+Kept kept_of(const int8_t* q, const uint16_t* s, int64_t rows) {
+  return Kept{const_cast<int8_t*>(q), const_cast<uint16_t*>(s), rows};
 }
 
 }  // namespace
@@ -565,31 +666,65 @@ extern "C" {
 int moe_glu(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
             const uint8_t* b_scale, const float* b_amax, int64_t sum_m, int64_t f, int64_t k, int32_t num_experts,
             const int64_t* h_splits, int32_t act, uint16_t* h, uint16_t* gu, void* stream) {
-  return fwd({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, sum_m, f, k, num_experts, h_splits, nullptr, nullptr,
-             false, act, h, gu, stream);
+  return fwd_bf16({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, sum_m, f, k, num_experts,
+                  {h_splits, nullptr, nullptr, false}, act, h, gu, stream);
 }
 
 int moe_glu_graphsafe(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
                       const uint8_t* b_scale, const float* b_amax, int64_t m_capacity, int64_t f, int64_t k,
                       int32_t num_experts, const int32_t* d_offs, int32_t act, uint16_t* h, uint16_t* gu,
                       int32_t* d_status, void* stream) {
-  return fwd({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, m_capacity, f, k, num_experts, nullptr, d_offs,
-             d_status, true, act, h, gu, stream);
+  return fwd_bf16({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, m_capacity, f, k, num_experts,
+                  {nullptr, d_offs, d_status, true}, act, h, gu, stream);
 }
 
 int moe_glu_bwd(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
                 const uint8_t* b_scale, const float* b_amax, int64_t sum_m, int64_t f, int64_t k, int32_t num_experts,
                 const int64_t* h_splits, const uint16_t* gu, int32_t act, uint16_t* dgu, void* stream) {
-  return bwd({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, sum_m, f, k, num_experts, h_splits, nullptr, nullptr,
-             false, gu, act, dgu, stream);
+  return bwd_bf16({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, sum_m, f, k, num_experts,
+                  {h_splits, nullptr, nullptr, false}, gu, act, dgu, stream);
 }
 
 int moe_glu_bwd_graphsafe(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
                           const uint8_t* b_scale, const float* b_amax, int64_t m_capacity, int64_t f, int64_t k,
                           int32_t num_experts, const int32_t* d_offs, const uint16_t* gu, int32_t act, uint16_t* dgu,
                           int32_t* d_status, void* stream) {
-  return bwd({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, m_capacity, f, k, num_experts, nullptr, d_offs,
-             d_status, true, gu, act, dgu, stream);
+  return bwd_bf16({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, m_capacity, f, k, num_experts,
+                  {nullptr, d_offs, d_status, true}, gu, act, dgu, stream);
+}
+
+int moe_glu_keep8(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
+                  const uint8_t* b_scale, const float* b_amax, int64_t sum_m, int64_t f, int64_t k,
+                  int32_t num_experts, const int64_t* h_splits, int32_t act, uint16_t* h, int8_t* gu8,
+                  uint16_t* gu_scale, void* stream) {
+  return fwd<kKeep8>({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, sum_m, f, k, num_experts,
+                     {h_splits, nullptr, nullptr, false}, act, h, nullptr, {gu8, gu_scale, sum_m}, stream);
+}
+
+int moe_glu_keep8_graphsafe(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
+                            const uint8_t* b_scale, const float* b_amax, int64_t m_capacity, int64_t f, int64_t k,
+                            int32_t num_experts, const int32_t* d_offs, int32_t act, uint16_t* h, int8_t* gu8,
+                            uint16_t* gu_scale, int32_t* d_status, void* stream) {
+  return fwd<kKeep8>({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, m_capacity, f, k, num_experts,
+                     {nullptr, d_offs, d_status, true}, act, h, nullptr, {gu8, gu_scale, m_capacity}, stream);
+}
+
+int moe_glu_bwd_keep8(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax, const uint8_t* b_data,
+                      const uint8_t* b_scale, const float* b_amax, int64_t sum_m, int64_t f, int64_t k,
+                      int32_t num_experts, const int64_t* h_splits, const int8_t* gu8, const uint16_t* gu_scale,
+                      int32_t act, uint16_t* dgu, uint16_t* h, void* stream) {
+  return bwd<true>({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, sum_m, f, k, num_experts,
+                   {h_splits, nullptr, nullptr, false}, nullptr, kept_of(gu8, gu_scale, sum_m), act, dgu, h, stream);
+}
+
+int moe_glu_bwd_keep8_graphsafe(const uint8_t* a_data, const uint8_t* a_scale, const float* a_amax,
+                                const uint8_t* b_data, const uint8_t* b_scale, const float* b_amax,
+                                int64_t m_capacity, int64_t f, int64_t k, int32_t num_experts, const int32_t* d_offs,
+                                const int8_t* gu8, const uint16_t* gu_scale, int32_t act, uint16_t* dgu, uint16_t* h,
+                                int32_t* d_status, void* stream) {
+  return bwd<true>({a_data, a_scale, a_amax, b_data, b_scale, b_amax}, m_capacity, f, k, num_experts,
+                   {nullptr, d_offs, d_status, true}, nullptr, kept_of(gu8, gu_scale, m_capacity), act, dgu, h,
+                   stream);
 }
 
 }  // extern "C"

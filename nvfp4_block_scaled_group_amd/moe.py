@@ -1,8 +1,9 @@
 """Thin ctypes binding of the operators in ``include/moe_ops.h``.
 
-Routing of tokens to experts, movement of rows into and out of the packed
-128-row groups, the experts' gated feed-forward block with its backward pass
-and its single-token form, and low-rank adapters beside a shared projection.
+Routing of tokens to experts, the balance loss of the router, movement of rows
+into and out of the packed 128-row groups, the experts' gated feed-forward block
+with its backward pass (checkpoint in bf16 or in 8 bits) and its single-token
+form, and low-rank adapters beside a shared projection.
 Same manner as ``binding``: every function has the name of its C entry point,
 checks its buffers on the host (ValueError), passes the current stream and
 raises ``Nvfp4GroupError`` on a non-zero status.  Outputs are the caller's.
@@ -10,6 +11,7 @@ raises ``Nvfp4GroupError`` on a non-zero status.  Outputs are the caller's.
 A training step of an expert layer::
 
     moe_route(logits, ids, weights)                       # [T, E] -> [T, k]
+    moe_balance(logits, ids, loss, counts, probs, seq_tokens, workspace, coef=0.01)
     moe_plan(ids, offs, counts, rows, src, status, workspace)
     moe_dispatch(x, rows, src, offs, packed)              # [T, H] -> [capacity, H]
     ...cast packed (binding.nvfp4_group_quantize_graphsafe)...
@@ -34,14 +36,18 @@ MAX_TOPK = 16
 MAX_PAIRS = 1 << 24
 MAX_TOKEN_PAIRS = 1024
 MAX_RANK = 128
+MAX_SEQS = 65535
+KEEP8_GROUP = 32      # columns that share a scale in moe_glu_keep8
 
 EXPORTS = (
-    "moe_route", "moe_route_bwd", "moe_plan_workspace", "moe_plan", "moe_dispatch", "moe_combine",
-    "moe_glu", "moe_glu_graphsafe", "moe_glu_bwd", "moe_glu_bwd_graphsafe", "moe_token_glu", "moe_token_linear",
+    "moe_route", "moe_route_bwd", "moe_balance_workspace", "moe_balance", "moe_balance_bwd", "moe_plan_workspace", "moe_plan", "moe_dispatch", "moe_combine",
+    "moe_glu", "moe_glu_graphsafe", "moe_glu_bwd", "moe_glu_bwd_graphsafe", "moe_glu_keep8",
+    "moe_glu_keep8_graphsafe", "moe_glu_bwd_keep8", "moe_glu_bwd_keep8_graphsafe", "moe_token_glu", "moe_token_linear",
     "lora_workspace", "lora_linear",
 )
 
 B16 = (torch.bfloat16, torch.int16, torch.uint16)
+I8 = (torch.int8,)
 _P, _I64, _I32, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 _NVFP4 = [_P, _P, _P]                                   # data, scale, amax
 _lib = None
@@ -54,6 +60,9 @@ def load_library() -> ctypes.CDLL:
     L = _b.load_library()
     L.moe_route.argtypes = [_P, _I32, _I64, _I32, _I32, _P, _I32, _I32, _F, _P, _P, _P]
     L.moe_route_bwd.argtypes = [_P, _I32, _I64, _I32, _I32, _P, _P, _I32, _I32, _F, _P, _P]
+    L.moe_balance_workspace.argtypes = [_I64, _I32, _I32]
+    L.moe_balance.argtypes = [_P, _I32, _I64, _I32, _I32, _P, _I32, _P, _I32, _F, _P, _P, _P, _P, _P, _I64, _P]
+    L.moe_balance_bwd.argtypes = [_P, _I32, _I64, _I32, _I32, _I32, _P, _I32, _F, _P, _P, _P, _P, _P, _P]
     L.moe_plan_workspace.argtypes = [_I64, _I32]
     L.moe_plan.argtypes = [_P, _I64, _I32, _I64, _P, _P, _P, _P, _P, _P, _I64, _P]
     L.moe_dispatch.argtypes = [_P, _I64, _I64, _I32, _P, _P, _P, _I32, _I64, _P, _P, _I32, _P, _P, _P]
@@ -62,6 +71,10 @@ def load_library() -> ctypes.CDLL:
     L.moe_glu_graphsafe.argtypes = _NVFP4 * 2 + [_I64, _I64, _I64, _I32, _P, _I32, _P, _P, _P, _P]
     L.moe_glu_bwd.argtypes = _NVFP4 * 2 + [_I64, _I64, _I64, _I32, _P, _P, _I32, _P, _P]
     L.moe_glu_bwd_graphsafe.argtypes = _NVFP4 * 2 + [_I64, _I64, _I64, _I32, _P, _P, _I32, _P, _P, _P]
+    L.moe_glu_keep8.argtypes = _NVFP4 * 2 + [_I64, _I64, _I64, _I32, _P, _I32, _P, _P, _P, _P]
+    L.moe_glu_keep8_graphsafe.argtypes = _NVFP4 * 2 + [_I64, _I64, _I64, _I32, _P, _I32, _P, _P, _P, _P, _P]
+    L.moe_glu_bwd_keep8.argtypes = _NVFP4 * 2 + [_I64, _I64, _I64, _I32, _P, _P, _P, _I32, _P, _P, _P]
+    L.moe_glu_bwd_keep8_graphsafe.argtypes = _NVFP4 * 2 + [_I64, _I64, _I64, _I32, _P, _P, _P, _I32, _P, _P, _P, _P]
     L.moe_token_glu.argtypes = [_P, _I64, _I64, _I32, _P] + _NVFP4 + [_I64, _I32, _I32, _P, _P]
     L.moe_token_linear.argtypes = [_P, _I64, _I64, _P] + _NVFP4 + [_I64, _I32, _P, _P]
     L.lora_workspace.argtypes = [_I64, _I64, _I64, _I32]
@@ -146,6 +159,54 @@ def moe_route_bwd(logits, ids, dweights, dlogits, *, score=SCORE_SOFTMAX, normal
     _check("moe_route_bwd", load_library().moe_route_bwd(
         lp, lt, T, E, k, _buf("ids", ids, I32, T * k, True), _buf("dweights", dweights, F32, T * k, True), int(score),
         int(bool(normalize)), float(scale), _buf("dlogits", dlogits, (logits.dtype,), T * E, True), _stream(stream)))
+
+
+def moe_balance_workspace(tokens: int, num_experts: int, num_seqs: int = 1) -> int:
+    """Bytes of workspace that moe_balance needs."""
+    return int(load_library().moe_balance_workspace(int(tokens), int(num_experts), int(num_seqs)))
+
+
+def _sequences(seq_ends, seq_tokens):
+    S, = _dims("seq_tokens", seq_tokens, 1)
+    if seq_ends is None and S != 1:
+        raise ValueError(f"seq_tokens has {S} entries; without seq_ends there is one sequence")
+    if seq_ends is not None:
+        _shape("seq_ends", seq_ends, (S,))
+    return _buf("seq_ends", seq_ends, I32, S), S
+
+
+def moe_balance(logits, ids, loss, counts, probs, seq_tokens, workspace=None, *, seq_ends=None, score=SCORE_SOFTMAX,
+                coef=1.0, stream=None):
+    """logits [T, E] f32 or bf16, ids [T, k] i32 -> loss [1] f32, counts [S, E] i32, probs [S, E] f32, seq_tokens [S]
+    i32, for the sequences that end at rows seq_ends [S] i32 (None: one of all rows)."""
+    lp, lt, T, E = _logits(logits)
+    k = _dims("ids", ids, 2)[1]
+    _shape("ids", ids, (T, k))
+    ends, S = _sequences(seq_ends, seq_tokens)
+    _shape("counts", counts, (S, E))
+    _shape("probs", probs, (S, E))
+    _check("moe_balance", load_library().moe_balance(
+        lp, lt, T, E, k, _buf("ids", ids, I32, T * k, True), int(score), ends, S, float(coef),
+        _buf("loss", loss, F32, 1, True), _buf("counts", counts, I32, S * E, True),
+        _buf("probs", probs, F32, S * E, True), _buf("seq_tokens", seq_tokens, I32, S, True),
+        _buf("workspace", workspace, U8, 0), 0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+def moe_balance_bwd(logits, counts, seq_tokens, dlogits, *, topk, seq_ends=None, score=SCORE_SOFTMAX, coef=1.0,
+                    dloss=None, add=None, stream=None):
+    """Gradient of moe_balance's loss times dloss [1] f32 (None: 1) -> dlogits [T, E] in the type of logits, plus add
+    [T, E] of that type if given (it may be dlogits)."""
+    lp, lt, T, E = _logits(logits)
+    ends, S = _sequences(seq_ends, seq_tokens)
+    _shape("counts", counts, (S, E))
+    _shape("dlogits", dlogits, (T, E))
+    if add is not None:
+        _shape("add", add, (T, E))
+    _check("moe_balance_bwd", load_library().moe_balance_bwd(
+        lp, lt, T, E, int(topk), int(score), ends, S, float(coef), _buf("counts", counts, I32, S * E, True),
+        _buf("seq_tokens", seq_tokens, I32, S, True), _buf("dloss", dloss, F32, 1),
+        _buf("add", add, (logits.dtype,), T * E), _buf("dlogits", dlogits, (logits.dtype,), T * E, True),
+        _stream(stream)))
 
 
 def moe_plan_workspace(pairs: int, num_experts: int) -> int:
@@ -276,6 +337,57 @@ def moe_glu_bwd_graphsafe(a_data, a_scale, a_amax, b_data, b_scale, b_amax, d_of
         *ptrs, m, f, k, E, do, gp, int(act), dp, ds, _stream(stream)))
 
 
+def _kept(gu8, gu_scale, m, f):
+    """8-bit checkpoint of m rows: codes [m, 2f] and bf16 scales [2 * ceil(f / 32), m]."""
+    _shape("gu8", gu8, (m, 2 * f))
+    _shape("gu_scale", gu_scale, (2 * -(-f // KEEP8_GROUP), m))
+    return _buf("gu8", gu8, I8, 2 * m * f, True), _buf("gu_scale", gu_scale, B16, gu_scale.numel(), True)
+
+
+def moe_glu_keep8(a_data, a_scale, a_amax, b_data, b_scale, b_amax, h_splits, h, gu8, gu_scale, act=ACT_SILU,
+                  stream=None):
+    """moe_glu that keeps g and u in 8 bits: gu8 [sum_m, 2f] i8, gu_scale [2 * ceil(f / 32), sum_m] bf16."""
+    ptrs, m, E, f, k = _glu_operands(a_data, a_scale, a_amax, b_data, b_scale, b_amax)
+    qp, sp = _kept(gu8, gu_scale, m, f)
+    _check("moe_glu_keep8", load_library().moe_glu_keep8(
+        *ptrs, m, f, k, E, _host_splits(h_splits, E), int(act), _buf("h", h, B16, m * f, True), qp, sp,
+        _stream(stream)))
+
+
+def moe_glu_keep8_graphsafe(a_data, a_scale, a_amax, b_data, b_scale, b_amax, d_offs, h, gu8, gu_scale, d_status,
+                            act=ACT_SILU, stream=None):
+    ptrs, m, E, f, k = _glu_operands(a_data, a_scale, a_amax, b_data, b_scale, b_amax)
+    do, ds = _routing(E, d_offs, d_status)
+    qp, sp = _kept(gu8, gu_scale, m, f)
+    _check("moe_glu_keep8_graphsafe", load_library().moe_glu_keep8_graphsafe(
+        *ptrs, m, f, k, E, do, int(act), _buf("h", h, B16, m * f, True), qp, sp, ds, _stream(stream)))
+
+
+def _bwd_keep8_operands(a_data, a_scale, a_amax, b_data, b_scale, b_amax, gu8, gu_scale, dgu, h):
+    a, m, k = _rows_operand(a_data, a_scale, a_amax)
+    b, E, f = _expert_operand(b_data, b_scale, b_amax, k)
+    return (a + b, m, E, f, k, *_kept(gu8, gu_scale, m, f), _buf("dgu", dgu, B16, 2 * m * f, True),
+            _buf("h", h, B16, m * f))
+
+
+def moe_glu_bwd_keep8(a_data, a_scale, a_amax, b_data, b_scale, b_amax, h_splits, gu8, gu_scale, dgu, h=None,
+                      act=ACT_SILU, stream=None):
+    """moe_glu_bwd on what moe_glu_keep8 kept -> dgu [sum_m, 2f] bf16, and h [sum_m, f] bf16 again if given."""
+    ptrs, m, E, f, k, qp, sp, dp, hp = _bwd_keep8_operands(a_data, a_scale, a_amax, b_data, b_scale, b_amax, gu8,
+                                                           gu_scale, dgu, h)
+    _check("moe_glu_bwd_keep8", load_library().moe_glu_bwd_keep8(
+        *ptrs, m, f, k, E, _host_splits(h_splits, E), qp, sp, int(act), dp, hp, _stream(stream)))
+
+
+def moe_glu_bwd_keep8_graphsafe(a_data, a_scale, a_amax, b_data, b_scale, b_amax, d_offs, gu8, gu_scale, dgu, d_status,
+                                h=None, act=ACT_SILU, stream=None):
+    ptrs, m, E, f, k, qp, sp, dp, hp = _bwd_keep8_operands(a_data, a_scale, a_amax, b_data, b_scale, b_amax, gu8,
+                                                           gu_scale, dgu, h)
+    do, ds = _routing(E, d_offs, d_status)
+    _check("moe_glu_bwd_keep8_graphsafe", load_library().moe_glu_bwd_keep8_graphsafe(
+        *ptrs, m, f, k, E, do, qp, sp, int(act), dp, hp, ds, _stream(stream)))
+
+
 def moe_token_glu(x, ids, b_data, b_scale, b_amax, h, act=ACT_SILU, stream=None):
     """x [T, k] bf16, ids [T, topk] i32, b as in moe_glu -> h [T * topk, f] bf16."""
     T, k = _dims("x", x, 2)
@@ -345,3 +457,18 @@ def alloc_plan(tokens: int, topk: int, num_experts: int, m_capacity: int | None 
             "rows": torch.empty((tokens, topk), **i32), "src": torch.empty(cap, **i32),
             "d_status": torch.zeros(1, **i32),
             "workspace": torch.empty(moe_plan_workspace(tokens * topk, num_experts), dtype=torch.uint8, device=device)}
+
+
+def alloc_balance(tokens: int, num_experts: int, num_seqs: int = 1, device="cuda"):
+    """Buffers of moe_balance, in the order of its arguments after ids."""
+    i32, f32 = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
+    need = moe_balance_workspace(tokens, num_experts, num_seqs)
+    return {"loss": torch.empty(1, **f32), "counts": torch.empty((num_seqs, num_experts), **i32),
+            "probs": torch.empty((num_seqs, num_experts), **f32), "seq_tokens": torch.empty(num_seqs, **i32),
+            "workspace": torch.empty(need, dtype=torch.uint8, device=device)}
+
+
+def alloc_keep8(rows: int, f: int, device="cuda"):
+    """Buffers of the 8-bit checkpoint of ``rows`` packed rows, f columns of g and of u."""
+    return {"gu8": torch.empty((rows, 2 * f), dtype=torch.int8, device=device),
+            "gu_scale": torch.empty((2 * -(-f // KEEP8_GROUP), rows), dtype=torch.bfloat16, device=device)}
