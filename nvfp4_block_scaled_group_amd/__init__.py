@@ -6,4 +6,4 @@ The work is done by hand-written HIP kernels behind a C-ABI library
 ctypes layer with the same entry-point names.  Importing this package loads
 nothing: the library is loaded on first use, and a missing library is an error.
 """
-__all__ = ["binding", "moe", "synth"]
+__all__ = ["binding", "i8", "moe", "synth"]

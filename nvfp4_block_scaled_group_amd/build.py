@@ -2,9 +2,9 @@
 
     python -m nvfp4_block_scaled_group_amd.build
 
-Compiles ``csrc/*.hip`` and ``csrc/moe/*.hip`` with hipcc for gfx950 and links
-a plain shared library exporting the C ABI of ``include/nvfp4_group.h`` and
-``include/moe_ops.h``; also builds
+Compiles ``csrc/*.hip``, ``csrc/moe/*.hip`` and ``csrc/i8/*.hip`` with hipcc for
+gfx950 and links a plain shared library exporting the C ABI of
+``include/nvfp4_group.h``, ``include/moe_ops.h`` and ``include/i8_group.h``; also builds
 ``probe/libhbmprobe.so`` (the benchmark's memory-ceiling kernels, not part
 of that ABI).  The library's dependency on
 the HIP runtime is recorded as ``libamdhip64.so`` (the name PyTorch's ROCm
@@ -55,7 +55,7 @@ def _hip_runtime_dir() -> str:
 def build(verbose: bool = False) -> str:
     hipcc = shutil.which("hipcc") or os.path.join(ROCM, "bin", "hipcc")
     os.makedirs(BUILD_DIR, exist_ok=True)
-    sources = sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + sorted(glob.glob(os.path.join(CSRC, "moe", "*.hip")))
+    sources = [src for part in ("", "moe", "i8") for src in sorted(glob.glob(os.path.join(CSRC, part, "*.hip")))]
     objs = [os.path.join(BUILD_DIR, os.path.basename(src) + ".o") for src in sources]
 
     def compile_one(src: str, obj: str) -> None:

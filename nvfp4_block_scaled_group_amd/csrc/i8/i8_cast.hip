@@ -1,0 +1,126 @@
+// i8_cast.hip -- cast of bf16 rows to 8-bit integers with a scale for each
+// row, behind the C ABI of include/i8_group.h.
+//
+// It reads 2 bytes an element and writes 1: memory bounds it.  A wave takes a
+// row whose values stay in registers between the maximum and the codes (up to
+// 8192 columns); longer rows take a work-group, which reads them twice.
+#include "i8_common.hpp"
+
+namespace {
+
+using namespace i8;
+
+constexpr int kSegCols = 512;  // a wave's 16-byte loads: 8 columns a lane
+constexpr int kRegSegs = 16;
+
+// Rows that exist: all of them, or the routed ones.
+__device__ __forceinline__ bool routed_rows(const Routing& R, int64_t* rows) {
+  if (R.d_offs) {
+    if (!routing_ok(R)) return false;
+    *rows = route_end(R, R.num_experts - 1);
+  }
+  return true;
+}
+
+template <int SEGS>
+__global__ __launch_bounds__(kThreads) void cast_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t k,
+                                                             Routing R, int8_t* __restrict__ q,
+                                                             float* __restrict__ scale) {
+  if (!routed_rows(R, &rows)) return;
+  const int lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)line_index() * (kThreads / 64) + uni((int32_t)(threadIdx.x >> 6));
+  if (r >= rows) return;
+  const rsrc_t xr = range_rsrc(x + r * k, 2 * k);
+  u32x4 v[SEGS];
+#pragma unroll
+  for (int s = 0; s < SEGS; ++s)
+    v[s] = __builtin_amdgcn_raw_buffer_load_b128(xr, 16 * lane, s * 2 * kSegCols, kLoadStream);
+  uint32_t m = 0;
+#pragma unroll
+  for (int s = 0; s < SEGS; ++s) m = max(m, abs_max8(v[s]));
+  m = wave_reduce(m, [](uint32_t a, uint32_t b) { return max(a, b); });
+  const RowCast c = row_cast(m);
+  if (lane == 0) scale[r] = c.scale;
+#pragma unroll
+  for (int s = 0; s < SEGS; ++s) {
+    const int64_t col = s * kSegCols + 8 * lane;
+    if (col < k) *reinterpret_cast<u32x2*>(q + r * k + col) = cast8(v[s], c);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void cast_long_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t k,
+                                                             Routing R, int8_t* __restrict__ q,
+                                                             float* __restrict__ scale) {
+  __shared__ uint32_t lmax[kThreads / 64];
+  if (!routed_rows(R, &rows)) return;
+  const int64_t r = line_index();
+  if (r >= rows) return;
+  const u32x4* row = reinterpret_cast<const u32x4*>(x + r * k);
+  uint32_t m = 0;
+  for (int64_t i = threadIdx.x; i < k / 8; i += kThreads) m = max(m, abs_max8(row[i]));
+  m = wave_reduce(m, [](uint32_t a, uint32_t b) { return max(a, b); });
+  if ((threadIdx.x & 63) == 0) lmax[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) m = max(m, lmax[w]);
+  const RowCast c = row_cast(m);
+  if (threadIdx.x == 0) scale[r] = c.scale;
+  for (int64_t i = threadIdx.x; i < k / 8; i += kThreads) *reinterpret_cast<u32x2*>(q + r * k + 8 * i) = cast8(row[i], c);
+}
+
+template <int SEGS>
+void launch(const uint16_t* x, int64_t rows, int64_t k, const Routing& R, int8_t* q, float* scale, hipStream_t st) {
+  const uint32_t per = kThreads / 64;
+  hipLaunchKernelGGL((cast_rows_kernel<SEGS>), line_grid((uint32_t)((rows + per - 1) / per)), dim3(kThreads), 0, st, x,
+                     rows, k, R, q, scale);
+}
+
+int cast(const uint16_t* x, int64_t rows, int64_t k, const Routing& R, int8_t* q, float* scale, hipStream_t st) {
+  const int64_t segs = (k + kSegCols - 1) / kSegCols;
+  if (segs <= 1) launch<1>(x, rows, k, R, q, scale, st);
+  else if (segs <= 2) launch<2>(x, rows, k, R, q, scale, st);
+  else if (segs <= 4) launch<4>(x, rows, k, R, q, scale, st);
+  else if (segs <= 8) launch<8>(x, rows, k, R, q, scale, st);
+  else if (segs <= 12) launch<12>(x, rows, k, R, q, scale, st);
+  else if (segs <= 14) launch<14>(x, rows, k, R, q, scale, st);
+  else if (segs <= kRegSegs) launch<kRegSegs>(x, rows, k, R, q, scale, st);
+  else
+    hipLaunchKernelGGL(cast_long_kernel, line_grid((uint32_t)rows), dim3(kThreads), 0, st, x, rows, k, R, q, scale);
+  return hip_status();
+}
+
+int check_cast(const uint16_t* x, int64_t rows, int64_t k, const int8_t* q, const float* scale) {
+  if (!valid_k(k) || rows < 0 || rows > kMaxRows) return NVFP4G_EINVAL;
+  if (rows && (!x || !q || !scale)) return NVFP4G_EINVAL;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return NVFP4G_EALIGN;
+  return NVFP4G_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int i8_group_cast(const uint16_t* x, int64_t rows, int64_t k, int8_t* q, float* scale, void* stream) {
+  const int rc = check_cast(x, rows, k, q, scale);
+  if (rc || rows == 0) return rc;
+  Routing R;
+  R.num_experts = 0;
+  R.m_capacity = (int32_t)rows;
+  R.d_offs = nullptr;
+  R.d_status = nullptr;
+  return cast(x, rows, k, R, q, scale, (hipStream_t)stream);
+}
+
+int i8_group_cast_graphsafe(const uint16_t* x, int64_t m_capacity, int64_t k, int32_t num_experts,
+                            const int32_t* d_offs, int8_t* q, float* scale, int32_t* d_status, void* stream) {
+  int rc = check_cast(x, m_capacity, k, q, scale);
+  if (rc) return rc;
+  Routing R;
+  R.num_experts = num_experts;
+  R.m_capacity = (int32_t)m_capacity;
+  if ((rc = graph_routing(d_offs, d_status, num_experts, m_capacity, &R))) return rc;
+  if (m_capacity == 0) return NVFP4G_OK;
+  return cast(x, m_capacity, k, R, q, scale, (hipStream_t)stream);
+}
+
+}  // extern "C"
