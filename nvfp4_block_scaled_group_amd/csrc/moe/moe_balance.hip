@@ -26,6 +26,7 @@ constexpr int kFwdThreads = 1024;
 // Threads of the forward pass: many experts a lane need the registers of many waves.
 constexpr int fwd_threads(int vpl) { return vpl <= 16 ? kFwdThreads : kFwdThreads / 4; }
 constexpr int kChunks = 256;    // chunks of a large batch: one for each CU
+constexpr int kMinChunk = 128;  // rows of a chunk at least
 constexpr int kJoinCols = 32;   // columns of a joining work-group
 
 // The first sequence whose end is above row t (num_seqs if none): the row's
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const T* __restri
 
 // ------------------------------------------------------------- host side
 
-int64_t chunk_rows(int64_t tokens) { return std::max<int64_t>(128, (tokens + kChunks - 1) / kChunks); }
+int64_t chunk_rows(int64_t tokens) { return std::max<int64_t>(kMinChunk, (tokens + kChunks - 1) / kChunks); }
 int64_t chunk_count(int64_t tokens) { return (tokens + chunk_rows(tokens) - 1) / chunk_rows(tokens); }
 bool one_group(int64_t tokens, int num_seqs) { return num_seqs == 1 && chunk_count(tokens) <= 1; }
 int64_t join_blocks(int E) { return (E + kJoinCols - 1) / kJoinCols; }
@@ -370,7 +371,9 @@ int64_t moe_balance_workspace(int64_t tokens, int32_t num_experts, int32_t num_s
       num_seqs > MOE_MAX_SEQS)
     return NVFP4G_EINVAL;
   if (one_group(tokens, num_seqs)) return 0;
-  return (chunk_count(tokens) + num_seqs) * (8 * (int64_t)num_experts + 4) + 4 * num_seqs * join_blocks(num_experts);
+  // more rows never need fewer bytes, though they may make fewer chunks
+  const int64_t chunks = std::min<int64_t>(kChunks, (tokens + kMinChunk - 1) / kMinChunk);
+  return (chunks + num_seqs) * (8 * (int64_t)num_experts + 4) + 4 * num_seqs * join_blocks(num_experts);
 }
 
 int moe_balance(const void* logits, int32_t logits_type, int64_t tokens, int32_t num_experts, int32_t topk,

@@ -1,0 +1,206 @@
+"""The experts' gated block with its checkpoint in 8 bits on the GPU, forward
+and backward, against the plain 64-bit implementation and the bf16 form."""
+import numpy as np
+import pytest
+import torch
+
+import i8_reference as I
+import moe_reference as R
+from gpu_helpers import CANARY, Guarded, log
+from nvfp4_block_scaled_group_amd import binding as B
+from nvfp4_block_scaled_group_amd import moe
+from test_gpu_moe_glu import ACTS, CASES, WIDE, case, factor, on_device, products
+
+pytestmark = pytest.mark.gpu
+
+
+def groups(f):
+    return 2 * -(-f // 32)
+
+
+def kept_buffers(M, f):
+    return Guarded(2 * M * f, torch.int8, (M, 2 * f)), Guarded(2 * M * groups(f), torch.bfloat16, (groups(f), M))
+
+
+@pytest.mark.parametrize("splits,f,k", CASES + WIDE["forward"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_forward(splits, f, k, kind):
+    log(f"keep8 {splits} f={f} k={k} {kind}")
+    rng, M, E, a, b = case(f + k + 3, splits, f, k, 2 * f)
+    dev = on_device(a, b, E, 2 * f)
+    h, (q, s) = Guarded(2 * M * f, torch.bfloat16, (M, f)), kept_buffers(M, f)
+    moe.moe_glu_keep8(*dev, splits, h.t, q.t, s.t, act=ACTS[kind])
+    plain = torch.empty((M, f), dtype=torch.bfloat16, device="cuda:0")
+    moe.moe_glu(*dev, splits, plain, act=ACTS[kind])
+    torch.cuda.synchronize()
+    assert h.guards_intact() and q.guards_intact() and s.guards_intact()
+    assert torch.equal(h.t, plain)
+    gu, err = products(a, b, splits, 2 * f, k)
+    got, step = I.kept_values(q.t, s.t, f)
+    codes = q.numpy().astype(np.int64)
+    assert np.abs(codes).max() <= 127
+    # half a step, the products' error, and two roundings of a value of at most 127.5 steps
+    assert (np.abs(got - gu) <= step * (0.5 + 128 * 4 * R.U) + err + np.abs(gu) * (step == 0)).all()
+    # the scale: the group's largest magnitude over 127, rounded to bf16
+    scales = s.t.double().cpu().numpy().T
+    at = I.group_of(f)
+    for j in range(groups(f)):
+        top, off = np.abs(gu[:, at == j]).max(1), err[:, at == j].max(1)
+        want = top / 127
+        assert (np.abs(scales[:, j] - want) <= R.UB * want + 1.02 * off / 127 + 1e-30).all()
+        zero = top + off < 2.0 ** -112
+        assert (scales[zero, j] == 0).all() and (codes[zero][:, at == j] == 0).all()
+
+
+def random_kept(rng, M, f, power_of_two=False):
+    q = rng.integers(-127, 128, (M, 2 * f), dtype=np.int8)
+    s = np.exp(rng.standard_normal((groups(f), M))) * 0.03
+    s = 2.0 ** np.round(np.log2(s)) if power_of_two else s
+    s[rng.random(s.shape) < 0.05] = 0.0
+    return torch.from_numpy(q), R.bf16_round(s)[0]
+
+
+@pytest.mark.parametrize("splits,f,k", CASES + WIDE["backward"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_backward(splits, f, k, kind):
+    log(f"keep8 bwd {splits} f={f} k={k} {kind}")
+    rng, M, E, a, b = case(f + k + 4, splits, f, k, f)
+    dev = on_device(a, b, E, f)
+    q, s = random_kept(rng, M, f)
+    gu, _ = I.kept_values(q, s, f)
+    dh, err = products(a, b, splits, f, k)
+    out, again = Guarded(4 * M * f, torch.bfloat16, (M, 2 * f)), Guarded(2 * M * f, torch.bfloat16, (M, f))
+    moe.moe_glu_bwd_keep8(*dev, splits, q.to("cuda:0"), s.to("cuda:0"), out.t, h=again.t, act=ACTS[kind])
+    alone = torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0")
+    moe.moe_glu_bwd_keep8(*dev, splits, q.to("cuda:0"), s.to("cuda:0"), alone, act=ACTS[kind])
+    torch.cuda.synchronize()
+    assert out.guards_intact() and again.guards_intact() and torch.equal(out.t, alone)
+    g, u = gu[:, :f], gu[:, f:]
+    v, d = R.act(g, kind)
+    rel = R.act_rel(g, kind)
+    # a kept value is exact in fp32, so the errors are those of the bf16 form
+    want = np.concatenate([dh * u * d, dh * v], 1)
+    slope = rel * (np.abs(d) + 1) + np.abs(v) * 8 * R.U * (1 + g ** 2)
+    eg = err * np.abs(u) * (np.abs(d) + slope) + np.abs(dh * u) * (slope + 8 * R.U)
+    eu = err * np.abs(v) * (1 + rel) + np.abs(dh * v) * (rel + 8 * R.U)
+    e = np.concatenate([eg, eu], 1) + 1e-30
+    R.check(out.t, want, e + R.UB * (np.abs(want) + e), "dgu")
+    R.check(again.t, v * u, R.glu_bound(g, u, 0 * g, 0 * u, kind), "h")
+
+
+@pytest.mark.parametrize("splits,f,k", [CASES[3], WIDE["backward"][0]])
+def test_backward_equals_the_bf16_form_on_values_that_both_hold(splits, f, k):
+    rng, M, E, a, b = case(6, splits, f, k, f)
+    dev = on_device(a, b, E, f)
+    q, s = random_kept(rng, M, f, power_of_two=True)
+    gu = torch.from_numpy(I.kept_values(q, s, f)[0]).to(torch.bfloat16).to("cuda:0")
+    got, want = (torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0") for _ in range(2))
+    moe.moe_glu_bwd_keep8(*dev, splits, q.to("cuda:0"), s.to("cuda:0"), got)
+    moe.moe_glu_bwd(*dev, splits, gu, want)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_backward_follows_differences(kind):
+    """dh is exact here; the loss sum(dh * act(g) * u) is differenced in 64 bits at the kept values."""
+    rng = np.random.default_rng(2)
+    f, k, M = 48, 128, 128
+    a = (np.full((M, k // 2), 0x22, np.uint8), np.full((M, k // 16), 0x38, np.uint8), np.full(M, 2688, np.float32))
+    b = (rng.integers(0, 3, (f, k // 2), dtype=np.uint8) * 2, np.full((f, k // 16), 0x38, np.uint8), np.full(f, 2688, np.float32))
+    q, s = random_kept(rng, M, f)
+    gu, _ = I.kept_values(q, s, f)
+    out = torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0")
+    moe.moe_glu_bwd_keep8(*on_device(a, b, 1, f), [M], q.to("cuda:0"), s.to("cuda:0"), out, act=ACTS[kind])
+    dh, _ = R.product(R.decode(*a[:2]), factor(a[2]), R.decode(*b[:2]), factor(b[2]))
+    eps, num = 1e-5, np.empty((M, 2 * f))
+    for c in range(2):
+        d = np.zeros((M, 2 * f))
+        d[:, c * f:(c + 1) * f] = eps
+        up, down = gu + d, gu - d
+        num[:, c * f:(c + 1) * f] = dh * (R.act(up[:, :f], kind)[0] * up[:, f:] - R.act(down[:, :f], kind)[0] * down[:, f:]) / (2 * eps)
+    R.check(out, num, R.UB * np.abs(num) * 1.01 + 1e-5 * (1 + np.abs(dh).max()) * (1 + np.abs(gu).max()), "dgu")
+
+
+def test_a_step_through_the_checkpoint():
+    """Forward, then backward on what it kept: near the bf16 form's gradients, by the size of the steps."""
+    splits, f, k, kd = [256, 0, 384], 208, 256, 384
+    rng, M, E, a, b = case(31, splits, f, k, 2 * f)
+    _, _, _, da, db = case(32, splits, f, kd, f)
+    fwd, bwd = on_device(a, b, E, 2 * f), on_device(da, db, E, f)
+    h, again = (torch.empty((M, f), dtype=torch.bfloat16, device="cuda:0") for _ in range(2))
+    kept, d8 = moe.alloc_keep8(M, f), torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0")
+    moe.moe_glu_keep8(*fwd, splits, h, **kept)
+    moe.moe_glu_bwd_keep8(*bwd, splits, **kept, dgu=d8, h=again)
+    gu, _ = products(a, b, splits, 2 * f, k)
+    got, _ = I.kept_values(kept["gu8"], kept["gu_scale"], f)
+    dh, err = products(da, db, splits, f, kd)
+    g, u = got[:, :f], got[:, f:]
+    v, d = R.act(g, "silu")
+    want = np.concatenate([dh * u * d, dh * v], 1)
+    mag = np.concatenate([err * np.abs(u) * 1.2 + np.abs(dh * u) * 64 * R.U, (err + np.abs(dh) * 64 * R.U) * (np.abs(v) + 1)], 1)
+    R.check(d8, want, mag * 2 + R.UB * np.abs(want) * 1.01 + 1e-30, "dgu")
+    assert np.abs(got - gu).max() <= np.abs(gu).max() / 127 * 0.51
+
+
+def test_groups_that_are_no_numbers_or_nothing():
+    splits, f, k = [256], 80, 128
+    rng, M, E, a, b = case(9, splits, f, k, 2 * f)
+    a[2][:] = 1.0
+    a[2][3], a[2][5], a[2][7], a[2][9] = np.inf, 0.0, 1e-36, np.nan
+    b[2][:] = 1.0
+    b[2][40] = np.inf                                # gate column 40: group 1 of g, every row
+    b[2][f:f + 16] = 1e-3
+    dev = on_device(a, b, E, 2 * f)
+    h, kept = torch.empty((M, f), dtype=torch.bfloat16, device="cuda:0"), moe.alloc_keep8(M, f)
+    moe.moe_glu_keep8(*dev, splits, h, **kept)
+    s, q = kept["gu_scale"].float().cpu().numpy(), kept["gu8"].cpu().numpy()
+    bad = np.zeros((groups(f), M), bool)
+    bad[:, 3] = bad[:, 9] = True
+    bad[1, :] = True
+    assert np.array_equal(np.isnan(s), bad)
+    at = I.group_of(f)
+    assert (q[bad.T[:, at]] == 0).all()
+    assert (s[:, 5][~bad[:, 5]] == 0).all() and (q[5] == 0).all() and (s[:, 7][~bad[:, 7]] == 0).all() and (q[7] == 0).all()
+    # a scale that is no number reaches its own group's gradients alone
+    _, _, _, da, db = case(10, splits, f, k, f)
+    d, again = torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0"), torch.empty((M, f), dtype=torch.bfloat16, device="cuda:0")
+    moe.moe_glu_bwd_keep8(*on_device(da, db, E, f), splits, **kept, dgu=d, h=again)
+    nan = torch.isnan(again).cpu().numpy()
+    gbad, ubad = bad.T[:, at[:f]], bad.T[:, at[f:]]
+    assert np.array_equal(nan, gbad | ubad)
+    assert np.isfinite(d.float().cpu().numpy()[~np.concatenate([gbad | ubad, gbad], 1)]).all()
+
+
+@pytest.mark.parametrize("splits,f,k,spare", [([128, 0, 256], 48, 256, 256), (*WIDE["forward"][0], 640)])
+def test_device_routing_writes_the_routed_rows_alone(splits, f, k, spare):
+    rng, M, E, a, b = case(17, splits, f, k, 2 * f)
+    _, _, _, da, db = case(18, splits, f, k, f)
+    cap = M + spare
+    pad = lambda o: [np.concatenate([v, np.full((spare, *v.shape[1:]), 0x7F, v.dtype)]) for v in o]  # noqa: E731
+    fwd, bwd = on_device(pad(a), b, E, 2 * f), on_device(pad(da), db, E, f)
+    h, again, d = (Guarded(2 * cap * w, torch.bfloat16, (cap, w)) for w in (f, f, 2 * f))
+    q, s = kept_buffers(cap, f)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    offs = torch.tensor(B.offsets_from_splits(splits), dtype=torch.int32, device="cuda:0")
+    moe.moe_glu_keep8_graphsafe(*fwd, offs, h.t, q.t, s.t, status)
+    moe.moe_glu_bwd_keep8_graphsafe(*bwd, offs, q.t, s.t, d.t, status, h=again.t)
+    kept = moe.alloc_keep8(M, f)
+    wh, wagain, wd = (torch.empty((M, w), dtype=torch.bfloat16, device="cuda:0") for w in (f, f, 2 * f))
+    moe.moe_glu_keep8(*on_device(a, b, E, 2 * f), splits, wh, **kept)
+    moe.moe_glu_bwd_keep8(*on_device(da, db, E, f), splits, **kept, dgu=wd, h=wagain)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and all(g.guards_intact() for g in (h, again, d, q, s))
+    for got, want in ((h.t[:M], wh), (again.t[:M], wagain), (d.t[:M], wd), (q.t[:M], kept["gu8"]),
+                      (s.t[:, :M], kept["gu_scale"])):
+        assert torch.equal(got, want)
+    for rest in (h.t[M:], again.t[M:], d.t[M:], q.t[M:], s.t[:, M:]):
+        assert (rest.contiguous().view(torch.uint8) == CANARY).all()
+    for bad, bit in (([100] + [M] * (E - 1), B.NVFP4G_DEV_UNALIGNED), ([M, 0] + [M] * (E - 2), B.NVFP4G_DEV_NONMONO),
+                     ([0] * (E - 1) + [cap + 128], B.NVFP4G_DEV_OVERFLOW)):
+        h, (q, s) = Guarded(2 * cap * f, torch.bfloat16, (cap, f)), kept_buffers(cap, f)
+        status.zero_()
+        moe.moe_glu_keep8_graphsafe(*fwd, torch.tensor(bad, dtype=torch.int32, device="cuda:0"), h.t, q.t, s.t, status)
+        torch.cuda.synchronize()
+        assert int(status) & bit
+        for g in (h, q, s):
+            assert (g.t.contiguous().view(torch.uint8) == CANARY).all()
