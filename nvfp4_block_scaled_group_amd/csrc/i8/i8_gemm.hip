@@ -8,27 +8,29 @@
 // matrix instruction are exact, so the order of the contraction is free.
 #include <algorithm>
 
-#include "i8_common.hpp"
+#include "i8_token.hpp"
 
 namespace {
 
 using namespace i8;
 
-constexpr int kBK = 128;  // contraction step: bytes (and elements) of a line in a stage
-
-enum Epilogue { kOutF32, kOutBf16, kGluSilu, kGluGelu };
+enum Epilogue { kOutF32, kOutBf16, kGluSilu, kGluGelu, kParts };
 constexpr bool is_glu(Epilogue e) { return e == kGluSilu || e == kGluGelu; }
 
-// A work-group's tile: WM x WN waves of TM x TN MFMA tiles (32 x 32 each).
-template <int WM_, int WN_, int TM_, int TN_>
+// A work-group's tile: WM x WN waves of TM x TN MFMA tiles (32 x 32 each), BK
+// bytes of a line in a stage, NS stages in LDS, OCC waves on a SIMD.
+template <int WM_, int WN_, int TM_, int TN_, int BK_, int NS_, int OCC_>
 struct Shape {
-  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;
+  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, BK = BK_, NS = NS_, OCC = OCC_;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
-  static constexpr int kStageBytes = (BM + BN) * kBK;
-  static constexpr int kCopyLines = 8 * kWaves;  // of one copy: 8 lines of 128 bytes a wave
-  static constexpr int kCopiesA = BM / kCopyLines, kCopiesB = BN / kCopyLines;
-  static_assert(BM % kCopyLines == 0 && BN % kCopyLines == 0, "copies are whole");
+  static constexpr int kStageBytes = (BM + BN) * BK;
+  static constexpr int kSlots = BK / 16;             // 16-byte granules of a line in a stage
+  static constexpr int kWaveLines = 64 / kSlots;     // lines of a wave's copy
+  static constexpr int kCopyLines = kWaveLines * kWaves;
+  static constexpr int kCopiesA = BM / kCopyLines, kCopiesB = BN / kCopyLines, kCopies = kCopiesA + kCopiesB;
+  static_assert(BM % kCopyLines == 0 && BN % kCopyLines == 0 && kCopyLines % 16 == 0, "copies are whole");
+  static_assert(NS == 2 || NS == 4, "stages");
 };
 
 // One operand: the lines of a tile, `valid` (at least 1) of which exist (others read 0).
@@ -37,74 +39,171 @@ struct Lines {
   uint32_t valid;
 };
 
-// 16-byte granule q of a line sits at slot q ^ (line % 8): a fragment read of
-// 32 consecutive lines at one granule then spreads over all banks.
-__device__ __forceinline__ uint32_t swz(uint32_t line, uint32_t q) { return q ^ (line & 7u); }
+// 16-byte granule q of a line sits at a slot that makes sixteen consecutive
+// lines at one granule, which an LDS read serves at once, meet all 64 banks:
+// two lines of 128 bytes, or four of 64, go once around them.
+template <class S>
+__device__ __forceinline__ uint32_t swz(uint32_t line, uint32_t q) {
+  return S::BK == 128 ? q ^ ((line >> 1) & 7u) : q ^ ((line >> 2) & 3u);
+}
 
-// acc[im][in] = A lines x B lines^T over k.  PAIR: B's LDS lines are blocks of
-// 16 TN lines, alternately of B0 (gate) and of B1 (up), so that a wave's first
-// TN / 2 tiles are gate lines and the others the up lines of the same columns.
-// Each step waits for its own copies, passes one barrier, issues the copies of
-// the next step into the other stage and multiplies meanwhile.  The granules of
-// a line's last step past k are copied as zeros.
+// The stages in LDS: arrays of their own, so that reads of one need not wait
+// for copies into the others.
+template <class S>
+struct Stages {
+  uint8_t *p0, *p1, *p2, *p3;
+  template <int I>
+  __device__ __forceinline__ uint8_t* at() const {
+    constexpr int i = I % S::NS;
+    return i == 0 ? p0 : i == 1 ? p1 : i == 2 ? p2 : p3;
+  }
+};
+
+// N products, then one copy, C times.
+template <int N, int C, int I = 0>
+__device__ __forceinline__ void spread_copies() {
+  if constexpr (I < C) {
+    __builtin_amdgcn_sched_group_barrier(0x008, (I + 1) * N / C - I * N / C, 0);
+    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    spread_copies<N, C, I + 1>();
+  }
+}
+// R reads of a substep's fragments between the N products of the one before.
+template <int N, int R, int I = 0>
+__device__ __forceinline__ void spread_reads() {
+  if constexpr (I < R) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, (I + 1) * N / R - I * N / R, 0);
+    spread_reads<N, R, I + 1>();
+  }
+}
+
+// All waves: this wave's LDS reads are done and at most N of its copies are
+// still on their way.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (0 << 8) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// acc[im][in] = A lines x B lines^T over steps ks0 .. ks1 - 1 of the
+// contraction.  PAIR: B's LDS lines are blocks of 16 TN lines, alternately of
+// B0 (gate) and of B1 (up), so that a wave's first TN / 2 tiles are gate lines
+// and the others the up lines of the same columns.  The granules of a line's
+// last step past k are copied as zeros.
+//
+// Fragments are read one substep ahead.  Before the last substep of a step one
+// barrier says that its stage is read by all and that the next one has landed;
+// behind it the copies of the step NS ahead go into the free stage, between the
+// products, and the next stage's first fragments are read.  Steps past the last
+// are copied too, as zeros without a look at memory: the compiler then knows how
+// many copies are on their way everywhere in the loop, and adds no waits.
+// A wave whose rows or columns are all past the last (`live` false) copies and
+// waits with the others but multiplies nothing.
 template <class S, bool PAIR>
-__device__ __forceinline__ void multiply(const Lines& A, const Lines& B0, const Lines& B1, uint32_t k, bool live,
-                                         i32x16 (&acc)[S::TM][S::TN], uint8_t* lds0, uint8_t* lds1) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  const uint32_t wave = uni((uint32_t)(tid >> 6));
-  const rsrc_t ar = range_rsrc(A.data, (int64_t)A.valid * k), b0r = range_rsrc(B0.data, (int64_t)B0.valid * k);
-  const rsrc_t b1r = PAIR ? range_rsrc(B1.data, (int64_t)B1.valid * k) : b0r;
-  constexpr uint32_t kBlock = 16 * S::TN;
-  const uint32_t cl = 8 * wave + (lane >> 3), granule = swz(cl, lane & 7);  // line of the first copy; its granule
-  const uint32_t nk = (k + kBK - 1) / kBK;
-  const uint32_t cut = (nk - 1) * kBK + 16 * granule >= k ? kOutOfRange : 0u;
+struct Multiply {
+  const Lines &A, &B0, &B1;
+  uint32_t k, ks0, ks1;
+  Stages<S> L;
+  rsrc_t ar, b0r, b1r;
+  uint32_t wave, lane, cl, granule, nk, cut;
 
-  auto issue = [&](uint32_t ks, uint8_t* base) {
-    const uint32_t so = ks * kBK, past = ks + 1 == nk ? cut : 0u;
+  __device__ __forceinline__ Multiply(const Lines& a, const Lines& b0, const Lines& b1, uint32_t k_, uint32_t first,
+                                      uint32_t end, Stages<S> l)
+      : A(a), B0(b0), B1(b1), k(k_), ks0(first), ks1(end), L(l) {
+    ar = range_rsrc(A.data, (int64_t)A.valid * k);
+    b0r = range_rsrc(B0.data, (int64_t)B0.valid * k);
+    b1r = PAIR ? range_rsrc(B1.data, (int64_t)B1.valid * k) : b0r;
+    wave = uni((uint32_t)(threadIdx.x >> 6));
+    lane = threadIdx.x & 63;
+    cl = S::kWaveLines * wave + lane / S::kSlots;  // line of the first copy
+    granule = swz<S>(cl, lane % S::kSlots);
+    nk = (k + S::BK - 1) / S::BK;
+    cut = (nk - 1) * S::BK + 16 * granule >= k ? kOutOfRange : 0u;
+  }
+
+  __device__ __forceinline__ void issue(uint32_t ks, uint8_t* base) const {
+    constexpr uint32_t kBlock = 16 * S::TN;
+    static_assert(!PAIR || kBlock % S::kWaveLines == 0, "a wave's copy stays in a block");
+    const uint32_t so = min(ks, nk - 1) * S::BK, past = ks >= ks1 ? kOutOfRange : ks + 1 == nk ? cut : 0u;
 #pragma unroll
     for (int c = 0; c < S::kCopiesA; ++c)
-      copy16(ar, base + (c * S::kCopyLines + 8 * wave) * kBK, ((c * S::kCopyLines + cl) * k + 16 * granule) | past, so);
+      copy16(ar, base + (c * S::kCopyLines + S::kWaveLines * wave) * S::BK,
+             ((c * S::kCopyLines + cl) * k + 16 * granule) | past, so);
 #pragma unroll
     for (int c = 0; c < S::kCopiesB; ++c) {
       const uint32_t at = c * S::kCopyLines + cl;
-      const bool up = PAIR && ((c * S::kCopyLines + 8 * wave) / kBlock) % 2;  // the same for a wave's 8 lines
+      const bool up = PAIR && ((c * S::kCopyLines + S::kWaveLines * wave) / kBlock) % 2;  // the same for a wave's lines
       const uint32_t line = PAIR ? at / kBlock / 2 * kBlock + at % kBlock : at;
-      copy16(up ? b1r : b0r, base + (S::BM + c * S::kCopyLines + 8 * wave) * kBK, (line * k + 16 * granule) | past, so);
+      copy16(up ? b1r : b0r, base + (S::BM + c * S::kCopyLines + S::kWaveLines * wave) * S::BK,
+             (line * k + 16 * granule) | past, so);
     }
-  };
+  }
 
-  const uint32_t wm = wave / S::WN, wn = wave % S::WN, h = lane >> 5;
-  const uint32_t la = wm * (32 * S::TM) + (lane & 31), lb = S::BM + wn * (32 * S::TN) + (lane & 31);
-  auto step = [&](uint32_t ks, const uint8_t* base, uint8_t* next) {
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-    __syncthreads();
-    if (ks + 1 < nk) issue(ks + 1, next);
-    if (!live) return;
+  template <bool LIVE>
+  __device__ __forceinline__ void run(i32x16 (&acc)[S::TM][S::TN]) const {
+    const uint32_t wm = wave / S::WN, wn = wave % S::WN, h = lane >> 5;
+    const uint32_t la = wm * (32 * S::TM) + (lane & 31), lb = S::BM + wn * (32 * S::TN) + (lane & 31);
+    constexpr int kSub = S::BK / 32, kReads = S::TM + S::TN, kMul = S::TM * S::TN;
+    i32x4 a[2][S::TM], b[2][S::TN];
+    auto read = [&](const uint8_t* base, int s, int to) {
+      const uint32_t q = 16 * swz<S>(lane, 2 * s + h);
 #pragma unroll
-    for (int s = 0; s < kBK / 32; ++s) {
-      const uint32_t q = 16 * swz(lane, 2 * s + h);
-      i32x4 a[S::TM], b[S::TN];
+      for (int im = 0; im < S::TM; ++im) a[to][im] = *reinterpret_cast<const i32x4*>(base + (la + 32 * im) * S::BK + q);
 #pragma unroll
-      for (int im = 0; im < S::TM; ++im) a[im] = *reinterpret_cast<const i32x4*>(base + (la + 32 * im) * kBK + q);
-#pragma unroll
-      for (int in = 0; in < S::TN; ++in) b[in] = *reinterpret_cast<const i32x4*>(base + (lb + 32 * in) * kBK + q);
+      for (int in = 0; in < S::TN; ++in) b[to][in] = *reinterpret_cast<const i32x4*>(base + (lb + 32 * in) * S::BK + q);
+    };
+    auto products = [&](int from) {
 #pragma unroll
       for (int im = 0; im < S::TM; ++im)
 #pragma unroll
         for (int in = 0; in < S::TN; ++in)
-          acc[im][in] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[im], b[in], acc[im][in], 0, 0, 0);
-    }
-  };
-  issue(0, lds0);
+          acc[im][in] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[from][im], b[from][in], acc[im][in], 0, 0, 0);
+    };
+    auto step = [&](uint32_t ks, uint8_t* base, const uint8_t* next) {
+      if (LIVE) {
+#pragma unroll
+        for (int s = 0; s + 1 < kSub; ++s) {
+          read(base, s + 1, (s + 1) & 1);
+          products(s & 1);
+          spread_reads<kMul, kReads>();
+        }
+      }
+      stage_barrier<(S::NS - 2) * S::kCopies>();
+      if (LIVE) {
+        read(next, 0, 0);
+        products((kSub - 1) & 1);
+      }
+      issue(ks + S::NS, base);
+      if (LIVE) {
+        __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+        spread_copies<kMul, S::kCopies>();
+      }
+    };
+    issue(ks0, L.template at<0>());
+    issue(ks0 + 1, L.template at<1>());
+    if (S::NS > 2) issue(ks0 + 2, L.template at<2>());
+    if (S::NS > 2) issue(ks0 + 3, L.template at<3>());
+    stage_barrier<(S::NS - 1) * S::kCopies>();
+    if (LIVE) read(L.template at<0>(), 0, 0);
+    uint32_t ks = ks0;
 #pragma unroll 1
-  for (uint32_t ks = 0; ks < nk; ks += 2) {
-    step(ks, lds0, lds1);
-    if (ks + 1 >= nk) break;
-    step(ks + 1, lds1, lds0);
+    for (; ks + S::NS <= ks1; ks += S::NS) {
+      step(ks, L.template at<0>(), L.template at<1>());
+      step(ks + 1, L.template at<1>(), L.template at<2>());
+      if (S::NS == 2) continue;
+      step(ks + 2, L.template at<2>(), L.template at<3>());
+      step(ks + 3, L.template at<3>(), L.template at<0>());
+    }
+    if (ks < ks1) step(ks, L.template at<0>(), L.template at<1>());
+    if (S::NS > 2 && ks + 1 < ks1) step(ks + 1, L.template at<1>(), L.template at<2>());
+    if (S::NS > 2 && ks + 2 < ks1) step(ks + 2, L.template at<2>(), L.template at<3>());
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __syncthreads();
   }
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-  __syncthreads();
-}
+};
 
 // Logical tile: super-tiles of 64 consecutive tiles dealt round-robin to the
 // 8 XCDs, so that each XCD's L2 holds the operand slices its tiles share.
@@ -172,7 +271,7 @@ __device__ __forceinline__ bool row_tile(const Routing& R, bool dense, uint32_t 
   return false;
 }
 
-// A wave's own half of a stage, free in the epilogue: 32 rows x COLS columns of
+// A wave's own piece of a stage, free in the epilogue: 32 rows x COLS columns of
 // fp32 go in as the MFMA layout holds them (column in the lane) and come out as
 // consecutive columns of a row, so that memory sees 16 bytes a lane.
 template <int COLS>
@@ -201,18 +300,27 @@ struct Operands {
 };
 
 // n: columns of the output (f of the gated block, whose experts have 2f lines).
-template <class S, Epilogue EPI, int OCC>
-__global__ __launch_bounds__(S::kThreads, OCC) void product_kernel(Operands O, int64_t n, int64_t k, Routing R,
-                                                                   bool dense, uint32_t ntm, uint32_t ntn,
-                                                                   void* __restrict__ out) {
+// With kParts a work-group sums `per` steps of the contraction: part p of a tile
+// writes its int32 sums to out [parts, rows, n].
+template <class S, Epilogue EPI>
+__global__ __launch_bounds__(S::kThreads, S::OCC) void product_kernel(Operands O, int64_t n, int64_t k, Routing R,
+                                                                      bool dense, uint32_t ntm, uint32_t ntn,
+                                                                      uint32_t per, void* __restrict__ out) {
   constexpr bool GLU = is_glu(EPI);
   constexpr int kCols = GLU ? S::BN / 2 : S::BN, kWaveCols = kCols / S::WN, BLK = kWaveCols / 32;
   __shared__ __attribute__((aligned(16))) uint8_t lds0[S::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t lds1[S::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds2[S::NS > 2 ? S::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t lds3[S::NS > 2 ? S::kStageBytes : 16];
   __shared__ float lsa[S::BM];
   if (!routing_ok(R)) return;
-  uint32_t tm, tn;
-  grouped_tile(xcd_tile(), ntm, ntn, &tm, &tn);
+  uint32_t tm, tn, t = xcd_tile(), part = 0;
+  if (EPI == kParts) {  // the parts of a tile side by side
+    const uint32_t parts = uni(gridDim.x / (ntm * ntn));
+    part = uni(t % parts);
+    t = uni(t / parts);
+  }
+  grouped_tile(t, ntm, ntn, &tm, &tn);
   RowTile T;
   if (!row_tile<S::BM>(R, dense, tm, &T)) return;
   const int64_t col0 = (int64_t)tn * kCols;
@@ -228,15 +336,23 @@ __global__ __launch_bounds__(S::kThreads, OCC) void product_kernel(Operands O, i
   for (int im = 0; im < S::TM; ++im)
 #pragma unroll
     for (int in = 0; in < S::TN; ++in) acc[im][in] = i32x16{};
-  for (int i = tid; i < S::BM; i += S::kThreads) lsa[i] = i < T.rows ? O.a_scale[T.row0 + i] : 0.0f;
-  multiply<S, GLU>(A, B0, B1, (uint32_t)k, live, acc, lds0, lds1);
-  if (!live) return;
+  if (EPI != kParts)
+    for (int i = tid; i < S::BM; i += S::kThreads) lsa[i] = i < T.rows ? O.a_scale[T.row0 + i] : 0.0f;
+  const uint32_t nk = (uint32_t)((k + S::BK - 1) / S::BK);
+  const uint32_t ks0 = EPI == kParts ? part * per : 0, ks1 = EPI == kParts ? min(ks0 + per, nk) : nk;
+  const Multiply<S, GLU> M(A, B0, B1, (uint32_t)k, ks0, ks1, Stages<S>{lds0, lds1, lds2, lds3});
+  if (!live) {
+    M.template run<false>(acc);
+    return;
+  }
+  M.template run<true>(acc);
 
-  constexpr int kHalf = (S::kWaves + 1) / 2;
-  static_assert(kHalf * RowStage<kWaveCols>::kBytes <= S::kStageBytes, "half of the waves share a stage");
-  RowStage<kWaveCols> stage{reinterpret_cast<float*>((wave < kHalf ? lds0 : lds1) +
-                                                     (wave % kHalf) * RowStage<kWaveCols>::kBytes)};
-  constexpr int kPer = EPI == kOutF32 ? 4 : 8;              // columns of a lane's store
+  constexpr int kShare = (S::kWaves + S::NS - 1) / S::NS;  // waves of a stage
+  static_assert(kShare * RowStage<kWaveCols>::kBytes <= S::kStageBytes, "the waves' rows fit the stages");
+  const int own = wave / kShare;
+  RowStage<kWaveCols> stage{reinterpret_cast<float*>((own == 0 ? lds0 : own == 1 ? lds1 : own == 2 ? lds2 : lds3) +
+                                                     (wave % kShare) * RowStage<kWaveCols>::kBytes)};
+  constexpr int kPer = EPI == kOutF32 || EPI == kParts ? 4 : 8;  // columns of a lane's store
   constexpr int kLanes = kWaveCols / kPer, kRows = 64 / kLanes;  // lanes of a row, rows of a store
   const int c = kPer * (lane % kLanes), srow = lane / kLanes;
   const bool inside = wn * kWaveCols + c < (int)cols;
@@ -244,8 +360,9 @@ __global__ __launch_bounds__(S::kThreads, OCC) void product_kernel(Operands O, i
 #pragma unroll
   for (int in = 0; in < S::TN; ++in) {
     const int j = wn * kWaveCols + (in % BLK) * 32 + (lane & 31);
-    sb[in] = j < (int)cols ? O.b_scale[line0 + (GLU && in >= BLK ? n : 0) + j] : 0.0f;
+    sb[in] = EPI != kParts && j < (int)cols ? O.b_scale[line0 + (GLU && in >= BLK ? n : 0) + j] : 0.0f;
   }
+  const int64_t first = EPI == kParts ? part * (int64_t)R.m_capacity : 0;
 #pragma unroll
   for (int im = 0; im < S::TM; ++im) {
     const int r0 = wm * (32 * S::TM) + 32 * im;
@@ -253,12 +370,17 @@ __global__ __launch_bounds__(S::kThreads, OCC) void product_kernel(Operands O, i
     for (int in = 0; in < BLK; ++in)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const float sa = lsa[r0 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
-        float y = ((float)acc[im][in][v] * sa) * sb[in];
-        if constexpr (GLU) {
-          const float u = ((float)acc[im][in + BLK][v] * sa) * sb[in + BLK];
-          float dv;
-          y = y * act_logistic<EPI == kGluSilu ? MOE_ACT_SILU : MOE_ACT_GELU>(y, &dv) * u;
+        float y;
+        if constexpr (EPI == kParts) {
+          y = __int_as_float(acc[im][in][v]);
+        } else {
+          const float sa = lsa[r0 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
+          y = ((float)acc[im][in][v] * sa) * sb[in];
+          if constexpr (GLU) {
+            const float u = ((float)acc[im][in + BLK][v] * sa) * sb[in + BLK];
+            float dv;
+            y = y * act_logistic<EPI == kGluSilu ? MOE_ACT_SILU : MOE_ACT_GELU>(y, &dv) * u;
+          }
         }
         stage.put(in, v, lane, y);
       }
@@ -266,9 +388,9 @@ __global__ __launch_bounds__(S::kThreads, OCC) void product_kernel(Operands O, i
 #pragma unroll
     for (int r = 0; r < 32; r += kRows) {
       const f32x4 lo = stage.get4(r + srow, c);
-      const int64_t at = (T.row0 + r0 + r + srow) * n + col0 + wn * kWaveCols + c;
+      const int64_t at = (first + T.row0 + r0 + r + srow) * n + col0 + wn * kWaveCols + c;
       const bool write = inside && r0 + r + srow < T.rows;
-      if constexpr (EPI == kOutF32) {
+      if constexpr (kPer == 4) {
         if (write) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + at) = lo;
       } else {
         const f32x4 hi = stage.get4(r + srow, c + 4);
@@ -279,6 +401,26 @@ __global__ __launch_bounds__(S::kThreads, OCC) void product_kernel(Operands O, i
     }
     wave_sync();
   }
+}
+
+// Adds the parts of a projection and applies the scales: four columns a lane.
+template <bool F32OUT>
+__global__ __launch_bounds__(kThreads) void join_kernel(const int32_t* __restrict__ parts, int nparts, int64_t rows,
+                                                        int64_t n, const float* __restrict__ a_scale,
+                                                        const float* __restrict__ b_scale, void* __restrict__ out) {
+  const int64_t at = 4 * ((int64_t)line_index() * kThreads + threadIdx.x);
+  if (at >= rows * n) return;
+  const int64_t r = at / n, c = at - r * n;
+  i32x4 s = *reinterpret_cast<const i32x4*>(parts + at);
+  for (int p = 1; p < nparts; ++p) s += *reinterpret_cast<const i32x4*>(parts + p * rows * n + at);
+  const float sa = a_scale[r];
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = ((float)s[i] * sa) * b_scale[c + i];
+  if (F32OUT)
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + at) = f32x4{y[0], y[1], y[2], y[3]};
+  else
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(out) + at) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
 }
 
 // ------------------------------------------------------------- host side
@@ -294,21 +436,83 @@ int64_t row_tiles(const Routing& R, bool dense, int64_t rows) {
   return t;
 }
 
-template <class S, Epilogue EPI, int OCC>
-int launch(const Operands& O, int64_t rows, int64_t n, int64_t k, const Routing& R, bool dense, void* out,
-           hipStream_t st) {
+template <class S, Epilogue EPI>
+int launch(const Operands& O, int64_t rows, int64_t n, int64_t k, const Routing& R, bool dense, int parts, int64_t per,
+           void* out, hipStream_t st) {
   constexpr int kCols = is_glu(EPI) ? S::BN / 2 : S::BN;
-  const int64_t ntm = row_tiles<S::BM>(R, dense, rows), ntn = (n + kCols - 1) / kCols;
-  if (ntm * ntn > (1ll << 32) / S::kThreads - 1) return NVFP4G_EINVAL;
-  hipLaunchKernelGGL((product_kernel<S, EPI, OCC>), dim3((uint32_t)(ntm * ntn)), dim3(S::kThreads), 0, st, O, n, k, R,
-                     dense, (uint32_t)ntm, (uint32_t)ntn, out);
+  const int64_t ntm = row_tiles<S::BM>(R, dense, rows), ntn = (n + kCols - 1) / kCols, wgs = ntm * ntn * parts;
+  if (wgs > (1ll << 32) / S::kThreads - 1) return NVFP4G_EINVAL;
+  hipLaunchKernelGGL((product_kernel<S, EPI>), dim3((uint32_t)wgs), dim3(S::kThreads), 0, st, O, n, k, R, dense,
+                     (uint32_t)ntm, (uint32_t)ntn, (uint32_t)per, out);
   return hip_status();
+}
+
+// The tiles a call can take.  Big: 256 x 256, one work-group on a CU.  Mid: 128
+// x 128, two of them.  Mid4: 128 x 128 with four stages, one on a CU: for grids
+// that do not fill the CUs twice, where a step takes as long as its copies.
+using Big = Shape<2, 4, 4, 2, 128, 2, 2>;
+using Mid = Shape<2, 2, 2, 2, 128, 2, 2>;
+using Mid4 = Shape<2, 2, 2, 2, 128, 4, 1>;
+constexpr int kMaxParts = 16;
+constexpr int64_t kMaxWorkspace = 32 << 20;
+
+// Row tiles that a call is likely to need: the host does not know the rows of
+// device routing, which leaves half a tile over for each expert that has any.
+template <int BM>
+int64_t likely_tiles(const Routing& R, bool dense, int64_t rows) {
+  if (dense || BM <= kTileRows || !R.d_offs) return row_tiles<BM>(R, dense, rows);
+  return rows / BM + std::min<int64_t>(R.num_experts, rows / kTileRows) / 2;
+}
+
+// Time in us: rounds of work-groups, each a fixed part (start, epilogue) and
+// its steps.  Measured (8192 x 8192 x 8192: Big 450, Mid 543, Mid4 604; 512 x
+// 7168 x 7168: 67, 50, 43; 128 rows of it: 54, 40, 27; 32768 rows of 64
+// experts, 2048 x 7168, fp32: 656, 756, 896).
+struct Choice {
+  int shape;  // 0 Big, 1 Mid, 2 Mid4
+  int parts;
+  int64_t per;  // steps of a part
+};
+template <Epilogue EPI>
+Choice choose(int64_t rows, int64_t n, int64_t k, const Routing& R, bool dense, int64_t workspace) {
+  constexpr int kDiv = is_glu(EPI) ? 2 : 1;
+  auto cols = [&](int bn) { return (n + bn / kDiv - 1) / (bn / kDiv); };
+  const int64_t steps = (k + 127) / 128;
+  const int64_t big = likely_tiles<256>(R, dense, rows) * cols(256), mid = row_tiles<128>(R, dense, rows) * cols(128);
+  const double fixed = EPI == kOutF32 ? 8 : 6;
+  auto rounds = [](int64_t tiles, int slots) { return (double)((tiles + slots - 1) / slots); };
+  Choice c{0, 1, steps};
+  double best = rounds(big, kCus) * (8 + 1.75 * steps);
+  auto take = [&](double t, const Choice& o) {
+    if (t < best) best = t, c = o;
+  };
+  take(rounds(mid, 2 * kCus) * (fixed + 1.06 * steps), Choice{1, 1, steps});
+  auto mid4 = [&](int64_t wgs, int64_t per) { return rounds(wgs, kCus) * (fixed + (0.45 + 0.3 * std::min(1.0, wgs / (double)kCus)) * per); };
+  take(mid4(mid, steps), Choice{2, 1, steps});
+  // parts of the contraction, joined by a second launch
+  for (int p = 2; p <= kMaxParts && dense; ++p) {
+    const int64_t per = (steps + p - 1) / p;
+    if (per * (p - 1) >= steps || mid * p > kCus || p * rows * n * 4 > workspace) continue;
+    take(mid4(mid * p, per) + 4 + 8e-6 * p * rows * n / 4, Choice{2, p, per});
+  }
+  return c;
 }
 
 template <Epilogue EPI>
 int product(const Operands& O, int64_t rows, int64_t n, int64_t k, const Routing& R, bool dense, void* out,
-            hipStream_t st) {
-  return launch<Shape<2, 2, 2, 4>, EPI, 1>(O, rows, n, k, R, dense, out, st);
+            void* workspace, hipStream_t st) {
+  const Choice c = choose<EPI>(rows, n, k, R, dense, workspace ? kMaxWorkspace : 0);
+  if (c.shape == 0) return launch<Big, EPI>(O, rows, n, k, R, dense, 1, 0, out, st);
+  if (c.shape == 1) return launch<Mid, EPI>(O, rows, n, k, R, dense, 1, 0, out, st);
+  if (c.parts == 1) return launch<Mid4, EPI>(O, rows, n, k, R, dense, 1, 0, out, st);
+  if constexpr (!is_glu(EPI)) {
+    const int rc = launch<Mid4, kParts>(O, rows, n, k, R, dense, c.parts, c.per, workspace, st);
+    if (rc) return rc;
+    hipLaunchKernelGGL((join_kernel<EPI == kOutF32>), line_grid((uint32_t)((rows * n / 4 + kThreads - 1) / kThreads)),
+                       dim3(kThreads), 0, st, (const int32_t*)workspace, c.parts, rows, n, O.a_scale, O.b_scale, out);
+    return hip_status();
+  }
+  return NVFP4G_EINVAL;
 }
 
 int check(const Operands& O, int64_t rows, int64_t lines, int64_t k, int32_t E, const void* out) {
@@ -338,8 +542,8 @@ int gemm(const Operands& O, int64_t rows, int64_t n, int64_t k, int32_t E, const
   Routing R;
   if ((rc = make_routing(h_splits, d_offs, d_status, rows, E, graph, &R))) return rc;
   if (rows == 0) return NVFP4G_OK;
-  return out_type == MOE_F32 ? product<kOutF32>(O, rows, n, k, R, false, out, (hipStream_t)stream)
-                             : product<kOutBf16>(O, rows, n, k, R, false, out, (hipStream_t)stream);
+  return out_type == MOE_F32 ? product<kOutF32>(O, rows, n, k, R, false, out, nullptr, (hipStream_t)stream)
+                             : product<kOutBf16>(O, rows, n, k, R, false, out, nullptr, (hipStream_t)stream);
 }
 
 int glu(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const int64_t* h_splits,
@@ -351,15 +555,19 @@ int glu(const Operands& O, int64_t rows, int64_t f, int64_t k, int32_t E, const 
   Routing R;
   if ((rc = make_routing(h_splits, d_offs, d_status, rows, E, graph, &R))) return rc;
   if (rows == 0) return NVFP4G_OK;
-  return act == MOE_ACT_SILU ? product<kGluSilu>(O, rows, f, k, R, false, h, (hipStream_t)stream)
-                             : product<kGluGelu>(O, rows, f, k, R, false, h, (hipStream_t)stream);
+  return act == MOE_ACT_SILU ? product<kGluSilu>(O, rows, f, k, R, false, h, nullptr, (hipStream_t)stream)
+                             : product<kGluGelu>(O, rows, f, k, R, false, h, nullptr, (hipStream_t)stream);
 }
 
 }  // namespace
 
 extern "C" {
 
-int64_t i8_linear_workspace(int64_t rows, int64_t k, int64_t n) { return 0; }
+// Grows with the rows, so that it serves every smaller batch too.
+int64_t i8_linear_workspace(int64_t rows, int64_t k, int64_t n) {
+  if (rows < 0 || rows > kMaxRows || !valid_k(k) || !valid_n(n)) return NVFP4G_EINVAL;
+  return std::min<int64_t>(kMaxWorkspace, kMaxParts * rows * n * 4);
+}
 
 int i8_linear(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q,
               const float* b_scale, int64_t n, void* out, int32_t out_type, void* workspace, int64_t workspace_bytes,
@@ -368,14 +576,18 @@ int i8_linear(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, 
   const int rc = check(O, rows, n, k, 1, out);
   if (rc) return rc;
   if (!valid_type(out_type)) return NVFP4G_EINVAL;
+  const int64_t need = i8_linear_workspace(rows, k, n);
+  if (need && (!workspace || workspace_bytes < need)) return NVFP4G_EINVAL;
+  if (!aligned(workspace, 16)) return NVFP4G_EALIGN;
   if (rows == 0) return NVFP4G_OK;
+  if (rows <= kFewRows) return few_rows(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, (hipStream_t)stream);
   Routing R;
   R.num_experts = 1;
   R.m_capacity = (int32_t)rows;
   R.d_offs = nullptr;
   R.d_status = nullptr;
-  return out_type == MOE_F32 ? product<kOutF32>(O, rows, n, k, R, true, out, (hipStream_t)stream)
-                             : product<kOutBf16>(O, rows, n, k, R, true, out, (hipStream_t)stream);
+  return out_type == MOE_F32 ? product<kOutF32>(O, rows, n, k, R, true, out, workspace, (hipStream_t)stream)
+                             : product<kOutBf16>(O, rows, n, k, R, true, out, workspace, (hipStream_t)stream);
 }
 
 int i8_group_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int64_t sum_m,

@@ -1,5 +1,6 @@
 // i8_token.hip -- products in 8-bit integers for single tokens: the experts'
-// projections, behind the C ABI of include/i8_group.h.
+// projections, and a projection of few rows, behind the C ABI of
+// include/i8_group.h.
 //
 // A work-group takes one expert (the first pair that chose it is its leader;
 // the work-groups of later pairs with the same expert end at once) and a run
@@ -128,7 +129,69 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void token_kernel(
   }
 }
 
+// A few rows of codes times the lines of one projection: no experts to find,
+// and the rows are copied as they are.
+template <int MT, int NL, bool F32OUT>
+__global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void few_rows_kernel(
+    const int8_t* __restrict__ a_q, const float* __restrict__ a_scale, int rows, int64_t k,
+    const int8_t* __restrict__ b_q, const float* __restrict__ b_scale, int64_t n, TokenPlan P, void* __restrict__ out) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t xlds[];
+  constexpr int kCols = NL * 16;
+  const int lane = threadIdx.x & 63, wave = uni((int32_t)(threadIdx.x >> 6));
+  const int groups = kTokenWaves / P.ks, group = wave / P.ks, part = wave % P.ks;
+  const int64_t col0 = ((int64_t)blockIdx.x * groups + group) * kCols;
+  TileLines<kModeLinear, NL> W;
+  W.init(b_q, 0, col0, n, k, lane);
+  float sb[NL];
+#pragma unroll
+  for (int t = 0; t < NL; ++t) sb[t] = b_scale[min<int64_t>(col0 + 16 * t, n - 16) + (lane & 15)];
+  i32x4* red = reinterpret_cast<i32x4*>(xlds);
+  const CodeRows X{a_q};
+  for (int first = 0; first < rows; first += P.rows) {
+    i32x4 acc[MT][NL];
+    if (first) __syncthreads();  // the last pass is done with the staged rows and the joined sums
+    const int cnt = min(rows - first, P.rows);
+    token_multiply<MT, NL>(W, P, X, k, cnt, wave, lane, xlds, [&](int i) { return (int64_t)(first + i); }, acc);
+    if (P.ks > 1) join_waves<MT, NL>(acc, red, wave, lane);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt * 16 >= cnt) continue;
+#pragma unroll
+      for (int t = 0; t < NL; ++t) {
+        if ((mt * NL + t) % P.ks != part || col0 + 16 * t >= n) continue;
+        const i32x4 s = P.ks > 1 ? joined<MT, NL>(red, group, P.ks, mt, t, lane) : acc[mt][t];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int i = mt * 16 + 4 * (lane >> 4) + v;
+          if (i >= cnt) continue;
+          const float y = ((float)s[v] * a_scale[first + i]) * sb[t];
+          const int64_t at = (first + i) * n + col0 + 16 * t + (lane & 15);
+          if (F32OUT) reinterpret_cast<float*>(out)[at] = y;
+          else reinterpret_cast<uint16_t*>(out)[at] = to_bf16(y);
+        }
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------- host side
+
+// Waves that split the contraction: the fewest rounds of work-groups (two a CU
+// where LDS and registers hold them; `experts` times the column tiles) times
+// steps of a wave and a start that takes about three of them.
+template <class Tiles>
+TokenPlan best_plan(int64_t k, int rows, int mt, int nl, int64_t experts, Tiles tiles) {
+  TokenPlan P{};
+  int64_t best = INT64_MAX;
+  for (int ks = 1; ks <= kTokenWaves; ks *= 2) {
+    const TokenPlan q = token_plan(k, rows, ks, mt * nl, experts * tiles(ks));
+    if (q.ks != ks) break;
+    const int64_t slots = (token_waves(mt) == 4 && q.lds <= kTokenLds ? 2 : 1) * kCus;
+    const int64_t cost = (experts * tiles(ks) + slots - 1) / slots * ((int64_t)q.per * q.chunks + 3);
+    if (cost < best) best = cost, P = q;
+  }
+  return P;
+}
 
 template <int MODE, int ACT, int MT>
 void launch(const uint16_t* x, int64_t k, int per, const int32_t* ids, int pairs, const int8_t* bq, const float* bs,
@@ -138,18 +201,7 @@ void launch(const uint16_t* x, int64_t k, int per, const int32_t* ids, int pairs
   auto tiles = [&](int ks) { return (ocols + kCols * (kTokenWaves / ks) - 1) / (kCols * (kTokenWaves / ks)); };
   // an expert has at most one pair of a token, or takes more passes
   const int rows = std::min((pairs + per - 1) / per, 16 * MT);
-  // Waves that split the contraction: the fewest rounds of work-groups (two a
-  // CU where LDS and registers hold them, with the experts that the pairs can
-  // reach) times steps of a wave and a start that takes about three of them.
-  TokenPlan P{};
-  int64_t best = INT64_MAX;
-  for (int ks = 1; ks <= kTokenWaves; ks *= 2) {
-    const TokenPlan q = token_plan(k, rows, ks, MT * NL, experts * tiles(ks));
-    if (q.ks != ks) break;
-    const int64_t slots = (token_waves(MT) == 4 && q.lds <= kTokenLds ? 2 : 1) * kCus;
-    const int64_t cost = (experts * tiles(ks) + slots - 1) / slots * ((int64_t)q.per * q.chunks + 3);
-    if (cost < best) best = cost, P = q;
-  }
+  const TokenPlan P = best_plan(k, rows, MT, NL, experts, tiles);
   hipLaunchKernelGGL((token_kernel<MODE, ACT, MT, NL>), dim3((uint32_t)tiles(P.ks), (uint32_t)pairs),
                      dim3(kTokenThreads), P.lds, st, x, k, per, ids, pairs, bq, bs, n, E, P, out);
 }
@@ -176,7 +228,31 @@ int check_token(const uint16_t* x, int64_t pairs, int64_t k, const int32_t* ids,
   return NVFP4G_OK;
 }
 
+template <int MT>
+int launch_few(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q,
+               const float* b_scale, int64_t n, void* out, int32_t out_type, hipStream_t st) {
+  constexpr int NL = 2, kCols = 16 * NL;
+  auto tiles = [&](int ks) { return (n + kCols * (kTokenWaves / ks) - 1) / (kCols * (kTokenWaves / ks)); };
+  const TokenPlan P = best_plan(k, (int)std::min<int64_t>(rows, 16 * MT), MT, NL, 1, tiles);
+  auto go = [&](auto* kernel) {
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)tiles(P.ks)), dim3(kTokenThreads), P.lds, st, a_q, a_scale, (int)rows, k,
+                       b_q, b_scale, n, P, out);
+  };
+  if (out_type == MOE_F32) go(few_rows_kernel<MT, NL, true>);
+  else go(few_rows_kernel<MT, NL, false>);
+  return hip_status();
+}
+
 }  // namespace
+
+namespace i8 {
+
+int few_rows(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q, const float* b_scale,
+             int64_t n, void* out, int32_t out_type, hipStream_t st) {
+  return launch_few<kFewRows / 16>(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, st);
+}
+
+}  // namespace i8
 
 extern "C" {
 

@@ -25,7 +25,7 @@ constexpr int kTokenLds = 72 * 1024;  // of the 160 KB of a CU, so that two work
 constexpr int kHeld = 8;        // 16-byte pieces of x that a thread can hold between the maximum and the codes
 
 // Waves on a SIMD that the registers leave room for.
-constexpr int token_waves(int mt) { return mt >= 4 ? 2 : 4; }
+constexpr int token_waves(int mt) { return mt >= 2 ? 2 : 4; }
 
 // How the contraction runs: chunks of KS * per steps whose rows are staged
 // together; in each, wave part p takes `per` steps (an even number).
@@ -228,5 +228,12 @@ __device__ __forceinline__ i32x4 joined(const i32x4* red, int group, int ks, int
   for (int w = 1; w < ks; ++w) s += red[(((group * ks + w) * MT + m) * NL + t) * 64 + lane];
   return s;
 }
+
+// A projection of a few rows of codes (i8_token.hip): out [rows, n] fp32 or
+// bf16.  Past 16 rows the 128 x 128 tiles of i8_gemm.hip are as fast or faster (7168
+// x 7168: 8 rows 12.0 us and 13.9, 32 rows 15.2 and 14.2, 64 rows 27 and 15.5).
+constexpr int64_t kFewRows = 16;
+int few_rows(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q, const float* b_scale,
+             int64_t n, void* out, int32_t out_type, hipStream_t st);
 
 }  // namespace i8
