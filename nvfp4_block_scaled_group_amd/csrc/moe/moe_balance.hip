@@ -23,10 +23,11 @@ namespace {
 using namespace moe;
 
 constexpr int kFwdThreads = 1024;
-// Threads of the forward pass: many experts a lane need the registers of many waves.
-constexpr int fwd_threads(int vpl) { return vpl <= 16 ? kFwdThreads : kFwdThreads / 4; }
+// Threads of a forward work-group: many experts a lane need the registers of
+// many waves, and small chunks give 1024 threads nothing to do.
+constexpr int fwd_threads(int vpl, bool small) { return vpl <= 16 && !small ? kFwdThreads : kFwdThreads / 4; }
 constexpr int kChunks = 256;    // chunks of a large batch: one for each CU
-constexpr int kMinChunk = 128;  // rows of a chunk at least
+constexpr int kOneRows = 128;   // rows of one sequence that one work-group takes by itself
 constexpr int kJoinCols = 32;   // columns of a joining work-group
 
 // The first sequence whose end is above row t (num_seqs if none): the row's
@@ -107,18 +108,16 @@ __device__ __forceinline__ float block_sum(float v, float* lred, int waves) {
 
 // whole: the launch is one work-group and one sequence, and writes the results
 // themselves.
-template <class T, int LANES, int VPL, bool SIGMOID>
-__global__ __launch_bounds__(fwd_threads(VPL)) void balance_kernel(const T* __restrict__ logits, int64_t tokens, int E,
-                                                              int topk, const int32_t* __restrict__ ids,
-                                                              const int32_t* __restrict__ ends, int num_seqs,
-                                                              int64_t rows, bool wide, bool whole, float coef, Slots P,
-                                                              Results out) {
-  constexpr int kFwd = fwd_threads(VPL);
-  extern __shared__ float lds[];  // E sums, E counts
+template <class T, int LANES, int VPL, bool SIGMOID, bool SMALL>
+__global__ __launch_bounds__(fwd_threads(VPL, SMALL)) void balance_kernel(
+    const T* __restrict__ logits, int64_t tokens, int E, int topk, const int32_t* __restrict__ ids,
+    const int32_t* __restrict__ ends, int num_seqs, int64_t rows, bool wide, bool whole, float coef, Slots P,
+    Results out) {
+  constexpr int kFwd = fwd_threads(VPL, SMALL), kWaves = kFwd / 64;
+  extern __shared__ float lds[];  // E sums of each wave, E counts
   __shared__ int32_t lany;
-  __shared__ float lred[kFwd / 64];
-  float* lsum = lds;
-  int32_t* lcount = reinterpret_cast<int32_t*>(lds + E);
+  __shared__ float lred[kWaves];
+  int32_t* lcount = reinterpret_cast<int32_t*>(lds + kWaves * E);
   constexpr int kPass = kFwd / LANES;  // tokens at a time
   const int tid = threadIdx.x, li = tid & (LANES - 1), wave = tid >> 6;
   const int64_t c0 = (int64_t)blockIdx.x * rows, c1 = min(c0 + rows, tokens);
@@ -126,16 +125,22 @@ __global__ __launch_bounds__(fwd_threads(VPL)) void balance_kernel(const T* __re
   for (int s = sequence_of(ends, num_seqs, c0); s < num_seqs && at < c1; ++s) {
     const int64_t to = ends ? min<int64_t>(ends[s], c1) : c1;
     if (to <= at) continue;
+    const int64_t t0 = at + tid / LANES, p0 = at * topk + tid, p1 = to * topk;
+    float l[VPL];
+    load_logits<T, VPL>(logits + min(t0, tokens - 1) * E, E, li, wide, l);
+    const int first = p0 < p1 ? ids[p0] : -1;  // on its way beside the logits
     for (int e = tid; e < E; e += kFwd) lcount[e] = 0;
     if (tid == 0) lany = 0;
     __syncthreads();
+    if ((uint32_t)first < (uint32_t)E) atomicAdd(&lcount[first], 1);
+    for (int64_t p = p0 + kFwd; p < p1; p += kFwd) {
+      const int e = ids[p];
+      if ((uint32_t)e < (uint32_t)E) atomicAdd(&lcount[e], 1);
+    }
     float acc[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
     int n = 0;
-    const int64_t t0 = at + tid / LANES;
-    float l[VPL];
-    load_logits<T, VPL>(logits + min(t0, tokens - 1) * E, E, li, wide, l);
     for (int64_t t = t0; t - tid / LANES < to; t += kPass) {
       float next[VPL], slope[SIGMOID ? VPL : 1];
       load_logits<T, VPL>(logits + min(t + kPass, tokens - 1) * E, E, li, wide, next);
@@ -148,49 +153,37 @@ __global__ __launch_bounds__(fwd_threads(VPL)) void balance_kernel(const T* __re
 #pragma unroll
       for (int i = 0; i < VPL; ++i) l[i] = next[i];
     }
-    for (int64_t p = at * topk + tid; p < to * topk; p += kFwd) {
-      const int e = ids[p];
-      if ((uint32_t)e < (uint32_t)E) atomicAdd(&lcount[e], 1);
-    }
     if (li == 0 && n) atomicAdd(&lany, n);
-    // groups of a wave, then the waves in order
+    // the groups of a wave, then the waves in order
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       float v = acc[i];
       if constexpr (LANES <= 8) v += __uint_as_float(exchange<3>(__float_as_uint(v)));
       if constexpr (LANES <= 16) v += __uint_as_float(exchange<4>(__float_as_uint(v)));
       if constexpr (LANES <= 32) v += __uint_as_float(exchange<5>(__float_as_uint(v)));
-      acc[i] = v;
+      if ((tid & 63) < LANES && li * VPL + i < E) lds[wave * E + li * VPL + i] = v;
     }
-    for (int w = 0; w < kFwd / 64; ++w) {
-      if (wave == w && (tid & 63) < LANES) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const int e = li * VPL + i;
-          if (e < E) lsum[e] = w ? lsum[e] + acc[i] : acc[i];
-        }
-      }
-      __syncthreads();
+    __syncthreads();
+    const int64_t slot = (int64_t)blockIdx.x + s;
+    float* probs = whole ? out.probs : P.probs + slot * E;
+    int32_t* counts = whole ? out.counts : P.counts + slot * E;
+    float v = 0.0f;
+    for (int e = tid; e < E; e += kFwd) {
+      float sum = lds[e];
+      for (int w = 1; w < kWaves; ++w) sum += lds[w * E + e];
+      const int c = lcount[e];
+      probs[e] = sum;
+      counts[e] = c;
+      v += (float)c * sum;
     }
     if (whole) {
-      float v = 0.0f;
-      for (int e = tid; e < E; e += kFwd) {
-        out.probs[e] = lsum[e];
-        out.counts[e] = lcount[e];
-        v += (float)lcount[e] * lsum[e];
-      }
-      v = block_sum(v, lred, kFwd / 64);
+      v = block_sum(v, lred, kWaves);
       if (tid == 0) {
         *out.tokens = lany;
         const bool good = !ends || (ends[0] >= 0 && ends[0] <= tokens);
         *out.loss = good ? v * sequence_weight(coef, 1, E, topk, lany) : __uint_as_float(0x7FC00000u);
       }
       return;
-    }
-    const int64_t slot = (int64_t)blockIdx.x + s;
-    for (int e = tid; e < E; e += kFwd) {
-      P.probs[slot * E + e] = lsum[e];
-      P.counts[slot * E + e] = lcount[e];
     }
     if (tid == 0) P.tokens[slot] = lany;
     __syncthreads();
@@ -333,9 +326,16 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const T* __restri
 
 // ------------------------------------------------------------- host side
 
-int64_t chunk_rows(int64_t tokens) { return std::max<int64_t>(kMinChunk, (tokens + kChunks - 1) / kChunks); }
-int64_t chunk_count(int64_t tokens) { return (tokens + chunk_rows(tokens) - 1) / chunk_rows(tokens); }
-bool one_group(int64_t tokens, int num_seqs) { return num_seqs == 1 && chunk_count(tokens) <= 1; }
+bool one_group(int64_t tokens, int num_seqs) { return num_seqs == 1 && tokens <= kOneRows; }
+// Rows of a chunk: 32 at least, fewer where several sequences would share them,
+// since a chunk takes its sequences one after another.
+int64_t least_rows(int64_t tokens, int num_seqs) {
+  return num_seqs == 1 ? 32 : std::clamp<int64_t>(tokens / num_seqs / 4, 4, 32);
+}
+int64_t chunk_rows(int64_t tokens, int num_seqs) {
+  if (one_group(tokens, num_seqs)) return kOneRows;
+  return std::max(least_rows(tokens, num_seqs), (tokens + kChunks - 1) / kChunks);
+}
 int64_t join_blocks(int E) { return (E + kJoinCols - 1) / kJoinCols; }
 
 int check_balance(const void* logits, int32_t type, int64_t tokens, int32_t E, int32_t topk, int32_t score,
@@ -372,7 +372,7 @@ int64_t moe_balance_workspace(int64_t tokens, int32_t num_experts, int32_t num_s
     return NVFP4G_EINVAL;
   if (one_group(tokens, num_seqs)) return 0;
   // more rows never need fewer bytes, though they may make fewer chunks
-  const int64_t chunks = std::min<int64_t>(kChunks, (tokens + kMinChunk - 1) / kMinChunk);
+  const int64_t least = num_seqs == 1 ? 32 : 4, chunks = std::min<int64_t>(kChunks, (tokens + least - 1) / least);
   return (chunks + num_seqs) * (8 * (int64_t)num_experts + 4) + 4 * num_seqs * join_blocks(num_experts);
 }
 
@@ -390,7 +390,7 @@ int moe_balance(const void* logits, int32_t logits_type, int64_t tokens, int32_t
     return NVFP4G_EALIGN;
   const hipStream_t st = (hipStream_t)stream;
   const int E = num_experts;
-  const int64_t rows = chunk_rows(tokens), chunks = chunk_count(tokens), slots = chunks + num_seqs;
+  const int64_t rows = chunk_rows(tokens, num_seqs), chunks = (tokens + rows - 1) / rows, slots = chunks + num_seqs;
   const bool whole = one_group(tokens, num_seqs);
   const Results R{loss, counts, probs, seq_tokens};
   Slots P{(float*)workspace, (int32_t*)workspace + slots * E, (int32_t*)workspace + 2 * slots * E};
@@ -399,17 +399,24 @@ int moe_balance(const void* logits, int32_t logits_type, int64_t tokens, int32_t
     by_experts(E, [&](auto lanes, auto vpl) {
       constexpr int L = decltype(lanes)::value, V = decltype(vpl)::value;
       const bool wide = wide_rows(logits, E, V, size);
-      auto go = [&](auto* kernel, auto* p) {
-        hipLaunchKernelGGL(kernel, dim3((uint32_t)std::max<int64_t>(chunks, 1)), dim3(fwd_threads(V)), 8 * E, st, p,
-                           tokens, E, topk, ids, seq_ends, num_seqs, rows, wide, whole, coef, P, R);
+      auto go = [&](auto* kernel, auto* p, int threads) {
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)std::max<int64_t>(chunks, 1)), dim3(threads),
+                           4 * E * (threads / 64 + 1), st, p, tokens, E, topk, ids, seq_ends, num_seqs, rows, wide,
+                           whole, coef, P, R);
       };
-      if (logits_type == MOE_F32) {
-        if (score == MOE_SCORE_SIGMOID) go(balance_kernel<float, L, V, true>, (const float*)logits);
-        else go(balance_kernel<float, L, V, false>, (const float*)logits);
-      } else {
-        if (score == MOE_SCORE_SIGMOID) go(balance_kernel<uint16_t, L, V, true>, (const uint16_t*)logits);
-        else go(balance_kernel<uint16_t, L, V, false>, (const uint16_t*)logits);
-      }
+      auto pick = [&](auto sigmoid, auto* p) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+        constexpr bool G = decltype(sigmoid)::value;
+        // the rows of a chunk in two passes of 256 threads
+        if (rows * L <= 2 * fwd_threads(V, true)) go(balance_kernel<T, L, V, G, true>, p, fwd_threads(V, true));
+        else go(balance_kernel<T, L, V, G, false>, p, fwd_threads(V, false));
+      };
+      auto typed = [&](auto* p) {
+        if (score == MOE_SCORE_SIGMOID) pick(std::true_type{}, p);
+        else pick(std::false_type{}, p);
+      };
+      if (logits_type == MOE_F32) typed((const float*)logits);
+      else typed((const uint16_t*)logits);
     });
     if (whole) return hip_status();
   }
