@@ -330,6 +330,12 @@ __device__ __forceinline__ float kept(u32x2 q, int i, float s) {
   return __builtin_fmaf((float)((w >> (8 * (i & 3))) & 0xFFu), s, -128.0f * s);
 }
 
+// 8 columns of a row as they were kept.
+struct KeptRow {
+  u32x2 g, u;
+  uint32_t gs, us;
+};
+
 // Forward: tiles of 128 packed rows x 32 NW columns (64 NW lines).
 template <int ACT, Keep KEEP, int NW>
 __global__ __launch_bounds__(kThreads, 2) void glu_fwd_kernel(Operands O, int64_t f, int64_t k, Routing R,
@@ -475,13 +481,34 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
   const bool live = (uint32_t)wn * (kCols / 2) < cols;
   multiply<false, NW>(A, B, B, (uint32_t)k, live, acc, lds0, lds1, lsc);
 
+  constexpr int BLK = NW / 2, kRows = Stage<BLK>::kRows, kPasses = 32 / kRows;
+  const int c = 8 * (lane % Stage<BLK>::kLanes), srow = lane / Stage<BLK>::kLanes;
+  // the kept rows of 32 x 32 BLK blocks, one block ahead
+  KeptRow k8[2][KEEP8 ? kPasses : 1];
+  auto load8 = [&](int blk) {
+    const uint32_t j = wn * (kCols / 2) + blk % (NW / BLK) * (32 * BLK) + c;
+    const int64_t row = row0 + wm * (kWM * 32) + blk / (NW / BLK) * 32 + srow;
+    const int64_t up = (f + kGroup - 1) / kGroup * K8.rows;  // from a scale of g to that of u
+    const uint16_t* scales = K8.s + (col0 + j) / kGroup * K8.rows + row;
+    const int8_t* q = K8.q + row * 2 * f + col0 + j;
+#pragma unroll
+    for (int r = 0; r < (KEEP8 ? kPasses : 0); ++r) {
+      KeptRow& o = k8[blk & 1][r];
+      o = KeptRow{u32x2{0, 0}, u32x2{0, 0}, 0, 0};
+      if (j < cols) {
+        o.g = *reinterpret_cast<const u32x2*>(q + 2 * kRows * r * f);
+        o.u = *reinterpret_cast<const u32x2*>(q + 2 * kRows * r * f + f);
+        o.gs = scales[kRows * r];
+        o.us = scales[up + kRows * r];
+      }
+    }
+  };
+  if (KEEP8) load8(0);
   if (tid < kBM) lsa[tid] = O.a_amax[row0 + tid] / 2688.0f;
   if (tid < kCols) lsb[tid] = (uint32_t)tid < cols ? O.b_amax[line0 + tid] / 2688.0f : 0.0f;
   __syncthreads();
   if (!live) return;
-  constexpr int BLK = NW / 2, kRows = Stage<BLK>::kRows, kPasses = 32 / kRows;
   Stage<BLK> stage(lds0, lds1, wave);
-  const int c = 8 * (lane % Stage<BLK>::kLanes), srow = lane / Stage<BLK>::kLanes;
 #pragma unroll
   for (int im = 0; im < kWM; ++im)
 #pragma unroll
@@ -492,23 +519,12 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
       // through the caches: rows of 2f columns start inside a cache line (past
       // them 1 to 4% slower); two blocks' loads at once were 8% slower
       u32x4 gq[kPasses], uq[kPasses];
-      u32x2 g8[kPasses], u8[kPasses];
-      uint16_t gs[kPasses], us[kPasses];
-      const int64_t groups = (f + kGroup - 1) / kGroup, grow0 = row0 + wm * (kWM * 32) + im * 32 + srow;
-      const uint16_t* scales = KEEP8 ? K8.s + (col0 + j0 + c) / kGroup * K8.rows + grow0 : nullptr;
+      constexpr int kBlocks = kWM * NW / BLK;
+      const int blk = im * (NW / BLK) + in0 / BLK;
+      if (KEEP8 && blk + 1 < kBlocks) load8(blk + 1);
 #pragma unroll
       for (int r = 0; r < kPasses; ++r) {
-        if (KEEP8) {
-          g8[r] = u8[r] = u32x2{0, 0};
-          gs[r] = us[r] = 0;
-          if (write) {
-            g8[r] = *reinterpret_cast<const u32x2*>(K8.q + at0 + 2 * kRows * r * f);
-            u8[r] = *reinterpret_cast<const u32x2*>(K8.q + at0 + 2 * kRows * r * f + f);
-            gs[r] = scales[kRows * r];
-            us[r] = scales[groups * K8.rows + kRows * r];
-          }
-          continue;
-        }
+        if (KEEP8) break;
         gq[r] = uq[r] = u32x4{0, 0, 0, 0};
         if (write) {
           gq[r] = *reinterpret_cast<const u32x4*>(gu + at0 + 2 * kRows * r * f);
@@ -529,12 +545,12 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
       for (int r = 0; r < kPasses; ++r) {
         float dh[8], dg[8], du[8], hh[8];
         stage.get(kRows * r + srow, c, dh);
-        const float sg = KEEP8 ? __uint_as_float((uint32_t)gs[r] << 16) : 0.0f;
-        const float su = KEEP8 ? __uint_as_float((uint32_t)us[r] << 16) : 0.0f;
+        const KeptRow& kr = k8[blk & 1][KEEP8 ? r : 0];
+        const float sg = KEEP8 ? __uint_as_float(kr.gs << 16) : 0.0f, su = KEEP8 ? __uint_as_float(kr.us << 16) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float g = KEEP8 ? kept(g8[r], i, sg) : i & 1 ? bf16hi(gq[r][i >> 1]) : bf16lo(gq[r][i >> 1]);
-          const float u = KEEP8 ? kept(u8[r], i, su) : i & 1 ? bf16hi(uq[r][i >> 1]) : bf16lo(uq[r][i >> 1]);
+          const float g = KEEP8 ? kept(kr.g, i, sg) : i & 1 ? bf16hi(gq[r][i >> 1]) : bf16lo(gq[r][i >> 1]);
+          const float u = KEEP8 ? kept(kr.u, i, su) : i & 1 ? bf16hi(uq[r][i >> 1]) : bf16lo(uq[r][i >> 1]);
           float dv;
           const float q = act_logistic<ACT>(g, &dv), a = g * q;
           du[i] = dh[i] * a;
@@ -542,7 +558,8 @@ __global__ __launch_bounds__(kThreads, 2) void glu_bwd_kernel(Operands O, int64_
           if (KEEP8) hh[i] = a * u;
         }
         if (KEEP8 && again && write)
-          *reinterpret_cast<u32x4*>(again + (grow0 + kRows * r) * f + col0 + j0 + c) = pack8(hh);
+          *reinterpret_cast<u32x4*>(again + (row0 + wm * (kWM * 32) + im * 32 + srow + kRows * r) * f + col0 + j0 + c) =
+              pack8(hh);
         if (write) {
           *reinterpret_cast<u32x4*>(dgu + at0 + 2 * kRows * r * f) = pack8(dg);
           *reinterpret_cast<u32x4*>(dgu + at0 + 2 * kRows * r * f + f) = pack8(du);
@@ -586,11 +603,25 @@ int make_routing(const int64_t* h_splits, const int32_t* d_offs, int32_t* d_stat
 // routing counts the capacity's tiles: the host does not know the rows.
 bool narrow(int64_t wide_tiles) { return wide_tiles <= kCus / 2; }
 
+// The same choice for the calls with an 8-bit checkpoint, by the time that each
+// kind of tile takes, in rounds of two wide tiles on a CU: one wide tile alone
+// on its CU 0.6 of a round; three narrow ones on a CU 0.82, two 0.55, one 0.35.
+// Forward and backward together, wide up to the rule above and by this one:
+// 8192 rows, 2048 x 1040: 173 and 159 us; 4096, 2048 x 1408: 110 and 103; 8192,
+// 7168 x 1280: 492 and 465; 6144, 4096 x 2048: 322 and 312.
+bool narrow_by_time(int64_t wide_tiles, int64_t narrow_tiles) {
+  const int64_t w = wide_tiles % (2 * kCus), n = narrow_tiles % (3 * kCus);
+  const double wide = wide_tiles / (2 * kCus) + (w == 0 ? 0.0 : w <= kCus ? 0.6 : 1.0);
+  const double nar = narrow_tiles / (3 * kCus) * 0.82 + (n == 0 ? 0.0 : n <= kCus ? 0.35 : n <= 2 * kCus ? 0.55 : 0.82);
+  return nar < wide;
+}
+
 template <int ACT, Keep KEEP, int NW>
 int launch_fwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Routing& R, uint16_t* h, uint16_t* gu,
                const Kept& K8, hipStream_t st) {
   const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + 32 * NW - 1) / (32 * NW));
-  if (NW == 4 && narrow((int64_t)ntm * ntn)) return launch_fwd<ACT, KEEP, 2>(O, rows, f, k, R, h, gu, K8, st);
+  if (NW == 4 && (KEEP == kKeep8 ? narrow_by_time((int64_t)ntm * ntn, ntm * ((f + 63) / 64)) : narrow((int64_t)ntm * ntn)))
+    return launch_fwd<ACT, KEEP, 2>(O, rows, f, k, R, h, gu, K8, st);
   hipLaunchKernelGGL((glu_fwd_kernel<ACT, KEEP, NW>), dim3(ntm * ntn), dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, h,
                      gu, K8);
   return hip_status();
@@ -600,7 +631,8 @@ template <int ACT, bool KEEP8, int NW>
 int launch_bwd(const Operands& O, int64_t rows, int64_t f, int64_t k, const Routing& R, const uint16_t* gu,
                const Kept& K8, uint16_t* dgu, uint16_t* again, hipStream_t st) {
   const uint32_t ntm = (uint32_t)(rows / kBM), ntn = (uint32_t)((f + 64 * NW - 1) / (64 * NW));
-  if (NW == 4 && narrow((int64_t)ntm * ntn)) return launch_bwd<ACT, KEEP8, 2>(O, rows, f, k, R, gu, K8, dgu, again, st);
+  if (NW == 4 && (KEEP8 ? narrow_by_time((int64_t)ntm * ntn, ntm * ((f + 127) / 128)) : narrow((int64_t)ntm * ntn)))
+    return launch_bwd<ACT, KEEP8, 2>(O, rows, f, k, R, gu, K8, dgu, again, st);
   hipLaunchKernelGGL((glu_bwd_kernel<ACT, KEEP8, NW>), dim3(ntm * ntn), dim3(kThreads), 0, st, O, f, k, R, ntm, ntn, gu,
                      K8, dgu, again);
   return hip_status();

@@ -204,3 +204,50 @@ def test_device_routing_writes_the_routed_rows_alone(splits, f, k, spare):
         assert int(status) & bit
         for g in (h, q, s):
             assert (g.t.contiguous().view(torch.uint8) == CANARY).all()
+
+
+# rows and columns whose tiles are the wide ones (128 columns forward, 256
+# backward), the last column of them ragged: 510 of them, and 768 (more than 512:
+# their XCD order); compared with the bf16 form, whose tests hold it to 64 bits
+WIDE8 = {"forward": [([4096, 0, 6784], 656), ([8192, 128, 8064], 752)],
+         "backward": [([4096, 0, 6784], 1296), ([8192, 128, 8064], 1520)]}
+
+
+@pytest.mark.parametrize("at", [0, 1])
+def test_forward_wide_tiles(at):
+    (splits, f), k = WIDE8["forward"][at], 256
+    assert sum(splits) // 128 * -(-f // 128) == (510, 768)[at]
+    rng, M, E, a, b = case(f, splits, f, k, 2 * f)
+    dev = on_device(a, b, E, 2 * f)
+    h, plain = Guarded(2 * M * f, torch.bfloat16, (M, f)), torch.empty((M, f), dtype=torch.bfloat16, device="cuda:0")
+    (q, s), gu = kept_buffers(M, f), torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0")
+    moe.moe_glu_keep8(*dev, splits, h.t, q.t, s.t)
+    moe.moe_glu(*dev, splits, plain, gu=gu)
+    torch.cuda.synchronize()
+    assert h.guards_intact() and q.guards_intact() and s.guards_intact() and torch.equal(h.t, plain)
+    step = s.t.float().t()[:, torch.from_numpy(I.group_of(f)).to("cuda:0")]
+    got = q.t.float() * step
+    # half a step, and the rounding of the bf16 value it is compared with (2^-8 of it, with room for fp32 here)
+    assert ((got - gu.float()).abs() <= step * 0.501 + gu.float().abs() * 1.01 * R.UB).all()
+
+
+@pytest.mark.parametrize("at", [0, 1])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_backward_wide_tiles(at, kind):
+    (splits, f), k = WIDE8["backward"][at], 256
+    assert sum(splits) // 128 * -(-f // 256) == (510, 768)[at]
+    rng, M, E, a, b = case(f, splits, f, k, f)
+    dev = on_device(a, b, E, f)
+    q, s = random_kept(rng, M, f, power_of_two=True)
+    q, s = q.to("cuda:0"), s.to("cuda:0")
+    gu = (q.float() * s.float().t()[:, torch.from_numpy(I.group_of(f)).to("cuda:0")]).to(torch.bfloat16)
+    out, again = Guarded(4 * M * f, torch.bfloat16, (M, 2 * f)), Guarded(2 * M * f, torch.bfloat16, (M, f))
+    want = torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0")
+    moe.moe_glu_bwd_keep8(*dev, splits, q, s, out.t, h=again.t, act=ACTS[kind])
+    moe.moe_glu_bwd(*dev, splits, gu, want, act=ACTS[kind])
+    torch.cuda.synchronize()
+    assert out.guards_intact() and again.guards_intact() and torch.equal(out.t, want)
+    rows = rng.choice(M, 300, replace=False)
+    at64 = gu[torch.from_numpy(rows).to("cuda:0")].double().cpu().numpy()
+    g, u = at64[:, :f], at64[:, f:]
+    R.check(again.t[torch.from_numpy(rows).to("cuda:0")], R.act(g, kind)[0] * u, R.glu_bound(g, u, 0 * g, 0 * u, kind), "h")
