@@ -112,7 +112,7 @@ LINEAR = [  # rows, n, k
     (1, 16, 16), (1, 512, 7168), (3, 48, 128), (5, 272, 80), (16, 1040, 144), (17, 64, 528), (31, 32, 2048), (33, 528, 272),
     (64, 80, 4112), (65, 16, 16), (100, 1024, 1040), (127, 144, 112), (128, 256, 256), (129, 272, 384), (193, 528, 1488),
     (255, 48, 2064), (300, 784, 96), (513, 1040, 208), (1000, 96, 4096), (1030, 2064, 144), (2049, 512, 272),
-    (8, 7168, 256), (12, 4096, 13072),
+    (8, 7168, 256), (12, 4096, 13072), (2100, 4112, 144), (9000, 4112, 48), (1500, 2304, 1040), (20, 7168, 1296), (40, 16, 7168),
 ]
 
 
@@ -157,7 +157,8 @@ def test_linear_offsets_past_32_bits():
 GROUPS = [  # splits, n, k
     ([128], 16, 16), ([128, 0, 256], 48, 144), ([0, 128], 272, 400), ([256, 128, 0, 0, 128], 144, 640), ([384], 528, 128),
     ([128] * 9, 32, 112), ([0, 0, 640, 128, 0], 1040, 272), ([1024, 0, 1536, 128, 384], 656, 208),
-    ([4096, 0, 128, 4224, 256], 528, 144), ([128] * 70 + [0, 384], 272, 80),
+    ([4096, 0, 128, 4224, 256], 528, 144), ([128] * 70 + [0, 384], 272, 80), ([1408, 0, 640, 256, 1152], 4112, 80),
+    ([2048, 384, 0, 1664, 4096], 2064, 48), ([640, 0, 384], 1040, 1040),
 ]
 
 
