@@ -13,7 +13,8 @@
 // fixed order and writes one slot.  The pair (chunk, sequence) goes up in one
 // of the two or in both from slot to slot, so slot chunk + sequence is its own
 // without any list.  A second launch adds the slots of each sequence in order,
-// a third the sequences.  No float is added by an atomic.
+// and the work-group of it that ends last adds the sequences.  No float is added
+// by an atomic.
 #include <algorithm>
 
 #include "moe_logits.hpp"
@@ -81,6 +82,8 @@ struct Slots {
   float* probs;     // [slots, E]
   int32_t* counts;  // [slots, E]
   int32_t* tokens;  // [slots]
+  float* loss;      // [num_seqs, blocks of kJoinCols columns]
+  uint32_t* done;   // work-groups of the second launch that have ended: 0 after the first
 };
 struct Results {
   float* loss;
@@ -121,6 +124,7 @@ __global__ __launch_bounds__(fwd_threads(VPL, SMALL)) void balance_kernel(
   constexpr int kPass = kFwd / LANES;  // tokens at a time
   const int tid = threadIdx.x, li = tid & (LANES - 1), wave = tid >> 6;
   const int64_t c0 = (int64_t)blockIdx.x * rows, c1 = min(c0 + rows, tokens);
+  if (!whole && blockIdx.x == 0 && tid == 0) *P.done = 0;
   int64_t at = c0;
   for (int s = sequence_of(ends, num_seqs, c0); s < num_seqs && at < c1; ++s) {
     const int64_t to = ends ? min<int64_t>(ends[s], c1) : c1;
@@ -202,16 +206,17 @@ __global__ __launch_bounds__(fwd_threads(VPL, SMALL)) void balance_kernel(
   }
 }
 
-// The slots of a sequence, in order: work-group (s, b) has kJoinCols columns.
-// lossp [num_seqs, blocks] gets its share of the loss.
+// The slots of a sequence, in order: work-group (b, s) has kJoinCols columns and
+// a share of the loss; the last one to end adds the shares in order.
 __global__ __launch_bounds__(kFwdThreads) void balance_join_kernel(Slots P, int64_t tokens, int E, int topk,
                                                                    const int32_t* __restrict__ ends, int num_seqs,
-                                                                   int64_t rows, float coef, float* __restrict__ lossp,
-                                                                   Results out) {
+                                                                   int64_t rows, float coef, Results out) {
   constexpr int kParts = kFwdThreads / kJoinCols;
   __shared__ float lsum[kParts][kJoinCols + 1];
   __shared__ int32_t lcount[kParts][kJoinCols + 1];
   __shared__ int32_t ltok[kParts];
+  __shared__ float lred[kFwdThreads / 64];
+  __shared__ bool llast;
   const int s = blockIdx.y, tid = threadIdx.x, part = tid / kJoinCols, c = tid % kJoinCols;
   const int64_t from = ends && s ? ends[s - 1] : 0, to = ends ? ends[s] : tokens;
   const bool good = from >= 0 && to >= from && to <= tokens;
@@ -231,36 +236,39 @@ __global__ __launch_bounds__(kFwdThreads) void balance_join_kernel(Slots P, int6
   lcount[part][c] = cnt;
   if (c == 0) ltok[part] = tok;
   __syncthreads();
-  if (tid >= 64) return;
-  float v = 0.0f;
-  tok = 0;
-  for (int p = 0; p < kParts; ++p) tok += ltok[p];
-  if (tid < kJoinCols && col < E) {
-    sum = 0.0f;
-    cnt = 0;
-    for (int p = 0; p < kParts; ++p) {
-      sum += lsum[p][c];
-      cnt += lcount[p][c];
+  if (tid < 64) {
+    float v = 0.0f;
+    tok = 0;
+    for (int p = 0; p < kParts; ++p) tok += ltok[p];
+    if (tid < kJoinCols && col < E) {
+      sum = 0.0f;
+      cnt = 0;
+      for (int p = 0; p < kParts; ++p) {
+        sum += lsum[p][c];
+        cnt += lcount[p][c];
+      }
+      out.probs[(int64_t)s * E + col] = sum;
+      out.counts[(int64_t)s * E + col] = cnt;
+      v = (float)cnt * sum;
     }
-    out.probs[(int64_t)s * E + col] = sum;
-    out.counts[(int64_t)s * E + col] = cnt;
-    v = (float)cnt * sum;
+    v = wave_sum(v);
+    if (tid == 0) {
+      if (blockIdx.x == 0) out.tokens[s] = tok;
+      const float share = good ? v * sequence_weight(coef, num_seqs, E, topk, tok) : __uint_as_float(0x7FC00000u);
+      // shares go past the caches of an XCD, and before the count that tells of them
+      __hip_atomic_store(P.loss + (int64_t)s * gridDim.x + blockIdx.x, share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint32_t all = gridDim.x * gridDim.y;
+      llast = __hip_atomic_fetch_add(P.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 == all;
+    }
   }
-  v = wave_sum(v);
-  if (tid == 0) {
-    if (blockIdx.x == 0) out.tokens[s] = tok;
-    lossp[(int64_t)s * gridDim.x + blockIdx.x] =
-        good ? v * sequence_weight(coef, num_seqs, E, topk, tok) : __uint_as_float(0x7FC00000u);
-  }
-}
-
-__global__ __launch_bounds__(kFwdThreads) void balance_loss_kernel(const float* __restrict__ lossp, int64_t n,
-                                                                   float* __restrict__ loss) {
-  __shared__ float lred[kFwdThreads / 64];
+  __syncthreads();
+  if (!llast) return;
+  const int64_t n = (int64_t)gridDim.x * gridDim.y;
   float v = 0.0f;
-  for (int64_t i = threadIdx.x; i < n; i += kFwdThreads) v += lossp[i];
+  for (int64_t i = tid; i < n; i += kFwdThreads)
+    v += __hip_atomic_load(P.loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   v = block_sum(v, lred, kFwdThreads / 64);
-  if (threadIdx.x == 0) *loss = v;
+  if (tid == 0) *out.loss = v;
 }
 
 template <class T, int LANES, int VPL, bool SIGMOID>
@@ -373,7 +381,7 @@ int64_t moe_balance_workspace(int64_t tokens, int32_t num_experts, int32_t num_s
   if (one_group(tokens, num_seqs)) return 0;
   // more rows never need fewer bytes, though they may make fewer chunks
   const int64_t least = num_seqs == 1 ? 32 : 4, chunks = std::min<int64_t>(kChunks, (tokens + least - 1) / least);
-  return (chunks + num_seqs) * (8 * (int64_t)num_experts + 4) + 4 * num_seqs * join_blocks(num_experts);
+  return (chunks + num_seqs) * (8 * (int64_t)num_experts + 4) + 4 * num_seqs * join_blocks(num_experts) + 4;
 }
 
 int moe_balance(const void* logits, int32_t logits_type, int64_t tokens, int32_t num_experts, int32_t topk,
@@ -393,38 +401,37 @@ int moe_balance(const void* logits, int32_t logits_type, int64_t tokens, int32_t
   const int64_t rows = chunk_rows(tokens, num_seqs), chunks = (tokens + rows - 1) / rows, slots = chunks + num_seqs;
   const bool whole = one_group(tokens, num_seqs);
   const Results R{loss, counts, probs, seq_tokens};
-  Slots P{(float*)workspace, (int32_t*)workspace + slots * E, (int32_t*)workspace + 2 * slots * E};
-  if (chunks || whole) {
-    const int size = logits_type == MOE_F32 ? 4 : 2;
-    by_experts(E, [&](auto lanes, auto vpl) {
-      constexpr int L = decltype(lanes)::value, V = decltype(vpl)::value;
-      const bool wide = wide_rows(logits, E, V, size);
-      auto go = [&](auto* kernel, auto* p, int threads) {
-        hipLaunchKernelGGL(kernel, dim3((uint32_t)std::max<int64_t>(chunks, 1)), dim3(threads),
-                           4 * E * (threads / 64 + 1), st, p, tokens, E, topk, ids, seq_ends, num_seqs, rows, wide,
-                           whole, coef, P, R);
-      };
-      auto pick = [&](auto sigmoid, auto* p) {
-        using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-        constexpr bool G = decltype(sigmoid)::value;
-        // the rows of a chunk in two passes of 256 threads
-        if (rows * L <= 2 * fwd_threads(V, true)) go(balance_kernel<T, L, V, G, true>, p, fwd_threads(V, true));
-        else go(balance_kernel<T, L, V, G, false>, p, fwd_threads(V, false));
-      };
-      auto typed = [&](auto* p) {
-        if (score == MOE_SCORE_SIGMOID) pick(std::true_type{}, p);
-        else pick(std::false_type{}, p);
-      };
-      if (logits_type == MOE_F32) typed((const float*)logits);
-      else typed((const uint16_t*)logits);
-    });
-    if (whole) return hip_status();
-  }
   const int64_t blocks = join_blocks(E);
-  float* lossp = (float*)(P.tokens + slots);
+  int32_t* w = (int32_t*)workspace;
+  const Slots P = whole ? Slots{}
+                        : Slots{(float*)w, w + slots * E, w + 2 * slots * E, (float*)(w + 2 * slots * E + slots),
+                                (uint32_t*)(w + 2 * slots * E + slots + num_seqs * blocks)};
+  const int size = logits_type == MOE_F32 ? 4 : 2;
+  by_experts(E, [&](auto lanes, auto vpl) {
+    constexpr int L = decltype(lanes)::value, V = decltype(vpl)::value;
+    const bool wide = wide_rows(logits, E, V, size);
+    auto go = [&](auto* kernel, auto* p, int threads) {
+      hipLaunchKernelGGL(kernel, dim3((uint32_t)std::max<int64_t>(chunks, 1)), dim3(threads),
+                         4 * E * (threads / 64 + 1), st, p, tokens, E, topk, ids, seq_ends, num_seqs, rows, wide,
+                         whole, coef, P, R);
+    };
+    auto pick = [&](auto sigmoid, auto* p) {
+      using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+      constexpr bool G = decltype(sigmoid)::value;
+      // the rows of a chunk in two passes of 256 threads
+      if (rows * L <= 2 * fwd_threads(V, true)) go(balance_kernel<T, L, V, G, true>, p, fwd_threads(V, true));
+      else go(balance_kernel<T, L, V, G, false>, p, fwd_threads(V, false));
+    };
+    auto typed = [&](auto* p) {
+      if (score == MOE_SCORE_SIGMOID) pick(std::true_type{}, p);
+      else pick(std::false_type{}, p);
+    };
+    if (logits_type == MOE_F32) typed((const float*)logits);
+    else typed((const uint16_t*)logits);
+  });
+  if (whole) return hip_status();
   hipLaunchKernelGGL(balance_join_kernel, dim3((uint32_t)blocks, (uint32_t)num_seqs), dim3(kFwdThreads), 0, st, P,
-                     tokens, E, topk, seq_ends, num_seqs, rows, coef, lossp, R);
-  hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFwdThreads), 0, st, lossp, blocks * num_seqs, loss);
+                     tokens, E, topk, seq_ends, num_seqs, rows, coef, R);
   return hip_status();
 }
 
