@@ -160,20 +160,29 @@ def timed(fn, reps=20):
     return a.elapsed_time(b) / reps * 1e3
 
 
-def main():
-    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+def arguments(doc):
+    ap = argparse.ArgumentParser(description=doc, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--tokens", type=int, default=4096)
     ap.add_argument("--hidden", type=int, default=2048)
     ap.add_argument("--inner", type=int, default=1024)
     ap.add_argument("--experts", type=int, default=32)
     ap.add_argument("--topk", type=int, default=4)
-    a = ap.parse_args()
+    return ap.parse_args()
+
+
+def generator(seed):
+    """rand(*shape, scale): seeded normal values in bf16."""
     g = torch.Generator(device="cuda")
-    g.manual_seed(0)
+    g.manual_seed(seed)
 
     def rand(*shape, scale=1.0):
         return (torch.randn(shape, generator=g, device="cuda") * scale).to(torch.bfloat16)
 
+    return rand
+
+
+def main():
+    a, rand = arguments(__doc__), generator(0)
     layer = ExpertLayer(rand(a.experts, 2 * a.inner, a.hidden, scale=a.hidden ** -0.5),
                         rand(a.experts, a.hidden, a.inner, scale=a.inner ** -0.5), rand(a.experts, a.hidden, scale=a.hidden ** -0.5),
                         a.topk)
