@@ -23,10 +23,11 @@ import torch
 
 from . import binding as _b
 from .binding import F32, I32, U8, _check
-from .moe import (ACT_GELU, ACT_SILU, B16, I8, MOE_BF16, MOE_F32, _buf, _dims, _host_splits,  # noqa: F401
-                  _routing, _shape, _stream)
+from .moe import (ACT_GELU, ACT_SILU, B16, I8, MOE_BF16, MOE_F32, _buf, _dims, _exact,  # noqa: F401
+                  _host_splits, _routing, _stream)
 
 MAX_K = 131056
+OUT = F32 + B16
 
 EXPORTS = (
     "i8_group_cast", "i8_group_cast_graphsafe", "i8_linear_workspace", "i8_linear", "i8_group_gemm",
@@ -60,29 +61,24 @@ def load_library() -> ctypes.CDLL:
 
 def _rows(a_q, a_scale):
     m, k = _dims("a_q", a_q, 2)
-    _shape("a_scale", a_scale, (m,))
-    return (_buf("a_q", a_q, I8, m * k, True), _buf("a_scale", a_scale, F32, m, True)), m, k
+    return (_buf("a_q", a_q, I8, m * k, True), _exact("a_scale", a_scale, F32, (m,))), m, k
 
 
 def _channels(b_q, b_scale, k, dim):
     shape = _dims("b_q", b_q, dim)
     if shape[-1] != k:
         raise ValueError(f"b_q has {shape[-1]} columns per channel, the rows have {k}")
-    _shape("b_scale", b_scale, shape[:-1])
-    return (_buf("b_q", b_q, I8, b_q.numel(), True), _buf("b_scale", b_scale, F32, b_scale.numel(), True)), shape
+    return (_buf("b_q", b_q, I8, 0, True), _exact("b_scale", b_scale, F32, shape[:-1])), shape
 
 
 def _product(out, m, n):
     """Output [m, n] of a product: f32, or bf16 (raw 16-bit too)."""
-    _shape("out", out, (m, n))
-    return _buf("out", out, F32 + B16, m * n, True), MOE_F32 if out.dtype == torch.float32 else MOE_BF16
+    return _exact("out", out, OUT, (m, n)), MOE_F32 if out.dtype == torch.float32 else MOE_BF16
 
 
 def _cast_buffers(x, q, scale):
     m, k = _dims("x", x, 2)
-    _shape("q", q, (m, k))
-    _shape("scale", scale, (m,))
-    return (_buf("x", x, B16, m * k, True), m, k), (_buf("q", q, I8, m * k, True), _buf("scale", scale, F32, m, True))
+    return (_buf("x", x, B16, m * k, True), m, k), (_exact("q", q, I8, (m, k)), _exact("scale", scale, F32, (m,)))
 
 
 def i8_group_cast(x, q, scale, stream=None):
@@ -134,8 +130,7 @@ def _glu_operands(a_q, a_scale, b_q, b_scale, h):
     b, (E, n, _) = _channels(b_q, b_scale, k, 3)
     if n % 2:
         raise ValueError("b_q must hold the gate channels and as many up channels")
-    _shape("h", h, (m, n // 2))
-    return (*a, *b, m, n // 2, k, E), _buf("h", h, B16, m * (n // 2), True)
+    return (*a, *b, m, n // 2, k, E), _exact("h", h, B16, (m, n // 2))
 
 
 def i8_group_glu(a_q, a_scale, b_q, b_scale, h_splits, h, act=ACT_SILU, stream=None):
@@ -156,14 +151,12 @@ def i8_token_glu(x, ids, b_q, b_scale, h, act=ACT_SILU, stream=None):
     """x [T, k] bf16, ids [T, topk] i32, b_q [E, 2f, k] -> h [T * topk, f] bf16."""
     T, k = _dims("x", x, 2)
     topk = _dims("ids", ids, 2)[1]
-    _shape("ids", ids, (T, topk))
     b, (E, n, _) = _channels(b_q, b_scale, k, 3)
     if n % 2:
         raise ValueError("b_q must hold the gate channels and as many up channels")
-    _shape("h", h, (T * topk, n // 2))
     _check("i8_token_glu", load_library().i8_token_glu(
-        _buf("x", x, B16, T * k, True), T, k, topk, _buf("ids", ids, I32, T * topk, True), *b, n // 2, E, int(act),
-        _buf("h", h, B16, T * topk * (n // 2), True), _stream(stream)))
+        _buf("x", x, B16, T * k, True), T, k, topk, _exact("ids", ids, I32, (T, topk)), *b, n // 2, E, int(act),
+        _exact("h", h, B16, (T * topk, n // 2)), _stream(stream)))
 
 
 def i8_token_linear(x, ids, b_q, b_scale, out, stream=None):
@@ -172,10 +165,9 @@ def i8_token_linear(x, ids, b_q, b_scale, out, stream=None):
     b, (E, n, _) = _channels(b_q, b_scale, k, 3)
     if not isinstance(ids, torch.Tensor) or ids.numel() != pairs:
         raise ValueError(f"ids must hold one expert for each of the {pairs} rows of x")
-    _shape("out", out, (pairs, n))
     _check("i8_token_linear", load_library().i8_token_linear(
         _buf("x", x, B16, pairs * k, True), pairs, k, _buf("ids", ids, I32, pairs, True), *b, n, E,
-        _buf("out", out, F32, pairs * n, True), _stream(stream)))
+        _exact("out", out, F32, (pairs, n)), _stream(stream)))
 
 
 # ------------------------------------------------------------------ helpers

@@ -123,6 +123,15 @@ def _shape(name: str, t, want):
         raise ValueError(f"{name} must be a tensor of shape {tuple(want)}, got {got}")
 
 
+def _exact(name: str, t, dtypes, want):
+    """Address of a required buffer whose whole shape is fixed by the other arguments: _shape and _buf in one."""
+    if (type(t) is torch.Tensor and t.shape == want and t.dtype in dtypes and t.is_contiguous()
+            and t.get_device() == _device_index()):
+        return t.data_ptr()
+    _shape(name, t, want)
+    return _buf(name, t, dtypes, t.numel(), True)
+
+
 def _logits(logits):
     T, E = _dims("logits", logits, 2)
     if logits.dtype not in (torch.float32, torch.bfloat16):
@@ -168,11 +177,11 @@ def moe_balance_workspace(tokens: int, num_experts: int, num_seqs: int = 1) -> i
 
 def _sequences(seq_ends, seq_tokens):
     S, = _dims("seq_tokens", seq_tokens, 1)
-    if seq_ends is None and S != 1:
-        raise ValueError(f"seq_tokens has {S} entries; without seq_ends there is one sequence")
     if seq_ends is not None:
-        _shape("seq_ends", seq_ends, (S,))
-    return _buf("seq_ends", seq_ends, I32, S), S
+        return _exact("seq_ends", seq_ends, I32, (S,)), S
+    if S != 1:
+        raise ValueError(f"seq_tokens has {S} entries; without seq_ends there is one sequence")
+    return None, S
 
 
 def moe_balance(logits, ids, loss, counts, probs, seq_tokens, workspace=None, *, seq_ends=None, score=SCORE_SOFTMAX,
@@ -181,15 +190,12 @@ def moe_balance(logits, ids, loss, counts, probs, seq_tokens, workspace=None, *,
     i32, for the sequences that end at rows seq_ends [S] i32 (None: one of all rows)."""
     lp, lt, T, E = _logits(logits)
     k = _dims("ids", ids, 2)[1]
-    _shape("ids", ids, (T, k))
     ends, S = _sequences(seq_ends, seq_tokens)
-    _shape("counts", counts, (S, E))
-    _shape("probs", probs, (S, E))
     _check("moe_balance", load_library().moe_balance(
-        lp, lt, T, E, k, _buf("ids", ids, I32, T * k, True), int(score), ends, S, float(coef),
-        _buf("loss", loss, F32, 1, True), _buf("counts", counts, I32, S * E, True),
-        _buf("probs", probs, F32, S * E, True), _buf("seq_tokens", seq_tokens, I32, S, True),
-        _buf("workspace", workspace, U8, 0), 0 if workspace is None else workspace.numel(), _stream(stream)))
+        lp, lt, T, E, k, _exact("ids", ids, I32, (T, k)), int(score), ends, S, float(coef),
+        _buf("loss", loss, F32, 1, True), _exact("counts", counts, I32, (S, E)), _exact("probs", probs, F32, (S, E)),
+        _buf("seq_tokens", seq_tokens, I32, S, True), _buf("workspace", workspace, U8, 0),
+        0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
 def moe_balance_bwd(logits, counts, seq_tokens, dlogits, *, topk, seq_ends=None, score=SCORE_SOFTMAX, coef=1.0,
@@ -198,14 +204,11 @@ def moe_balance_bwd(logits, counts, seq_tokens, dlogits, *, topk, seq_ends=None,
     [T, E] of that type if given (it may be dlogits)."""
     lp, lt, T, E = _logits(logits)
     ends, S = _sequences(seq_ends, seq_tokens)
-    _shape("counts", counts, (S, E))
-    _shape("dlogits", dlogits, (T, E))
-    if add is not None:
-        _shape("add", add, (T, E))
+    same = (logits.dtype,)
     _check("moe_balance_bwd", load_library().moe_balance_bwd(
-        lp, lt, T, E, int(topk), int(score), ends, S, float(coef), _buf("counts", counts, I32, S * E, True),
-        _buf("seq_tokens", seq_tokens, I32, S, True), _buf("dloss", dloss, F32, 1),
-        _buf("add", add, (logits.dtype,), T * E), _buf("dlogits", dlogits, (logits.dtype,), T * E, True),
+        lp, lt, T, E, int(topk), int(score), ends, S, float(coef), _exact("counts", counts, I32, (S, E)),
+        _buf("seq_tokens", seq_tokens, I32, S, True), None if dloss is None else _buf("dloss", dloss, F32, 1),
+        None if add is None else _exact("add", add, same, (T, E)), _exact("dlogits", dlogits, same, (T, E)),
         _stream(stream)))
 
 
@@ -339,9 +342,8 @@ def moe_glu_bwd_graphsafe(a_data, a_scale, a_amax, b_data, b_scale, b_amax, d_of
 
 def _kept(gu8, gu_scale, m, f):
     """8-bit checkpoint of m rows: codes [m, 2f] and bf16 scales [2 * ceil(f / 32), m]."""
-    _shape("gu8", gu8, (m, 2 * f))
-    _shape("gu_scale", gu_scale, (2 * -(-f // KEEP8_GROUP), m))
-    return _buf("gu8", gu8, I8, 2 * m * f, True), _buf("gu_scale", gu_scale, B16, gu_scale.numel(), True)
+    return (_exact("gu8", gu8, I8, (m, 2 * f)),
+            _exact("gu_scale", gu_scale, B16, (2 * -(-f // KEEP8_GROUP), m)))
 
 
 def moe_glu_keep8(a_data, a_scale, a_amax, b_data, b_scale, b_amax, h_splits, h, gu8, gu_scale, act=ACT_SILU,
