@@ -91,7 +91,6 @@ __global__ __launch_bounds__(kTokenThreads, token_waves(MT)) void token_kernel(
     if (first) __syncthreads();  // the last pass is done with the staged rows and the joined sums
     const int rows = min(cnt - first, P.rows);
     auto row_of = [&](int i) { return (int64_t)(pair_at(first + i) / per); };
-    cast_maxima(X, rows, k, wave, lane, row_of);
     token_multiply<MT, NL>(W, P, X, k, rows, wave, lane, xlds, row_of, acc);
     if (P.ks > 1) join_waves<MT, NL>(acc, red, wave, lane);
     // each wave finishes its share: with split waves the tiles whose number

@@ -22,7 +22,6 @@ constexpr int kStepK = 256;     // contraction step of a wave
 constexpr int kTokenThreads = 512;
 constexpr int kTokenWaves = kTokenThreads / 64;
 constexpr int kTokenLds = 72 * 1024;  // of the 160 KB of a CU, so that two work-groups fit; twice that where one is enough
-constexpr int kHeld = 8;        // 16-byte pieces of x that a thread can hold between the maximum and the codes
 
 // Waves on a SIMD that the registers leave room for.
 constexpr int token_waves(int mt) { return mt >= 2 ? 2 : 4; }
@@ -105,7 +104,7 @@ struct CodeRows {
 
 // Stages elements k0 .. k0 + len - 1 (len a multiple of 512) of the rows; what
 // lies past k stays as it is, since the weights are zero there.
-template <class RowOf>
+template <int AHEAD, class RowOf>
 __device__ __forceinline__ void stage_rows(const CodeRows& X, int rows, int64_t k, int64_t k0, int len, int pitch, int wave,
                                            int lane, uint8_t* xlds, RowOf row_of) {
   const int pieces = (len + 1023) / 1024;  // 1 KB a copy
@@ -115,32 +114,58 @@ __device__ __forceinline__ void stage_rows(const CodeRows& X, int rows, int64_t 
     if (1024 * p + 16 * lane < len) copy16(xs, xlds + r * pitch + 1024 * p, 1024 * p + 16 * lane, 0);
   }
 }
-template <class RowOf>
+// Waves that share a row where there are fewer rows than waves.
+__device__ __forceinline__ int row_waves(int rows) { return rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8; }
+// Pieces of a row that a lane has on their way (one by one a row took 0.7 us
+// out of the L2); four of them beside the weights' need the registers of two
+// work-groups.
+constexpr int ahead(int mt) { return mt >= 2 ? 4 : 2; }
+
+template <int AHEAD, class RowOf>
 __device__ __forceinline__ void stage_rows(const CastRows& X, int rows, int64_t k, int64_t k0, int len, int pitch, int wave,
                                            int lane, uint8_t* xlds, RowOf row_of) {
-  const int granules = (int)(min<int64_t>(len, k - k0) / 16);
-  for (int r = 0; r < rows; ++r) {
+  const int granules = (int)(min<int64_t>(len, k - k0) / 16), parts = row_waves(rows);
+  for (int r = wave / parts; r < rows; r += kTokenWaves / parts) {
     const u32x4* row = reinterpret_cast<const u32x4*>(X.x + row_of(r) * k + k0);
     const RowCast c = X.rc[r];
-    for (int g = 64 * wave + lane; g < granules; g += kTokenThreads) {
-      const u32x2 lo = cast8(row[2 * g], c), hi = cast8(row[2 * g + 1], c);
-      *reinterpret_cast<u32x4*>(xlds + r * pitch + 16 * g) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    uint8_t* to = xlds + r * pitch;
+    for (int g0 = 64 * (wave % parts) + lane; g0 < granules; g0 += 64 * parts * AHEAD) {
+      u32x4 lo[AHEAD], hi[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int g = min(g0 + 64 * parts * i, granules - 1);
+        lo[i] = row[2 * g];
+        hi[i] = row[2 * g + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int g = g0 + 64 * parts * i;
+        const u32x2 a = cast8(lo[i], c), b = cast8(hi[i], c);
+        if (g < granules) *reinterpret_cast<u32x4*>(to + 16 * g) = u32x4{a[0], a[1], b[0], b[1]};
+      }
     }
   }
 }
 
 // Largest magnitude of each row, from memory, and how it is cast.  All threads;
 // ends with a barrier.
-template <class RowOf>
-__device__ __forceinline__ void cast_maxima(const CastRows& X, int rows, int64_t k, int wave, int lane, RowOf row_of) {
-  // waves of a row: 8 / rows of them, or a row at a time
-  const int parts = rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8;
+template <int AHEAD, class RowOf>
+__device__ __forceinline__ void prepare_rows(const CodeRows&, int, int64_t, int, int, RowOf) {}
+template <int AHEAD, class RowOf>
+__device__ __forceinline__ void prepare_rows(const CastRows& X, int rows, int64_t k, int wave, int lane, RowOf row_of) {
+  const int parts = row_waves(rows), pieces = (int)(k / 8);
   if ((int)threadIdx.x < rows) X.lmax[threadIdx.x] = 0;
   __syncthreads();
   for (int r = wave / parts; r < rows; r += kTokenWaves / parts) {
     const u32x4* row = reinterpret_cast<const u32x4*>(X.x + row_of(r) * k);
     uint32_t m = 0;
-    for (int64_t g = 64 * (wave % parts) + lane; g < k / 8; g += 64 * parts) m = max(m, abs_max8(row[g]));
+    for (int g0 = 64 * (wave % parts) + lane; g0 < pieces; g0 += 64 * parts * AHEAD) {
+      u32x4 v[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) v[i] = row[min(g0 + 64 * parts * i, pieces - 1)];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) m = max(m, abs_max8(v[i]));
+    }
     m = wave_reduce(m, [](uint32_t a, uint32_t b) { return max(a, b); });
     if (lane == 0) atomicMax(&X.lmax[r], m);
   }
@@ -176,6 +201,7 @@ __device__ __forceinline__ void token_multiply(const W& w, const TokenPlan& P, c
   };
   load_next(ring[0]);
   load_next(ring[1]);
+  prepare_rows<ahead(MT)>(x, rows, k, wave, lane, row_of);
   uint32_t xoff[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -197,7 +223,7 @@ __device__ __forceinline__ void token_multiply(const W& w, const TokenPlan& P, c
   };
   for (int c = 0; c < P.chunks; ++c) {
     if (c) __syncthreads();
-    stage_rows(x, rows, k, (int64_t)c * span * kStepK, span * kStepK, P.pitch, wave, lane, xlds, row_of);
+    stage_rows<ahead(MT)>(x, rows, k, (int64_t)c * span * kStepK, span * kStepK, P.pitch, wave, lane, xlds, row_of);
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
     const uint8_t* xs = xlds + part * P.per * kStepK;
