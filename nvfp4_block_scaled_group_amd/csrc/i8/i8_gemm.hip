@@ -5,7 +5,13 @@
 //   out[r, j] = (sum_c qa[r, c] qb[j, c]) * sa[r] * sb[j],   h = act(g) * u
 //
 // Both operands are stored along the contraction index; the int32 sums of the
-// matrix instruction are exact, so the order of the contraction is free.
+// matrix instruction are exact, so the order of the contraction is free: parts
+// of it may be added in any order with the same bits.
+//
+// What bounds it: at large sizes power (8192 x 8192 x 8192 in 410 to 450 us, 2.4 to
+// 2.7 POP/s, matrix units 63% busy at a clock of 1.5 GHz; the same launch on
+// zeros runs at 3.4), with few steps a tile its start and epilogue (16384 x 1024 x
+// 8192: 158 us, 1.7 POP/s), with few tiles the copies' latency.
 #include <algorithm>
 
 #include "i8_token.hpp"
@@ -88,8 +94,9 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// acc[im][in] = A lines x B lines^T over steps ks0 .. ks1 - 1 of the
-// contraction.  PAIR: B's LDS lines are blocks of 16 TN lines, alternately of
+// acc[im][in] = B lines x A lines^T over steps ks0 .. ks1 - 1 of the
+// contraction: a lane has one row of A (lane % 32) and in its sixteen sums the B
+// lines 8 (v / 4) + 4 (lane / 32) + v % 4, four neighbours at a time.  PAIR: B's LDS lines are blocks of 16 TN lines, alternately of
 // B0 (gate) and of B1 (up), so that a wave's first TN / 2 tiles are gate lines
 // and the others the up lines of the same columns.  The granules of a line's
 // last step past k are copied as zeros.
@@ -160,7 +167,7 @@ struct Multiply {
       for (int im = 0; im < S::TM; ++im)
 #pragma unroll
         for (int in = 0; in < S::TN; ++in)
-          acc[im][in] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[from][im], b[from][in], acc[im][in], 0, 0, 0);
+          acc[im][in] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[from][in], a[from][im], acc[im][in], 0, 0, 0);
     };
     auto step = [&](uint32_t ks, uint8_t* base, const uint8_t* next) {
       if (LIVE) {
@@ -271,20 +278,16 @@ __device__ __forceinline__ bool row_tile(const Routing& R, bool dense, uint32_t 
   return false;
 }
 
-// A wave's own piece of a stage, free in the epilogue: 32 rows x COLS columns of
-// fp32 go in as the MFMA layout holds them (column in the lane) and come out as
-// consecutive columns of a row, so that memory sees 16 bytes a lane.
-template <int COLS>
+// A wave's own piece of a stage, free in the epilogue: 32 rows x COLS columns go
+// in four neighbours at a time, as the sums lie in the lanes, and come out as 16
+// bytes a lane of whole row pieces.  Pitches: the rows that an LDS access serves
+// at once (32 of 8 bytes, 16 of 16) meet all 64 banks.
+template <int COLS, int SIZE>
 struct RowStage {
-  static constexpr int kPitch = COLS + 8;  // floats: the two lane halves, 4 rows apart, on different banks
-  static constexpr int kBytes = 32 * kPitch * 4;
-  float* p;
-  __device__ __forceinline__ void put(int block, int v, int lane, float x) {
-    p[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * kPitch + 32 * block + (lane & 31)] = x;
-  }
-  __device__ __forceinline__ f32x4 get4(int row, int col) const {
-    return *reinterpret_cast<const f32x4*>(p + row * kPitch + col);
-  }
+  static constexpr int kPitch = COLS * SIZE + 4 * SIZE;
+  static constexpr int kBytes = 32 * kPitch;
+  uint8_t* p;
+  __device__ __forceinline__ uint8_t* at(int row, int col) const { return p + row * kPitch + SIZE * col; }
 };
 // Orders a wave's own LDS writes and reads (they run in issue order).
 __device__ __forceinline__ void wave_sync() {
@@ -312,7 +315,7 @@ __global__ __launch_bounds__(S::kThreads, S::OCC) void product_kernel(Operands O
   __shared__ __attribute__((aligned(16))) uint8_t lds1[S::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t lds2[S::NS > 2 ? S::kStageBytes : 16];
   __shared__ __attribute__((aligned(16))) uint8_t lds3[S::NS > 2 ? S::kStageBytes : 16];
-  __shared__ float lsa[S::BM];
+  __shared__ __attribute__((aligned(16))) float lsb[S::BN];
   if (!routing_ok(R)) return;
   uint32_t tm, tn, t = xcd_tile(), part = 0;
   if (EPI == kParts) {  // the parts of a tile side by side
@@ -336,32 +339,46 @@ __global__ __launch_bounds__(S::kThreads, S::OCC) void product_kernel(Operands O
   for (int im = 0; im < S::TM; ++im)
 #pragma unroll
     for (int in = 0; in < S::TN; ++in) acc[im][in] = i32x16{};
-  if (EPI != kParts)
-    for (int i = tid; i < S::BM; i += S::kThreads) lsa[i] = i < T.rows ? O.a_scale[T.row0 + i] : 0.0f;
+  // scales are on their way beside the first copies, and wait in registers: a
+  // lane has its rows', a thread one line's, in the order of the stage
+  static_assert(S::kThreads >= S::BN, "a thread has a line's scale");
+  float sa[S::TM], line_scale = 0.0f;
+#pragma unroll
+  for (int im = 0; im < S::TM; ++im) {
+    const int r = wm * (32 * S::TM) + 32 * im + (lane & 31);
+    sa[im] = EPI != kParts && r < T.rows ? O.a_scale[T.row0 + r] : 0.0f;
+  }
+  if (EPI != kParts && tid < S::BN) {
+    const int j = GLU ? tid / (32 * S::TN) * kWaveCols + tid % kWaveCols : tid;
+    const bool up = GLU && tid % (32 * S::TN) >= kWaveCols;
+    if (j < (int)cols) line_scale = O.b_scale[line0 + (up ? n : 0) + j];
+  }
   const uint32_t nk = (uint32_t)((k + S::BK - 1) / S::BK);
   const uint32_t ks0 = EPI == kParts ? part * per : 0, ks1 = EPI == kParts ? min(ks0 + per, nk) : nk;
   const Multiply<S, GLU> M(A, B0, B1, (uint32_t)k, ks0, ks1, Stages<S>{lds0, lds1, lds2, lds3});
-  if (!live) {
-    M.template run<false>(acc);
-    return;
+  if (live) M.template run<true>(acc);
+  else M.template run<false>(acc);
+  if (EPI != kParts) {
+    if (tid < S::BN) lsb[tid] = line_scale;
+    __syncthreads();
   }
-  M.template run<true>(acc);
+  if (!live) return;
 
+  constexpr int SIZE = EPI == kOutF32 || EPI == kParts ? 4 : 2;  // bytes of an output
+  using Rows = RowStage<kWaveCols, SIZE>;
   constexpr int kShare = (S::kWaves + S::NS - 1) / S::NS;  // waves of a stage
-  static_assert(kShare * RowStage<kWaveCols>::kBytes <= S::kStageBytes, "the waves' rows fit the stages");
+  static_assert(kShare * Rows::kBytes <= S::kStageBytes, "the waves' rows fit the stages");
   const int own = wave / kShare;
-  RowStage<kWaveCols> stage{reinterpret_cast<float*>((own == 0 ? lds0 : own == 1 ? lds1 : own == 2 ? lds2 : lds3) +
-                                                     (wave % kShare) * RowStage<kWaveCols>::kBytes)};
-  constexpr int kPer = EPI == kOutF32 || EPI == kParts ? 4 : 8;  // columns of a lane's store
-  constexpr int kLanes = kWaveCols / kPer, kRows = 64 / kLanes;  // lanes of a row, rows of a store
+  const Rows stage{(own == 0 ? lds0 : own == 1 ? lds1 : own == 2 ? lds2 : lds3) + (wave % kShare) * Rows::kBytes};
+  constexpr int kPer = 16 / SIZE, kLanes = kWaveCols / kPer, kRows = 64 / kLanes;  // columns of a lane's store, lanes of a row, rows of a store
   const int c = kPer * (lane % kLanes), srow = lane / kLanes;
   const bool inside = wn * kWaveCols + c < (int)cols;
-  float sb[S::TN];
+  f32x4 sb[S::TN][4];
 #pragma unroll
-  for (int in = 0; in < S::TN; ++in) {
-    const int j = wn * kWaveCols + (in % BLK) * 32 + (lane & 31);
-    sb[in] = EPI != kParts && j < (int)cols ? O.b_scale[line0 + (GLU && in >= BLK ? n : 0) + j] : 0.0f;
-  }
+  for (int in = 0; in < S::TN; ++in)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      sb[in][q] = *reinterpret_cast<const f32x4*>(&lsb[wn * (32 * S::TN) + 32 * in + 8 * q + 4 * (lane >> 5)]);
   const int64_t first = EPI == kParts ? part * (int64_t)R.m_capacity : 0;
 #pragma unroll
   for (int im = 0; im < S::TM; ++im) {
@@ -369,35 +386,33 @@ __global__ __launch_bounds__(S::kThreads, S::OCC) void product_kernel(Operands O
 #pragma unroll
     for (int in = 0; in < BLK; ++in)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        float y;
+      for (int q = 0; q < 4; ++q) {
+        uint8_t* to = stage.at(lane & 31, 32 * in + 8 * q + 4 * (lane >> 5));
         if constexpr (EPI == kParts) {
-          y = __int_as_float(acc[im][in][v]);
+          *reinterpret_cast<i32x4*>(to) = i32x4{acc[im][in][4 * q], acc[im][in][4 * q + 1], acc[im][in][4 * q + 2], acc[im][in][4 * q + 3]};
         } else {
-          const float sa = lsa[r0 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
-          y = ((float)acc[im][in][v] * sa) * sb[in];
-          if constexpr (GLU) {
-            const float u = ((float)acc[im][in + BLK][v] * sa) * sb[in + BLK];
-            float dv;
-            y = y * act_logistic<EPI == kGluSilu ? MOE_ACT_SILU : MOE_ACT_GELU>(y, &dv) * u;
+          f32x4 y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = ((float)acc[im][in][4 * q + i] * sa[im]) * sb[in][q][i];
+            if constexpr (GLU) {
+              const float u = ((float)acc[im][in + BLK][4 * q + i] * sa[im]) * sb[in + BLK][q][i];
+              float dv;
+              y[i] = y[i] * act_logistic<EPI == kGluSilu ? MOE_ACT_SILU : MOE_ACT_GELU>(y[i], &dv) * u;
+            }
           }
+          if constexpr (SIZE == 4) *reinterpret_cast<f32x4*>(to) = y;
+          else *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
         }
-        stage.put(in, v, lane, y);
       }
     wave_sync();
 #pragma unroll
     for (int r = 0; r < 32; r += kRows) {
-      const f32x4 lo = stage.get4(r + srow, c);
+      const uint8_t* from = stage.at(r + srow, c);
+      const u32x2 lo = *reinterpret_cast<const u32x2*>(from), hi = *reinterpret_cast<const u32x2*>(from + 8);
       const int64_t at = (first + T.row0 + r0 + r + srow) * n + col0 + wn * kWaveCols + c;
-      const bool write = inside && r0 + r + srow < T.rows;
-      if constexpr (kPer == 4) {
-        if (write) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + at) = lo;
-      } else {
-        const f32x4 hi = stage.get4(r + srow, c + 4);
-        if (write)
-          *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(out) + at) =
-              u32x4{pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]), pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3])};
-      }
+      if (inside && r0 + r + srow < T.rows)
+        *reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(out) + SIZE * at) = u32x4{lo[0], lo[1], hi[0], hi[1]};
     }
     wave_sync();
   }
@@ -467,7 +482,7 @@ int64_t likely_tiles(const Routing& R, bool dense, int64_t rows) {
 // Time in us: rounds of work-groups, each a fixed part (start, epilogue) and
 // its steps.  Measured (8192 x 8192 x 8192: Big 450, Mid 543, Mid4 604; 512 x
 // 7168 x 7168: 67, 50, 43; 128 rows of it: 54, 40, 27; 32768 rows of 64
-// experts, 2048 x 7168, fp32: 656, 756, 896).
+// experts, 2048 x 7168, fp32: 656, 756, 896; 18560 rows, 448 x 2 x 512: 28, 25).
 struct Choice {
   int shape;  // 0 Big, 1 Mid, 2 Mid4
   int parts;
@@ -479,15 +494,19 @@ Choice choose(int64_t rows, int64_t n, int64_t k, const Routing& R, bool dense, 
   auto cols = [&](int bn) { return (n + bn / kDiv - 1) / (bn / kDiv); };
   const int64_t steps = (k + 127) / 128;
   const int64_t big = likely_tiles<256>(R, dense, rows) * cols(256), mid = row_tiles<128>(R, dense, rows) * cols(128);
-  const double fixed = EPI == kOutF32 ? 8 : 6;
+  const double fixed = EPI == kOutF32 ? 6.5 : 5;
   auto rounds = [](int64_t tiles, int slots) { return (double)((tiles + slots - 1) / slots); };
   Choice c{0, 1, steps};
-  double best = rounds(big, kCus) * (8 + 1.75 * steps);
+  double best = rounds(big, kCus) * (6.5 + 1.75 * steps);
   auto take = [&](double t, const Choice& o) {
     if (t < best) best = t, c = o;
   };
-  take(rounds(mid, 2 * kCus) * (fixed + 1.06 * steps), Choice{1, 1, steps});
-  auto mid4 = [&](int64_t wgs, int64_t per) { return rounds(wgs, kCus) * (fixed + (0.45 + 0.3 * std::min(1.0, wgs / (double)kCus)) * per); };
+  // a last round with one work-group on a CU at most takes 0.7 of a full one
+  const int64_t rest = mid % (2 * kCus);
+  take((mid / (2 * kCus) + (rest == 0 ? 0.0 : rest <= kCus ? 0.7 : 1.0)) * (fixed + 1.06 * steps), Choice{1, 1, steps});
+  auto mid4 = [&](int64_t wgs, int64_t per) {
+    return rounds(wgs, kCus) * (fixed + (0.43 + 0.12 * std::min(1.0, wgs / (double)kCus)) * per);
+  };
   take(mid4(mid, steps), Choice{2, 1, steps});
   // parts of the contraction, joined by a second launch
   for (int p = 2; p <= kMaxParts && dense; ++p) {
@@ -566,7 +585,7 @@ extern "C" {
 // Grows with the rows, so that it serves every smaller batch too.
 int64_t i8_linear_workspace(int64_t rows, int64_t k, int64_t n) {
   if (rows < 0 || rows > kMaxRows || !valid_k(k) || !valid_n(n)) return NVFP4G_EINVAL;
-  return std::min<int64_t>(kMaxWorkspace, kMaxParts * rows * n * 4);
+  return rows <= kFewRows ? 0 : std::min<int64_t>(kMaxWorkspace, kMaxParts * rows * n * 4);
 }
 
 int i8_linear(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q,
