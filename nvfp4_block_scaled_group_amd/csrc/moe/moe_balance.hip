@@ -211,11 +211,11 @@ __global__ __launch_bounds__(fwd_threads(VPL, SMALL)) void balance_kernel(
 __global__ __launch_bounds__(kFwdThreads) void balance_join_kernel(Slots P, int64_t tokens, int E, int topk,
                                                                    const int32_t* __restrict__ ends, int num_seqs,
                                                                    int64_t rows, float coef, Results out) {
-  constexpr int kParts = kFwdThreads / kJoinCols;
-  __shared__ float lsum[kParts][kJoinCols + 1];
-  __shared__ int32_t lcount[kParts][kJoinCols + 1];
-  __shared__ int32_t ltok[kParts];
-  __shared__ float lred[kFwdThreads / 64];
+  constexpr int kParts = kFwdThreads / kJoinCols, kWaves = kFwdThreads / 64, kAhead = 8;
+  __shared__ float lsum[kWaves][kJoinCols + 1];
+  __shared__ int32_t lcount[kWaves][kJoinCols + 1];
+  __shared__ int32_t ltok[kWaves];
+  __shared__ float lred[kWaves];
   __shared__ bool llast;
   const int s = blockIdx.y, tid = threadIdx.x, part = tid / kJoinCols, c = tid % kJoinCols;
   const int64_t from = ends && s ? ends[s - 1] : 0, to = ends ? ends[s] : tokens;
@@ -225,27 +225,47 @@ __global__ __launch_bounds__(kFwdThreads) void balance_join_kernel(Slots P, int6
   const int col = blockIdx.x * kJoinCols + c;
   float sum = 0.0f;
   int cnt = 0, tok = 0;
-  if (col < E)
-    for (int64_t j = first + part; j <= last; j += kParts) {
-      sum += P.probs[(j + s) * E + col];
-      cnt += P.counts[(j + s) * E + col];
+  for (int64_t j0 = first + part; j0 <= last; j0 += kParts * kAhead) {
+    float p[kAhead];
+    int n[kAhead], t[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {  // every load on its way before one is used; past the last slot they count nothing
+      const int64_t slot = min(j0 + i * kParts, last) + s;
+      p[i] = P.probs[slot * E + min(col, E - 1)];
+      n[i] = P.counts[slot * E + min(col, E - 1)];
+      t[i] = P.tokens[slot];
     }
-  if (c == 0)
-    for (int64_t j = first + part; j <= last; j += kParts) tok += P.tokens[j + s];
-  lsum[part][c] = sum;
-  lcount[part][c] = cnt;
-  if (c == 0) ltok[part] = tok;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (j0 + i * kParts <= last) {
+        sum += p[i];
+        cnt += n[i];
+        tok += t[i];
+      }
+  }
+  // the two parts of a wave, then the waves in order
+  static_assert(kJoinCols == 32, "a wave holds two parts");
+  sum += __uint_as_float(exchange<5>(__float_as_uint(sum)));
+  cnt += (int)exchange<5>((uint32_t)cnt);
+  tok += (int)exchange<5>((uint32_t)tok);
+  if ((tid & 63) < kJoinCols) {
+    lsum[tid >> 6][c] = sum;
+    lcount[tid >> 6][c] = cnt;
+    if (c == 0) ltok[tid >> 6] = tok;
+  }
   __syncthreads();
   if (tid < 64) {
     float v = 0.0f;
     tok = 0;
-    for (int p = 0; p < kParts; ++p) tok += ltok[p];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) tok += ltok[w];
     if (tid < kJoinCols && col < E) {
       sum = 0.0f;
       cnt = 0;
-      for (int p = 0; p < kParts; ++p) {
-        sum += lsum[p][c];
-        cnt += lcount[p][c];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        sum += lsum[w][c];
+        cnt += lcount[w][c];
       }
       out.probs[(int64_t)s * E + col] = sum;
       out.counts[(int64_t)s * E + col] = cnt;
