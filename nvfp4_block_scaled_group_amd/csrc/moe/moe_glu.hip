@@ -324,10 +324,12 @@ __device__ __forceinline__ u32x2 keep8(const float (&v)[8], uint16_t* scale) {
   const float inv = 1.0f / __uint_as_float((uint32_t)*scale << 16);
   return u32x2{codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
 }
-// The value of byte i of a lane's codes, exact: (code + 128) s - 128 s.
+// The value of byte i of a lane's codes, exact: the code's byte plus 128 is a
+// float in one conversion, and the 128 leave it again before the scale comes (128 s
+// would pass fp32's range where s is 2^121).
 __device__ __forceinline__ float kept(u32x2 q, int i, float s) {
   const uint32_t w = q[i >> 2] ^ 0x80808080u;
-  return __builtin_fmaf((float)((w >> (8 * (i & 3))) & 0xFFu), s, -128.0f * s);
+  return ((float)((w >> (8 * (i & 3))) & 0xFFu) - 128.0f) * s;
 }
 
 // 8 columns of a row as they were kept.

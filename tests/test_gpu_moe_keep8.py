@@ -100,6 +100,21 @@ def test_backward_equals_the_bf16_form_on_values_that_both_hold(splits, f, k):
     assert torch.equal(got, want)
 
 
+def test_backward_at_the_largest_scale():
+    """S = 2^121: 127 S is finite, 128 S is not; dh is small enough for finite gradients."""
+    splits, f, k = [128, 256], 208, 128
+    rng, M, E, a, b = case(8, splits, f, k, f)
+    a[2][:] *= np.float32(2.0 ** -100)
+    dev = on_device(a, b, E, f)
+    q, s = random_kept(rng, M, f)
+    s[:] = 2.0 ** 121
+    gu = torch.from_numpy(I.kept_values(q, s, f)[0]).to(torch.bfloat16).to("cuda:0")
+    got, want = (torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda:0") for _ in range(2))
+    moe.moe_glu_bwd_keep8(*dev, splits, q.to("cuda:0"), s.to("cuda:0"), got)
+    moe.moe_glu_bwd(*dev, splits, gu, want)
+    assert torch.isfinite(want).all() and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 def test_backward_follows_differences(kind):
     """dh is exact here; the loss sum(dh * act(g) * u) is differenced in 64 bits at the kept values."""
