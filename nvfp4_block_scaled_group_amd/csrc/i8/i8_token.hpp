@@ -3,7 +3,10 @@
 //
 // MFMA 16x16x64: rows are tokens, columns are weight lines, so a tile costs
 // the same for 1 token as for 16.  Reading the weights bounds it (1 byte an
-// element, no decode).  A lane takes 16 bytes of its line at a time, four
+// element, no decode: 24 tokens of 6 among 64 experts, 2048 x 7168, 844 MB in 131 us,
+// 6.4 TB/s; 1 token of 8, 7168 x 2 x 2048, 235 MB in 38 us, 6.2 TB/s, where a quarter
+// of the time is the start, the cast of the row and the join; 8 rows of one 2048 x
+// 7168 projection 8.2 us, 1.8 TB/s, eight steps of latency).  A lane takes 16 bytes of its line at a time, four
 // neighbouring lanes 64 in a row; the eight waves of a work-group split the
 // contraction KS ways and the lines 8 / KS ways, and join their int32 sums,
 // which are exact in any order, in LDS.  The rows are staged in LDS as codes:

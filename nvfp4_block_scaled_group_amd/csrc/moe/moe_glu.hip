@@ -308,7 +308,10 @@ struct Kept {
 constexpr int kGroup = MOE_KEEP8_GROUP;  // columns of a scale: four lanes hold 8 each
 static_assert(kGroup == 32, "the reductions below are over four lanes");
 
-// Codes of a lane's 8 values and the scale (bf16 bits) of its group.
+// Codes of a lane's 8 values and the scale (bf16 bits) of its group.  Beside the
+// products they cost little: 16384 rows, 7168 x 2 x 2048: 799 us, 789 with g and u in
+// bf16, 774 with none kept; the backward pass 433 us and 429, 447 where it writes
+// act(g) u again; 8192 rows, 2048 x 2 x 1040: 87.5 us, 89.1, 85.6, and 58.8, 68.4, 59.8.
 __device__ __forceinline__ u32x2 keep8(const float (&v)[8], uint16_t* scale) {
   uint32_t m = 0;
 #pragma unroll

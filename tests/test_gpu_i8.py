@@ -156,9 +156,9 @@ def test_linear_offsets_past_32_bits():
 
 GROUPS = [  # splits, n, k
     ([128], 16, 16), ([128, 0, 256], 48, 144), ([0, 128], 272, 400), ([256, 128, 0, 0, 128], 144, 640), ([384], 528, 128),
-    ([128] * 9, 32, 112), ([0, 0, 640, 128, 0], 1040, 272), ([1024, 0, 1536, 128, 384], 656, 208),
+    ([128] * 9, 32, 112), ([0, 0, 640, 128, 0], 1040, 272), ([1024, 0, 1664, 128, 384], 656, 208),
     ([4096, 0, 128, 4224, 256], 528, 144), ([128] * 70 + [0, 384], 272, 80), ([1408, 0, 640, 256, 1152], 4112, 80),
-    ([2048, 384, 0, 1664, 4096], 2064, 48), ([640, 0, 384], 1040, 1040),
+    ([2048, 384, 0, 1664, 4096], 2064, 48), ([640, 0, 384], 1040, 1040), ([8192, 128, 0, 7936, 128], 2064, 400),
 ]
 
 
@@ -198,7 +198,7 @@ def test_group_glu(splits, n, k, kind):
     R.check(h.t, *glu_expect(ops, splits, f, kind), "h")
 
 
-@pytest.mark.parametrize("splits,spare", [([128, 0, 256], 256), ([1024, 0, 1536, 128, 384], 640), ([0, 0], 128)])
+@pytest.mark.parametrize("splits,spare", [([128, 0, 256], 256), ([1024, 0, 1664, 128, 384], 640), ([0, 0], 128)])
 @pytest.mark.parametrize("op", ["gemm", "glu"])
 def test_device_routing_writes_the_routed_rows_alone(splits, spare, op):
     n, k, M, E = 96, 208, sum(splits), len(splits)
@@ -227,6 +227,39 @@ def test_device_routing_writes_the_routed_rows_alone(splits, spare, op):
                      (ends[:-1] + [cap + 128], B.NVFP4G_DEV_OVERFLOW)):
         out, status = call(bad)
         assert status & bit and untouched(out)
+
+
+@pytest.mark.parametrize("splits,spare", [([4096, 0, 128, 4224, 256], 128), ([384] * 23 + [0], 1280)])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "silu", "gelu"])
+def test_device_routing_of_large_tiles(splits, spare, kind):
+    """Rows enough for tiles that hold two 128-row groups of an expert, the last of them half empty."""
+    glu = kind in ACTS
+    n, k, M, E = 2080 if glu else 2064, 400, sum(splits), len(splits)
+    cap = M + spare
+    rng = np.random.default_rng(M)
+    width = n // 2 if glu else n
+    qa, qb = (torch.randint(-128, 128, s, dtype=torch.int8, device="cuda:0") for s in ((cap, k), (E, n, k)))
+    sa, sb = dev(np.exp(rng.standard_normal(cap)).astype(np.float32)), dev((np.exp(rng.standard_normal((E, n))) * 1e-5).astype(np.float32))
+    t, size = (torch.bfloat16, 2) if glu else TYPES[kind]
+    out, status = Guarded(size * cap * width, t, (cap, width)), torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    offs = torch.tensor(B.offsets_from_splits(splits), dtype=torch.int32, device="cuda:0")
+    if glu:
+        i8.i8_group_glu_graphsafe(qa, sa, qb, sb, offs, out.t, status, act=ACTS[kind])
+    else:
+        i8.i8_group_gemm_graphsafe(qa, sa, qb, sb, offs, out.t, status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and out.guards_intact() and untouched(out.t[M:])
+    rows = np.sort(rng.choice(M, 200, replace=False))
+    ends = np.cumsum(splits)
+    ops = [v.cpu().numpy() for v in (qa, sa, qb, sb)]
+    for r in rows:
+        e = int(np.searchsorted(ends, r, side="right"))
+        y = I.product(ops[0][r:r + 1], ops[1][r:r + 1], ops[2][e], ops[3][e])
+        if glu:
+            g, u = y[:, :width].astype(np.float64), y[:, width:].astype(np.float64)
+            R.check(out.t[r:r + 1], R.act(g, kind)[0] * u, R.glu_bound(g, u, 2 * R.U * np.abs(g), 2 * R.U * np.abs(u), kind), "h")
+        else:
+            I.same_bits(out.t[r:r + 1], y, f"row {r}")
 
 
 def test_no_rows():
