@@ -1,8 +1,8 @@
 // i8_cast.hip -- cast of bf16 rows to 8-bit integers with a scale for each
 // row, behind the C ABI of include/i8_group.h.
 //
-// It reads 2 bytes an element and writes 1: memory bounds it (65536 x 7168 in 213 to
-// 248 us, 5.7 to 6.6 TB/s, the rate of a copy).  A wave or a work-group takes a row, whose
+// It reads 2 bytes an element and writes 1: memory bounds it (65536 x 7168 in 223 us,
+// 6.3 TB/s, the rate of a copy and more).  A wave or a work-group takes a row, whose
 // values stay in registers between the maximum and the codes; rows past 8192
 // columns are read twice.
 #include "i8_common.hpp"
@@ -23,10 +23,19 @@ __device__ __forceinline__ bool routed_rows(const Routing& R, int64_t* rows) {
   return true;
 }
 
+// Codes past the caches where they would not stay there (`stream`).
+__device__ __forceinline__ void put(int8_t* to, u32x2 codes, bool stream) {
+  if (stream) __builtin_nontemporal_store(codes, reinterpret_cast<u32x2*>(to));
+  else *reinterpret_cast<u32x2*>(to) = codes;
+}
+// From 16 MB of codes on: 65536 x 7168 in 223 us (248 through the caches), 4095 x 7168
+// 15.1 (16.1); 1024 x 7168 with its reader 10.9 (10.6), 193 x 5920 alone 4.0 (3.5).
+bool streams(int64_t rows, int64_t k) { return rows * k >= 1 << 24; }
+
 template <int SEGS>
 __global__ __launch_bounds__(kThreads) void cast_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t k,
                                                              Routing R, int8_t* __restrict__ q,
-                                                             float* __restrict__ scale) {
+                                                             float* __restrict__ scale, bool stream) {
   if (!routed_rows(R, &rows)) return;
   const int lane = threadIdx.x & 63;
   const int64_t r = (int64_t)line_index() * (kThreads / 64) + uni((int32_t)(threadIdx.x >> 6));
@@ -45,7 +54,7 @@ __global__ __launch_bounds__(kThreads) void cast_rows_kernel(const uint16_t* __r
 #pragma unroll
   for (int s = 0; s < SEGS; ++s) {
     const int64_t col = s * kSegCols + 8 * lane;
-    if (col < k) *reinterpret_cast<u32x2*>(q + r * k + col) = cast8(v[s], c);
+    if (col < k) put(q + r * k + col, cast8(v[s], c), stream);
   }
 }
 
@@ -53,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void cast_rows_kernel(const uint16_t* __r
 template <int SEGS>
 __global__ __launch_bounds__(kThreads) void cast_wide_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t k,
                                                              Routing R, int8_t* __restrict__ q,
-                                                             float* __restrict__ scale) {
+                                                             float* __restrict__ scale, bool stream) {
   __shared__ uint32_t lmax[kThreads / 64];
   if (!routed_rows(R, &rows)) return;
   const int64_t r = line_index();
@@ -76,13 +85,13 @@ __global__ __launch_bounds__(kThreads) void cast_wide_kernel(const uint16_t* __r
 #pragma unroll
   for (int s = 0; s < SEGS; ++s) {
     const int64_t col = 8 * ((int64_t)s * kThreads + threadIdx.x);
-    if (col < k) *reinterpret_cast<u32x2*>(q + r * k + col) = cast8(v[s], c);
+    if (col < k) put(q + r * k + col, cast8(v[s], c), stream);
   }
 }
 
 __global__ __launch_bounds__(kThreads) void cast_long_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t k,
                                                              Routing R, int8_t* __restrict__ q,
-                                                             float* __restrict__ scale) {
+                                                             float* __restrict__ scale, bool stream) {
   __shared__ uint32_t lmax[kThreads / 64];
   if (!routed_rows(R, &rows)) return;
   const int64_t r = line_index();
@@ -97,19 +106,20 @@ __global__ __launch_bounds__(kThreads) void cast_long_kernel(const uint16_t* __r
   for (int w = 0; w < kThreads / 64; ++w) m = max(m, lmax[w]);
   const RowCast c = row_cast(m);
   if (threadIdx.x == 0) scale[r] = c.scale;
-  for (int64_t i = threadIdx.x; i < k / 8; i += kThreads) *reinterpret_cast<u32x2*>(q + r * k + 8 * i) = cast8(row[i], c);
+  for (int64_t i = threadIdx.x; i < k / 8; i += kThreads) put(q + r * k + 8 * i, cast8(row[i], c), stream);
 }
 
 template <int SEGS>
 void launch(const uint16_t* x, int64_t rows, int64_t k, const Routing& R, int8_t* q, float* scale, hipStream_t st) {
   const uint32_t per = kThreads / 64;
   hipLaunchKernelGGL((cast_rows_kernel<SEGS>), line_grid((uint32_t)((rows + per - 1) / per)), dim3(kThreads), 0, st, x,
-                     rows, k, R, q, scale);
+                     rows, k, R, q, scale, streams(rows, k));
 }
 
 template <int SEGS>
 int launch_wide(const uint16_t* x, int64_t rows, int64_t k, const Routing& R, int8_t* q, float* scale, hipStream_t st) {
-  hipLaunchKernelGGL((cast_wide_kernel<SEGS>), line_grid((uint32_t)rows), dim3(kThreads), 0, st, x, rows, k, R, q, scale);
+  hipLaunchKernelGGL((cast_wide_kernel<SEGS>), line_grid((uint32_t)rows), dim3(kThreads), 0, st, x, rows, k, R, q, scale,
+                     streams(rows, k));
   return hip_status();
 }
 
@@ -122,7 +132,8 @@ int cast(const uint16_t* x, int64_t rows, int64_t k, const Routing& R, int8_t* q
   if (segs > kRegSegs) {
     if (segs <= 12) return launch_wide<3>(x, rows, k, R, q, scale, st);
     if (segs <= 16) return launch_wide<4>(x, rows, k, R, q, scale, st);
-    hipLaunchKernelGGL(cast_long_kernel, line_grid((uint32_t)rows), dim3(kThreads), 0, st, x, rows, k, R, q, scale);
+    hipLaunchKernelGGL(cast_long_kernel, line_grid((uint32_t)rows), dim3(kThreads), 0, st, x, rows, k, R, q, scale,
+                       streams(rows, k));
   } else if (segs > 2 && rows <= 512) {
     return segs <= 4 ? launch_wide<1>(x, rows, k, R, q, scale, st) : launch_wide<2>(x, rows, k, R, q, scale, st);
   } else if (segs <= 1) {

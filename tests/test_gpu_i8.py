@@ -43,7 +43,8 @@ def rows_of(rng, m, k):
 
 
 CASTS = [(1, 16), (3, 48), (9, 512), (7, 528), (12, 1040), (5, 2064), (8, 4112), (9, 6160), (9, 7168), (8, 8192), (8, 8208),
-         (3, 131056), (300, 256)]
+         (3, 131056), (300, 256), (513, 1040), (600, 2064),
+         (16400, 1040), (4200, 4112), (1100, 16400)]  # codes past the caches
 
 
 @pytest.mark.parametrize("m,k", CASTS)
