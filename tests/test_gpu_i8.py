@@ -125,7 +125,7 @@ def test_linear(m, n, k, kind):
     I.same_bits(linear(*ops, kind), I.product(*ops), "out")
 
 
-@pytest.mark.parametrize("m", [1, 40, 200])
+@pytest.mark.parametrize("m", [1, 16, 40, 200])
 def test_linear_longest_sums(m):
     """All codes -128 at the largest k: the sum is 2147221504, just below 2^31."""
     n, k = 32, i8.MAX_K
@@ -331,6 +331,28 @@ def test_token_linear(T, E, topk, k, f):
     torch.cuda.synchronize()
     assert out.guards_intact()
     I.same_bits(out.t, token_product(xt, ids, qb, sb, 1), "out")
+
+
+@pytest.mark.parametrize("pairs,E,k", [(100, 32, 272), (1024, 300, 528), (128, 8, 1040), (999, 16, 64)])
+def test_all_tokens_choose_one_expert_of_many(pairs, E, k):
+    """More rows for one expert than its share: further passes over them."""
+    log(f"one expert pairs={pairs} E={E} k={k}")
+    rng, f = np.random.default_rng(pairs), 48
+    xt = R.bf16_round(rng.standard_normal((pairs, k)))[0]
+    qb, sb = rng.integers(-128, 128, (E, 2 * f, k), dtype=np.int8), np.full((E, 2 * f), 0.01 / k ** 0.5, np.float32)
+    ids = np.full((pairs, 1), E - 2, np.int32)
+    ids[pairs // 2] = 0
+    y, h = Guarded(4 * pairs * 2 * f, torch.float32, (pairs, 2 * f)), Guarded(2 * pairs * f, torch.bfloat16, (pairs, f))
+    i8.i8_token_linear(xt.to("cuda:0"), dev(ids), dev(qb), dev(sb), y.t)
+    i8.i8_token_glu(xt.to("cuda:0"), dev(ids), dev(qb), dev(sb), h.t)
+    torch.cuda.synchronize()
+    assert y.guards_intact() and h.guards_intact()
+    q, s = I.cast(xt.float().numpy())
+    want = I.product(q, s, qb[E - 2], sb[E - 2])
+    want[pairs // 2] = I.product(q[pairs // 2:pairs // 2 + 1], s[pairs // 2:pairs // 2 + 1], qb[0], sb[0])[0]
+    I.same_bits(y.t, want, "out")
+    g, u = want[:, :f].astype(np.float64), want[:, f:].astype(np.float64)
+    R.check(h.t, R.act(g, "silu")[0] * u, R.glu_bound(g, u, 2 * R.U * np.abs(g), 2 * R.U * np.abs(u), "silu"), "h")
 
 
 def test_token_projection_and_grouped_forms_agree():

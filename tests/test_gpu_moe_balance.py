@@ -97,6 +97,21 @@ def test_balance(T, E, k, ends, score, dtype):
     assert torch.equal(d.cpu()[plain], add[plain])                     # masked: what was there before, exactly
 
 
+@pytest.mark.parametrize("T,E,k,ends", [
+    (70000, 3, 2, list(range(1, moe.MAX_SEQS)) + [69999]), (1 << 20, 16, 16, None), (1 << 20, 16, 16, [5, 5, 700000])])
+def test_most_sequences_and_most_pairs(T, E, k, ends):
+    log(f"balance T={T} E={E} k={k}")
+    rng, lt, l, ids = make(T, T, E, k, "f32")
+    got, d = both(lt, ids, ends, "softmax", 0.3, k)
+    loss, counts, probs, tokens, grad, scale = I.balance(l, ids, ends, "softmax", 0.3, k)
+    assert np.array_equal(got["counts"].cpu().numpy(), counts) and np.array_equal(got["seq_tokens"].cpu().numpy(), tokens)
+    rel, n = rel_of(l, E), tokens[:, None].astype(np.float64)
+    worst = float(rel.max())
+    R.check(got["probs"], probs, probs * (worst + (n + 24) * R.U) + n * 1e-37, "probs")
+    R.check(got["loss"], np.array([loss]), np.array([loss * (worst + (n.max() + E + len(tokens) + 40) * R.U) + 1e-37]), "loss")
+    R.check(d, grad, scale * (3 * rel + worst + (E + 24) * R.U) + 2 * R.U * np.abs(grad) + 1e-36, "dlogits")
+
+
 def test_without_options():
     rng, lt, l, ids = make(9, 50, 24, 3, "f32")
     _, d = both(lt, ids, None, "softmax", 1.0, 3)
