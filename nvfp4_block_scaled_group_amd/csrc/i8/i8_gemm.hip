@@ -10,8 +10,11 @@
 //
 // What bounds it: at large sizes power (8192 x 8192 x 8192 in 410 to 450 us, 2.4 to
 // 2.7 POP/s, matrix units 63% busy at a clock of 1.5 GHz; the same launch on
-// zeros runs at 3.4), with few steps a tile its start and epilogue (16384 x 1024 x
-// 8192: 158 us, 1.7 POP/s), with few tiles the copies' latency.
+// zeros runs at 3.4; gated block of 65536 rows of 32 experts, 7168 x 2 x 2048: 1.62
+// to 1.73 ms, 2.2 to 2.4), with few steps a tile its start and epilogue (32768 rows of
+// 64 experts, 2048 x 7168, fp32: 600 to 660 us, 1.5 to 1.6 POP/s), with few rows an
+// expert the weights' way from memory (256 rows of each of 32, 7168 x 2 x 2048: 261 us,
+// 3.6 TB/s), with few tiles the copies' latency.
 #include <algorithm>
 #include <cmath>
 

@@ -17,10 +17,10 @@
 // by an atomic.
 //
 // What bounds it: reading the logits and, in the gradient, writing as much
-// (32768 x 256 fp32: 10.3 to 11.5 us forward, 3.2 TB/s of logits and choices; 5.2
-// for the join, three quarters of it a launch and two dependent rounds of loads;
-// 15.5 for the gradient, 4.3 TB/s).  Small batches cost a launch (33 x 8: one work-
-// group, 3.7 us, and 2.5 for the gradient).
+// (32768 x 256 fp32: 10.4 us forward, 3.3 TB/s of logits and choices; 5.3 for the
+// join, three quarters of it a launch and two dependent rounds of loads; 14.8 for
+// the gradient, 4.5 TB/s).  Small batches cost a launch (33 x 8: one work-group,
+// 4.0 us, and 2.9 for the gradient).
 #include <algorithm>
 
 #include "moe_logits.hpp"
