@@ -624,7 +624,7 @@ extern "C" {
 // Grows with the rows, so that it serves every smaller batch too.
 int64_t i8_linear_workspace(int64_t rows, int64_t k, int64_t n) {
   if (rows < 0 || rows > kMaxRows || !valid_k(k) || !valid_n(n)) return NVFP4G_EINVAL;
-  return rows <= kFewRows ? 0 : std::min<int64_t>(kMaxWorkspace, kMaxParts * rows * n * 4);
+  return rows <= kFewRows && few(rows, k) ? 0 : std::min<int64_t>(kMaxWorkspace, kMaxParts * rows * n * 4);
 }
 
 int i8_linear(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q,
@@ -638,7 +638,7 @@ int i8_linear(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, 
   if (need && (!workspace || workspace_bytes < need)) return NVFP4G_EINVAL;
   if (!aligned(workspace, 16)) return NVFP4G_EALIGN;
   if (rows == 0) return NVFP4G_OK;
-  if (rows <= kFewRows) return few_rows(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, (hipStream_t)stream);
+  if (few(rows, k)) return few_rows(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, (hipStream_t)stream);
   Routing R;
   R.num_experts = 1;
   R.m_capacity = (int32_t)rows;

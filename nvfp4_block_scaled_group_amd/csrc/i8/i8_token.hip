@@ -227,12 +227,18 @@ int check_token(const uint16_t* x, int64_t pairs, int64_t k, const int32_t* ids,
   return NVFP4G_OK;
 }
 
-template <int MT>
+// NL: one tile of lines a wave instead of two while a work-group has a CU to
+// itself: the lines' way into one CU takes half as long (8 rows of 2048 x 7168: 6.8 us and
+// 8.7, of 7168 x 2048: 9.2 and 12.8, of 8192 x 8192: 17.0 and 18.4; 16 rows of 7168 x 7168: 16.7
+// and 16.1).
+template <int MT, int NL>
 int launch_few(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q,
                const float* b_scale, int64_t n, void* out, int32_t out_type, hipStream_t st) {
-  constexpr int NL = 2, kCols = 16 * NL;
+  constexpr int kCols = 16 * NL;
   auto tiles = [&](int ks) { return (n + kCols * (kTokenWaves / ks) - 1) / (kCols * (kTokenWaves / ks)); };
   const TokenPlan P = best_plan(k, (int)std::min<int64_t>(rows, 16 * MT), MT, NL, 1, tiles);
+  if (NL > 1 && tiles(P.ks) <= kCus)
+    return launch_few<MT, 1>(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, st);
   auto go = [&](auto* kernel) {
     hipLaunchKernelGGL(kernel, dim3((uint32_t)tiles(P.ks)), dim3(kTokenThreads), P.lds, st, a_q, a_scale, (int)rows, k,
                        b_q, b_scale, n, P, out);
@@ -248,7 +254,9 @@ namespace i8 {
 
 int few_rows(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q, const float* b_scale,
              int64_t n, void* out, int32_t out_type, hipStream_t st) {
-  return launch_few<kFewRows / 16>(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, st);
+  if (rows <= 16) return launch_few<1, 2>(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, st);
+  if (rows <= 32) return launch_few<2, 2>(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, st);
+  return launch_few<4, 2>(a_q, a_scale, rows, k, b_q, b_scale, n, out, out_type, st);
 }
 
 }  // namespace i8

@@ -6,7 +6,7 @@
 // element, no decode: 24 tokens of 6 among 64 experts, 2048 x 7168, 844 MB in 131 us,
 // 6.4 TB/s; 1 token of 8, 7168 x 2 x 2048, 235 MB in 38 us, 6.2 TB/s, where a quarter
 // of the time is the start, the cast of the row and the join; 8 rows of one 2048 x
-// 7168 projection 8.2 us, 1.8 TB/s, eight steps of latency).  A lane takes 16 bytes of its line at a time, four
+// 7168 projection 6.8 us, 2.2 TB/s, most of it start and one round of latency).  A lane takes 16 bytes of its line at a time, four
 // neighbouring lanes 64 in a row; the eight waves of a work-group split the
 // contraction KS ways and the lines 8 / KS ways, and join their int32 sums,
 // which are exact in any order, in LDS.  The rows are staged in LDS as codes:
@@ -259,9 +259,15 @@ __device__ __forceinline__ i32x4 joined(const i32x4* red, int group, int ks, int
 }
 
 // A projection of a few rows of codes (i8_token.hip): out [rows, n] fp32 or
-// bf16.  Past 16 rows the 128 x 128 tiles of i8_gemm.hip are as fast or faster (7168
-// x 7168: 8 rows 12.0 us and 13.9, 32 rows 15.2 and 14.2, 64 rows 27 and 15.5).
+// bf16.  It is taken while the rows fit LDS in one or two pieces; past that, and
+// where more than 16 rows are short, the 128 x 128 tiles of i8_gemm.hip are
+// faster (us, this kernel and the tiles: 32 rows of 2048 x 7168 7.3 and 11.8, 64 rows
+// 9.6 and 12.8; 24 rows of 7168 x 2048 11.0 and 14.0, 40 rows 18.0 and 14.5; 16 rows of
+// 16384 x 8192 33.7 and 26.6; 32 rows of 512 x 512 5.8 and 5.2).
 constexpr int64_t kFewRows = 16;
+inline bool few(int64_t rows, int64_t k) {
+  return rows <= 64 && rows * k <= 200000 && (rows <= kFewRows || k >= 1024);
+}
 int few_rows(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q, const float* b_scale,
              int64_t n, void* out, int32_t out_type, hipStream_t st);
 

@@ -114,6 +114,7 @@ LINEAR = [  # rows, n, k
     (64, 80, 4112), (65, 16, 16), (100, 1024, 1040), (127, 144, 112), (128, 256, 256), (129, 272, 384), (193, 528, 1488),
     (255, 48, 2064), (300, 784, 96), (513, 1040, 208), (1000, 96, 4096), (1030, 2064, 144), (2049, 512, 272),
     (8, 7168, 256), (12, 4096, 13072), (2100, 4112, 144), (9000, 4112, 48), (1500, 2304, 1040), (20, 7168, 1296), (40, 16, 7168),
+    (29, 272, 6160), (48, 144, 4112), (63, 4112, 1040), (18, 8208, 2064), (50, 528, 2064), (9, 48, 23056), (16, 8208, 1040), (15, 96, 13328),
 ]
 
 

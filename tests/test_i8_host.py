@@ -174,7 +174,8 @@ def test_linear_workspace_serves_smaller_batches(lib, k, n):
         size = i8.i8_linear_workspace(rows, k, n)
         assert last <= size <= 32 << 20, rows
         last = size
-    assert i8.i8_linear_workspace(16, k, n) == 0 < i8.i8_linear_workspace(17, k, n)
+    short = 16 * k <= 200000                                       # few and short rows need none
+    assert (i8.i8_linear_workspace(16, k, n) == 0) == short and i8.i8_linear_workspace(17, k, n) > 0
 
 
 class _NoCalls:
