@@ -192,15 +192,21 @@ TokenPlan best_plan(int64_t k, int rows, int mt, int nl, int64_t experts, Tiles 
   return P;
 }
 
-template <int MODE, int ACT, int MT>
+// NL: one tile of lines a wave in place of two while a work-group has a CU to itself
+// (the gated block needs a gate and an up tile): the lines' way into one CU takes half as
+// long (1 token, 2048 x 7168: 6.6 us and 8.7; 8 of 64 experts, 2048 x 2048: 9.4 and 9.9;
+// 32 tokens of 2 experts: 10.7 and 13.1).
+template <int MODE, int ACT, int MT, int NL = 2>
 void launch(const uint16_t* x, int64_t k, int per, const int32_t* ids, int pairs, const int8_t* bq, const float* bs,
             int64_t n, int E, void* out, hipStream_t st) {
-  constexpr int NL = 2, kCols = MODE == kModeGlu ? 16 : 32;
+  constexpr int kCols = MODE == kModeGlu ? 8 * NL : 16 * NL;
   const int64_t ocols = MODE == kModeGlu ? n / 2 : n, experts = std::min(pairs, E);
   auto tiles = [&](int ks) { return (ocols + kCols * (kTokenWaves / ks) - 1) / (kCols * (kTokenWaves / ks)); };
   // an expert has at most one pair of a token, or takes more passes
   const int rows = std::min((pairs + per - 1) / per, 16 * MT);
   const TokenPlan P = best_plan(k, rows, MT, NL, experts, tiles);
+  if constexpr (MODE == kModeLinear && NL > 1)
+    if (experts * tiles(P.ks) <= kCus) return launch<MODE, ACT, MT, 1>(x, k, per, ids, pairs, bq, bs, n, E, out, st);
   hipLaunchKernelGGL((token_kernel<MODE, ACT, MT, NL>), dim3((uint32_t)tiles(P.ks), (uint32_t)pairs),
                      dim3(kTokenThreads), P.lds, st, x, k, per, ids, pairs, bq, bs, n, E, P, out);
 }
@@ -227,10 +233,8 @@ int check_token(const uint16_t* x, int64_t pairs, int64_t k, const int32_t* ids,
   return NVFP4G_OK;
 }
 
-// NL: one tile of lines a wave instead of two while a work-group has a CU to
-// itself: the lines' way into one CU takes half as long (8 rows of 2048 x 7168: 6.8 us and
-// 8.7, of 7168 x 2048: 9.2 and 12.8, of 8192 x 8192: 17.0 and 18.4; 16 rows of 7168 x 7168: 16.7
-// and 16.1).
+// NL as above (8 rows of 2048 x 7168: 6.8 us and 8.7, of 7168 x 2048: 9.2 and 12.8, of
+// 8192 x 8192: 17.0 and 18.4; 16 rows of 7168 x 7168: 16.7 and 16.1).
 template <int MT, int NL>
 int launch_few(const int8_t* a_q, const float* a_scale, int64_t rows, int64_t k, const int8_t* b_q,
                const float* b_scale, int64_t n, void* out, int32_t out_type, hipStream_t st) {

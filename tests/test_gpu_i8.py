@@ -115,6 +115,7 @@ LINEAR = [  # rows, n, k
     (255, 48, 2064), (300, 784, 96), (513, 1040, 208), (1000, 96, 4096), (1030, 2064, 144), (2049, 512, 272),
     (8, 7168, 256), (12, 4096, 13072), (2100, 4112, 144), (9000, 4112, 48), (1500, 2304, 1040), (20, 7168, 1296), (40, 16, 7168),
     (29, 272, 6160), (48, 144, 4112), (63, 4112, 1040), (18, 8208, 2064), (50, 528, 2064), (9, 48, 23056), (16, 8208, 1040), (15, 96, 13328),
+    (8, 66064, 272), (20, 66064, 1040), (40, 66064, 1040),  # more work-groups than CUs
 ]
 
 
@@ -280,7 +281,7 @@ TOKENS = [  # T, E, topk, k, f
     (1, 1, 1, 16, 16), (1, 8, 8, 176, 48), (3, 4, 2, 112, 16), (17, 4, 2, 128, 64), (33, 1, 1, 272, 32), (64, 8, 8, 256, 80),
     (24, 64, 6, 2048, 128), (2, 3, 3, 7168, 32), (4, 2, 1, 4112, 48), (7, 2, 2, 528, 16), (100, 2, 2, 64, 16), (60, 1, 16, 64, 16),
     (24, 2, 1, 2064, 32), (29, 1, 1, 7168, 32), (32, 16, 8, 96, 1040), (64, 1, 1, 13072, 16), (1, 2, 1, 131056, 16),
-    (9, 1, 1, 20000, 32),
+    (9, 1, 1, 20000, 32), (16, 64, 4, 272, 1040), (64, 64, 16, 272, 1040), (64, 32, 16, 272, 2064),
 ]
 
 
