@@ -6,7 +6,7 @@
 // element, no decode: 24 tokens of 6 among 64 experts, 2048 x 7168, 844 MB in 131 us,
 // 6.4 TB/s; 1 token of 8, 7168 x 2 x 2048, 235 MB in 38 us, 6.2 TB/s, where a quarter
 // of the time is the start, the cast of the row and the join; 8 rows of one 2048 x
-// 7168 projection 6.8 us, 2.2 TB/s, most of it start and one round of latency).  A lane takes 16 bytes of its line at a time, four
+// 7168 projection 5.9 us, 2.5 TB/s, most of it start and one round of latency).  A lane takes 16 bytes of its line at a time, four
 // neighbouring lanes 64 in a row; the eight waves of a work-group split the
 // contraction KS ways and the lines 8 / KS ways, and join their int32 sums,
 // which are exact in any order, in LDS.  The rows are staged in LDS as codes:
