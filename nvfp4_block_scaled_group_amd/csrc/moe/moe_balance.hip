@@ -37,11 +37,11 @@ constexpr int kChunks = 256;    // chunks of a large batch: one for each CU
 constexpr int kOneRows = 128;   // rows of one sequence that one work-group takes by itself
 constexpr int kJoinCols = 32;   // columns of a joining work-group
 
-// The first sequence whose end is above row t (num_seqs if none): the row's
-// sequence.  Whatever the ends hold, the result is in 0 .. num_seqs.
-__device__ __forceinline__ int sequence_of(const int32_t* ends, int num_seqs, int64_t t) {
+// The first sequence from lo on whose end is above row t (num_seqs if none): the
+// row's sequence.  Whatever the ends hold, the result is in lo .. num_seqs.
+__device__ __forceinline__ int sequence_of(const int32_t* ends, int num_seqs, int64_t t, int lo = 0) {
   if (!ends) return 0;
-  int lo = 0, hi = num_seqs;
+  int hi = num_seqs;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (ends[mid] > t) hi = mid; else lo = mid + 1;
@@ -132,9 +132,15 @@ __global__ __launch_bounds__(fwd_threads(VPL, SMALL)) void balance_kernel(
   const int64_t c0 = (int64_t)blockIdx.x * rows, c1 = min(c0 + rows, tokens);
   if (!whole && blockIdx.x == 0 && tid == 0) *P.done = 0;
   int64_t at = c0;
-  for (int s = sequence_of(ends, num_seqs, c0); s < num_seqs && at < c1; ++s) {
+  for (int s = sequence_of(ends, num_seqs, c0); s < num_seqs && at < c1;) {
     const int64_t to = ends ? min<int64_t>(ends[s], c1) : c1;
-    if (to <= at) continue;
+    // Empty sequences, however many, by one search: ends padded to a fixed number
+    // end with a long run of them (8191 rows of 64 experts in 11 sequences padded to
+    // 65535: 2.3 ms, the same as without a row; one after another 9 ms more).
+    if (to <= at) {
+      s = sequence_of(ends, num_seqs, at, s + 1);
+      continue;
+    }
     const int64_t t0 = at + tid / LANES, p0 = at * topk + tid, p1 = to * topk;
     float l[VPL];
     load_logits<T, VPL>(logits + min(t0, tokens - 1) * E, E, li, wide, l);
@@ -198,6 +204,7 @@ __global__ __launch_bounds__(fwd_threads(VPL, SMALL)) void balance_kernel(
     if (tid == 0) P.tokens[slot] = lany;
     __syncthreads();
     at = to;
+    ++s;
   }
   // one work-group and an empty sequence
   if (whole) {

@@ -226,3 +226,46 @@ def test_results_do_not_depend_on_the_run_and_replay():
         torch.cuda.synchronize()
         assert torch.equal(dl, dwant), i
         assert all(torch.equal(b[key], want[key]) for key in want), i
+
+
+def least_us(call, reps=9):
+    times = []
+    for _ in range(reps):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return min(times)
+
+
+@pytest.mark.parametrize("where", ["behind", "between"])
+def test_long_runs_of_empty_sequences(where):
+    """Ends padded to a fixed number, the usual form for captured graphs: the real sequences get the same bits, the
+    empty ones nothing, and the call takes about as long as one whose sequences are all empty (one after another the
+    empty ones took five times as long)."""
+    T, E, k, S = 8191, 64, 6, moe.MAX_SEQS
+    rng, lt, l, ids = make(17, T, E, k, "f32")
+    real = [0, 700, 1500, 1500, 4000, 5000, 8000]                    # rows behind the last one: padding
+    cut = len(real) if where == "behind" else 3                      # real sequences before the long run
+    ends = real[:cut] + [real[cut - 1]] * (S - len(real)) + real[cut:]
+    log(f"balance {S} sequences, empty ones {where}")
+    got, d = both(lt, ids, ends, "softmax", 0.3, k)
+    few, dfew = both(lt, ids, real, "softmax", 0.3, k)
+    at = torch.tensor([i for i in range(S) if i < cut or i >= S - len(real) + cut], device="cuda:0")
+    for key in ("counts", "probs", "seq_tokens"):
+        assert torch.equal(got[key][at], few[key]), key
+        assert int((got[key] != 0).sum()) == int((few[key] != 0).sum()), key
+    # the mean is over all sequences: the same sum over another number (a weight has five roundings), in other parts
+    assert abs(float(got["loss"]) * S / len(real) - float(few["loss"])) < 64 * R.U * float(few["loss"])
+    assert float((d.double() * (S / len(real)) - dfew.double()).abs().max()) < 16 * R.U * float(dfew.abs().max())
+    dev_l, dev_ids, b = lt.to("cuda:0"), R.to_dev(ids), moe.alloc_balance(T, E, S)
+
+    def call(e):
+        e = R.to_dev(np.asarray(e, np.int32))
+        return least_us(lambda: moe.moe_balance(dev_l, dev_ids, **b, seq_ends=e))
+
+    padded, empty = call(ends), call([0] * S)
+    log(f"padded {padded:.0f} us, all empty {empty:.0f} us")
+    assert padded < 2 * empty
