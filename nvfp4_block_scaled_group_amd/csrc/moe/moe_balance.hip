@@ -14,7 +14,7 @@
 // of the two or in both from slot to slot, so slot chunk + sequence is its own
 // without any list.  A second launch adds the slots of each sequence in order,
 // and the work-group of it that ends last adds the sequences.  No float is added
-// by an atomic.
+// by an atomic.  With many sequences a third launch adds them.
 //
 // What bounds it: reading the logits and, in the gradient, writing as much
 // (32768 x 256 fp32: 10.4 us forward, 3.3 TB/s of logits and choices; 5.3 for the
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(fwd_threads(VPL, SMALL)) void balance_kernel(
     const int64_t to = ends ? min<int64_t>(ends[s], c1) : c1;
     // Empty sequences, however many, by one search: ends padded to a fixed number
     // end with a long run of them (8191 rows of 64 experts in 11 sequences padded to
-    // 65535: 2.3 ms, the same as without a row; one after another 9 ms more).
+    // 65535: 0.49 ms, the same as without a row; one after another 9 ms more).
     if (to <= at) {
       s = sequence_of(ends, num_seqs, at, s + 1);
       continue;
@@ -219,11 +219,20 @@ __global__ __launch_bounds__(fwd_threads(VPL, SMALL)) void balance_kernel(
   }
 }
 
+// The shares of the loss, in order, by a work-group.
+__device__ __forceinline__ float add_shares(const float* loss, int64_t n, float* lred) {
+  float v = 0.0f;
+  for (int64_t i = threadIdx.x; i < n; i += kFwdThreads)
+    v += __hip_atomic_load(loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return block_sum(v, lred, kFwdThreads / 64);
+}
+
 // The slots of a sequence, in order: work-group (b, s) has kJoinCols columns and
-// a share of the loss; the last one to end adds the shares in order.
+// a share of the loss; the last one to end adds the shares in order, or with
+// `apart` a launch of its own.
 __global__ __launch_bounds__(kFwdThreads) void balance_join_kernel(Slots P, int64_t tokens, int E, int topk,
                                                                    const int32_t* __restrict__ ends, int num_seqs,
-                                                                   int64_t rows, float coef, Results out) {
+                                                                   int64_t rows, float coef, bool apart, Results out) {
   constexpr int kParts = kFwdThreads / kJoinCols, kWaves = kFwdThreads / 64, kAhead = 8;
   __shared__ float lsum[kWaves][kJoinCols + 1];
   __shared__ int32_t lcount[kWaves][kJoinCols + 1];
@@ -291,17 +300,21 @@ __global__ __launch_bounds__(kFwdThreads) void balance_join_kernel(Slots P, int6
       // shares go past the caches of an XCD, and before the count that tells of them
       __hip_atomic_store(P.loss + (int64_t)s * gridDim.x + blockIdx.x, share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       const uint32_t all = gridDim.x * gridDim.y;
-      llast = __hip_atomic_fetch_add(P.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 == all;
+      llast = !apart && __hip_atomic_fetch_add(P.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 == all;
     }
   }
+  if (apart) return;
   __syncthreads();
   if (!llast) return;
-  const int64_t n = (int64_t)gridDim.x * gridDim.y;
-  float v = 0.0f;
-  for (int64_t i = tid; i < n; i += kFwdThreads)
-    v += __hip_atomic_load(P.loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  v = block_sum(v, lred, kFwdThreads / 64);
+  const float v = add_shares(P.loss, (int64_t)gridDim.x * gridDim.y, lred);
   if (tid == 0) *out.loss = v;
+}
+
+__global__ __launch_bounds__(kFwdThreads) void balance_loss_kernel(const float* __restrict__ shares, int64_t n,
+                                                                   float* __restrict__ loss) {
+  __shared__ float lred[kFwdThreads / 64];
+  const float v = add_shares(shares, n, lred);
+  if (threadIdx.x == 0) *loss = v;
 }
 
 template <class T, int LANES, int VPL, bool SIGMOID>
@@ -377,6 +390,11 @@ int64_t chunk_rows(int64_t tokens, int num_seqs) {
   if (one_group(tokens, num_seqs)) return kOneRows;
   return std::max(least_rows(tokens, num_seqs), (tokens + kChunks - 1) / kChunks);
 }
+// Joining work-groups that count themselves, so that the last one adds the
+// sequences' shares; more of them wait for each other at the counter, 18 ns apiece,
+// and a launch of its own adds (8191 rows; 64 work-groups 12 us both ways, 128:
+// 13.2 counted and 12.5 apart, 256: 16 and 13, 2048: 56 and 27, 131070: 2377 and 643).
+constexpr int64_t kCountedJoin = 128;
 int64_t join_blocks(int E) { return (E + kJoinCols - 1) / kJoinCols; }
 
 int check_balance(const void* logits, int32_t type, int64_t tokens, int32_t E, int32_t topk, int32_t score,
@@ -463,8 +481,11 @@ int moe_balance(const void* logits, int32_t logits_type, int64_t tokens, int32_t
     else typed((const uint16_t*)logits);
   });
   if (whole) return hip_status();
+  const bool apart = blocks * num_seqs > kCountedJoin;
   hipLaunchKernelGGL(balance_join_kernel, dim3((uint32_t)blocks, (uint32_t)num_seqs), dim3(kFwdThreads), 0, st, P,
-                     tokens, E, topk, seq_ends, num_seqs, rows, coef, R);
+                     tokens, E, topk, seq_ends, num_seqs, rows, coef, apart, R);
+  if (apart)
+    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFwdThreads), 0, st, P.loss, blocks * num_seqs, loss);
   return hip_status();
 }
 
