@@ -220,8 +220,9 @@ int moe_glu_bwd_graphsafe(const uint8_t* a_data, const uint8_t* a_scale,
 /* The gated block with its checkpoint in 8 bits: moe_glu, with g and u kept
  * for the backward call as whole numbers of a scale that 32 columns of a row
  * share (16 where f ends inside a group):
- *     S = bf16(max |v| / 127),   code = v / S to the nearest (ties to even),
- * value code * S, off by at most S / 2 (and two fp32 roundings).  A group whose
+ *     S = bf16(max |v| / 127),   code = the whole number nearest to v / S
+ * (both quotients rounded to fp32; ties to even), value code * S, off by at
+ * most S / 2 (and the quotient's rounding).  A group whose
  * largest magnitude is below 2^-112 is kept as zeros, one with a value that is
  * not finite as S = NaN and codes 0.  gu8 [sum_m, 2f] with g first; gu_scale
  * [2 * ceil(f / 32), sum_m], the groups of g first (m_capacity in place of

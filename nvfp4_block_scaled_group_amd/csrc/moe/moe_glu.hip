@@ -323,9 +323,18 @@ __device__ __forceinline__ u32x2 keep8(const float (&v)[8], uint16_t* scale) {
     return u32x2{0, 0};
   }
   *scale = to_bf16(__uint_as_float(m) / 127.0f);
-  // at most 127 (1 + 2^-8) / (1 - 2^-9) < 127.5: a code never passes 127
-  const float inv = 1.0f / __uint_as_float((uint32_t)*scale << 16);
-  return u32x2{codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+  // v / S, correctly rounded: a rounded reciprocal's product is an ulp off at most, and
+  // one step on its exact remainder ends there (Markstein).  At most 127 (1 + 2^-8)
+  // (1 + 2^-24)^2 < 127.497 (S is the bf16 value nearest to m / 127, which it is below
+  // by 2^-8 of itself at most): a code never passes 127.
+  const float S = __uint_as_float((uint32_t)*scale << 16), inv = 1.0f / S;
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = v[i] * inv;
+    t[i] = __builtin_fmaf(__builtin_fmaf(-q, S, v[i]), inv, q);
+  }
+  return u32x2{codes4(t[0], t[1], t[2], t[3]), codes4(t[4], t[5], t[6], t[7])};
 }
 // The value of byte i of a lane's codes, exact: the code's byte plus 128 is a
 // float in one conversion, and the 128 leave it again before the scale comes (128 s

@@ -266,3 +266,42 @@ def test_backward_wide_tiles(at, kind):
     at64 = gu[torch.from_numpy(rows).to("cuda:0")].double().cpu().numpy()
     g, u = at64[:, :f], at64[:, f:]
     R.check(again.t[torch.from_numpy(rows).to("cuda:0")], R.act(g, kind)[0] * u, R.glu_bound(g, u, 0 * g, 0 * u, kind), "h")
+
+
+def test_codes_are_the_nearest_to_the_quotient():
+    """g and u that are exact in the kernel, at and beside the ties between two codes and at scales that are themselves
+    ties between two bf16 values: the code is the whole number nearest to the fp32 quotient, ties to even, and a
+    group's largest is +-127."""
+    G, k, M = 64, 128, 128
+    f, rng, F32 = 32 * G, np.random.default_rng(4), np.float32
+    want = np.empty((2 * G, 32))                       # [group of g then u, column]
+    for j in range(2 * G):
+        e, top = int(rng.integers(-40, 40)), 1 + int(rng.integers(0, 128)) / 128
+        top += (0, 1, -1)[j % 3] / 256                 # max / 127: a bf16 value, or half way to the next or the last one
+        step = float(torch.tensor(top * 2.0 ** e, dtype=torch.float64).to(torch.bfloat16))
+        ties = ((rng.integers(0, 126, 31) + 0.5) * step).astype(F32)              # 16 bits: exact
+        beside = np.nextafter(ties, F32(np.inf) * rng.choice([-1, 1], 31).astype(F32))
+        want[j, 0], want[j, 1:] = 127 * top * 2.0 ** e, np.where(rng.random(31) < 0.6, ties, beside)
+    # a line's value is amax / 2688 in fp32: the amax that gives the wanted one, or one beside it
+    want = want.reshape(-1).astype(F32)
+    amax = (want.astype(np.float64) * 2688).astype(F32)
+    for near in (np.nextafter(amax, F32(np.inf)), np.nextafter(amax, F32(0))):
+        amax = np.where((amax / F32(2688) != want) & (near / F32(2688) == want), near, amax)
+    v = (amax / F32(2688)).reshape(2 * G, 32)
+    one = np.zeros((2 * f, k // 2), np.uint8)
+    one[:, 0] = 0x02                                   # 1.0, then zeros
+    rows = np.zeros((M, k // 2), np.uint8)
+    rows[:, 0] = np.where(np.arange(M) % 2, 0x0A, 0x02)  # -1.0 in the odd rows
+    a = (rows, np.full((M, k // 16), 0x38, np.uint8), np.full(M, 2688, F32))
+    b = (one, np.full((2 * f, k // 16), 0x38, np.uint8), amax)
+    h, kept = torch.empty((M, f), dtype=torch.bfloat16, device="cuda:0"), moe.alloc_keep8(M, f)
+    moe.moe_glu_keep8(*on_device(a, b, 1, 2 * f), [M], h, **kept)
+    s = torch.from_numpy(np.abs(v).max(1) / F32(127)).to(torch.bfloat16)
+    codes = np.rint(v / s.float().numpy()[:, None]).astype(np.int64).reshape(-1)
+    got, scale = kept["gu8"].cpu().numpy().astype(np.int64), kept["gu_scale"].cpu()
+    assert torch.equal(scale, s[:, None].expand(2 * G, M))
+    # the cases do what they are for: exact ties, and ties of the scale
+    assert (np.abs(v / s.float().numpy()[:, None] % 1) == 0.5).sum() > 500
+    assert (np.abs(codes.reshape(-1, 32)[:, 0]) == 127).all()
+    for r in range(M):
+        assert np.array_equal(got[r], -codes if r % 2 else codes), (r, np.nonzero(got[r] != (-codes if r % 2 else codes))[0][:5])
