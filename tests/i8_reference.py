@@ -103,6 +103,27 @@ def balance(logits, ids, ends, score, coef, topk):
     return loss, counts, probs, tokens, grad, p * slope * scale
 
 
+def balance_bounds(logits, ids, ends, score, coef, topk, rel):
+    """What probs and the loss may be off by, from the depth of their sums and not from their length.  rel [T, E]: the
+    relative error of a sigmoid or exponential.  All terms are positive, so a sum is off by its terms' errors and one u
+    for each addition that a term goes through: of probs at most 32 rows of a lane, 3 exchanges, 16 waves, 8 slots of a
+    joining part, an exchange and 16 waves (80 u); of the loss also the product with the count, 6 exchanges (16 experts
+    of a thread and 16 waves where one work-group does it all, without a join), 7 roundings of the weight, up to 128
+    shares of a thread, 6 exchanges and 16 waves (256 u)."""
+    p, _, any_ = probabilities(logits, score)
+    T, E = logits.shape
+    each = p * (rel + (p * rel).sum(1, keepdims=True))        # its own error, and that of the sum it is divided by
+    loss, counts, probs, tokens, _, _ = balance(logits, ids, ends, score, coef, topk)
+    ends = [T] if ends is None else list(ends)
+    off, loss_off, b = np.zeros((len(ends), E)), 256 * R.U * loss + 1e-37, 0
+    for s, e in enumerate(ends):
+        if tokens[s]:
+            off[s] = each[b:e].sum(0) + 80 * R.U * probs[s] + tokens[s] * 1e-37
+            loss_off += coef / len(ends) * E / (topk * float(tokens[s]) ** 2) * float(counts[s] @ off[s])
+        b = e
+    return off, loss_off
+
+
 # ----------------------------------------------------------- 8-bit checkpoint
 
 def group_of(f):

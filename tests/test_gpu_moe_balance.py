@@ -306,3 +306,24 @@ def test_sequences_are_added_by_the_last_one_or_apart(S, E):
         g.replay() if i % 2 else moe.moe_balance(dev_l, dev_ids, **b, seq_ends=e, coef=0.3)
         torch.cuda.synchronize()
         assert all(torch.equal(b[key], first[key]) for key in first), i
+
+
+SUMS = [  # T, E, k, ends: all chunks and slots in use, one work-group alone, as many sequences as there can be
+    (1 << 20, 16, 16, None), (1 << 20, 16, 16, [5, 5, 700000]), (40000, 16, 2, None), (33000, 40, 4, [1, 20000, 20001, 32000]),
+    (1000, 256, 8, None), (128, 64, 6, None), (140, 4096, 4, None), (300, 2048, 5, [10, 290]),
+    (70000, 3, 2, list(range(1, moe.MAX_SEQS)) + [69999]), (70000, 64, 2, list(range(1, moe.MAX_SEQS)) + [69999]),
+]
+
+
+@pytest.mark.parametrize("at", range(len(SUMS)))
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_sums_are_off_by_their_depth(at, score):
+    """Bounds that the rows of a fraction of a chunk would pass, if they were lost (test_i8_host.py shows it)."""
+    T, E, k, ends = SUMS[at]
+    log(f"balance sums T={T} E={E} k={k} {score}")
+    rng, lt, l, ids = make(T + E + 1, T, E, k, "f32")
+    got, _ = both(lt, ids, ends, score, 0.3, k)
+    loss, counts, probs, tokens, _, _ = I.balance(l, ids, ends, score, 0.3, k)
+    off, loss_off = I.balance_bounds(l, ids, ends, score, 0.3, k, rel_of(l, E))
+    R.check(got["probs"], probs, off, "probs")
+    R.check(got["loss"], np.array([loss]), np.array([loss_off]), "loss")

@@ -291,6 +291,30 @@ def test_balance_reference_follows_differences(score):
     assert abs(I.balance(np.zeros((8, 4)), even, None, score, 0.25, k)[0] - 0.25) < 1e-12
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("at", [0, 1, 2, 3])
+def test_balance_bounds_notice_lost_rows(score, at):
+    """Without the probabilities of one chunk, or of a 32nd of one, probs and the loss leave the GPU test's bounds."""
+    from test_gpu_moe_balance import SUMS, make, rel_of
+    T, E, k, ends = SUMS[at]
+    rng, lt, l, ids = make(T + E + 1, T, E, k, "f32")
+    loss, counts, probs, tokens, _, _ = I.balance(l, ids, ends, score, 0.3, k)
+    off, loss_off = I.balance_bounds(l, ids, ends, score, 0.3, k, rel_of(l, E))
+    p, _, _ = I.probabilities(l, score)
+    rows = max(32, -(-T // 256))
+    cuts = [T] if ends is None else ends
+    for chunk in (1, 100, 150):
+        for lost in (rows, max(rows // 32, 1)):
+            b = chunk * rows
+            s = int(np.searchsorted(cuts, b, side="right"))
+            gone = p[b:b + lost].sum(0)
+            assert b + lost <= cuts[s]
+            assert (gone > 2 * off[s]).any(), (chunk, lost)
+            if lost == rows:
+                weight = 0.3 / len(cuts) * E / (k * float(tokens[s]) ** 2)
+                assert weight * float(counts[s] @ gone) > 2 * loss_off, chunk
+
+
 def test_cast_reference_is_the_nearest_code():
     rng = np.random.default_rng(1)
     x = R.bf16_round(rng.standard_normal((50, 64)) * np.exp(5 * rng.standard_normal((50, 1))))[0].float().numpy()
