@@ -377,3 +377,43 @@ def test_token_projection_and_grouped_forms_agree():
         ws = torch.empty(i8.i8_linear_workspace(rows, k, n), dtype=torch.uint8, device="cuda:0")
         i8.i8_linear(made["q"][:rows], made["scale"][:rows], qb[0], sb[0], few, ws)
         assert torch.equal(few, y[0][:rows])
+
+
+DEVICE = [  # splits, spare rows, n (f of the gated block), k: few tiles, long contractions
+    ([128, 0, 256], 128, 528, 1040), ([128, 0, 256], 128, 272, 2064), ([0, 384, 128, 0], 256, 1040, 2064),
+    ([256, 0, 0, 128], 128, 48, 1296), ([128] * 7 + [0], 128, 144, 7168), ([0, 0, 128], 0, 16, 4112), ([0, 0], 256, 64, 1040),
+]
+
+
+@pytest.mark.parametrize("splits,spare,n,k", DEVICE)
+@pytest.mark.parametrize("kind", ["f32", "bf16", "silu", "gelu"])
+def test_device_routing_of_long_contractions(splits, spare, n, k, kind):
+    """The tiles with four stages under device routing (test_i8_host.py shows that these cases take them): experts
+    without rows, rows past the last group left as they were."""
+    log(f"device routing {splits} + {spare} n={n} k={k} {kind}")
+    glu, M, E = kind in ACTS, sum(splits), len(splits)
+    cap = M + spare
+    qa, sa, qb, sb = operands(np.random.default_rng(n + k + 2), cap, 2 * n if glu else n, k, E)
+    sb = (sb * np.float32(1e-4)).astype(np.float32)
+    if glu:
+        sa[1] = 0.5                                                 # finite throughout
+    t, size = (torch.bfloat16, 2) if glu else TYPES[kind]
+    out, status = Guarded(size * cap * n, t, (cap, n)), torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    ops = [dev(v) for v in (qa, sa, qb, sb)]
+    f, more = (i8.i8_group_glu_graphsafe, dict(act=ACTS[kind])) if glu else (i8.i8_group_gemm_graphsafe, {})
+
+    def call(offs, out):
+        f(*ops, torch.tensor(offs, dtype=torch.int32, device="cuda:0"), out, status, **more)
+        torch.cuda.synchronize()
+
+    call(B.offsets_from_splits(splits), out.t)
+    assert int(status) == 0 and out.guards_intact() and untouched(out.t[M:])
+    if M:
+        own = (qa[:M], sa[:M], qb, sb)
+        if glu:
+            R.check(out.t[:M], *glu_expect(own, splits, n, kind), "h")
+        else:
+            I.same_bits(out.t[:M], I.grouped(*own, splits), "out")
+    out.t.view(torch.uint8).fill_(CANARY)
+    call([0] * (E - 1) + [cap + 128], out.t)
+    assert int(status) & B.NVFP4G_DEV_OVERFLOW and untouched(out.t) and out.guards_intact()

@@ -178,6 +178,51 @@ def test_linear_workspace_serves_smaller_batches(lib, k, n):
     assert (i8.i8_linear_workspace(16, k, n) == 0) == short and i8.i8_linear_workspace(17, k, n) > 0
 
 
+# ------------------------------------------- which kernels the GPU tests reach
+
+FEW, BIG, MID, MID4, MID4_PARTS = 6, 0, 1, 2, 5
+
+
+@pytest.fixture(scope="module")
+def choice():
+    import sys
+    sys.path.insert(0, os.path.join(ROOT, "tests", "hip"))
+    import build_selftest
+    if not os.path.exists(build_selftest.CHOICE_LIB):
+        build_selftest.build_choice()
+    fn = ctypes.CDLL(build_selftest.CHOICE_LIB).i8_choice
+    fn.argtypes = [ctypes.c_int, ctypes.c_int] + [ctypes.c_int64] * 3 + [ctypes.c_int32, ctypes.c_void_p]
+
+    def ask(kind, rows, n, k, splits=None, device=False):
+        routing = 0 if splits is None else 2 if device else 1
+        E, given = (1, None) if splits is None else (len(splits), (ctypes.c_int64 * len(splits))(*splits))
+        return fn({"f32": 0, "bf16": 1, "glu": 2}[kind], routing, rows, n, k, E, given)
+    return ask
+
+
+def parameters(test, names):
+    return next(m.args[1] for m in test.pytestmark if m.args and m.args[0] == names)
+
+
+def test_gpu_cases_reach_every_tile_of_a_projection(choice):
+    import test_gpu_i8 as T
+    for kind in ("f32", "bf16"):
+        assert {choice(kind, m, n, k) for m, n, k in T.LINEAR} == {FEW, BIG, MID, MID4, MID4_PARTS}
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "glu"])
+def test_gpu_cases_reach_every_tile_of_the_experts(choice, kind):
+    import test_gpu_i8 as T
+    assert {choice(kind, sum(s), n, k, s) for s, n, k in T.GROUPS} == {BIG, MID, MID4}
+    wide = 1 if kind != "glu" else 2                               # the tests below halve n for the gated block
+    small = parameters(T.test_device_routing_writes_the_routed_rows_alone, "splits,spare")
+    large = parameters(T.test_device_routing_of_large_tiles, "splits,spare")
+    assert {choice(kind, sum(s) + more, 96 // wide, 208, s, device=True) for s, more in small} == {MID}
+    n = 2064 if kind != "glu" else 1040
+    assert BIG in {choice(kind, sum(s) + more, n, 400, s, device=True) for s, more in large}
+    assert {choice(kind, sum(s) + more, n, k, s, device=True) for s, more, n, k in T.DEVICE} == {MID4}
+
+
 class _NoCalls:
     def __getattr__(self, name):
         def fail(*args, **kwargs):
