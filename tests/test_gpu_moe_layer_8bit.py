@@ -215,3 +215,32 @@ def test_examples_run(capsys, monkeypatch):
                                       "--topk", "2"])
     L.main()
     assert "balance loss" in capsys.readouterr().out
+
+
+def test_two_calls_at_once_all_end(made):
+    """As above, with a record of every round: a thread that stops short, or does not end, fails."""
+    L, g, w, shared, kept_layer, layer = made
+    xs = [rand(g, T, H) for _ in range(2)]
+    alone = [(layer.batch(x), layer.decode(x[:5].contiguous()), *kept_layer.forward(x)[:2]) for x in xs]
+    torch.cuda.synchronize()
+    rounds, errors = [[], []], []
+
+    def run(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for n in range(10):
+                    got = (layer.batch(xs[i]), layer.decode(xs[i][:5].contiguous()), *kept_layer.forward(xs[i])[:2])
+                    s.synchronize()
+                    assert all(torch.equal(a, b) for a, b in zip(got, alone[i])), n
+                    rounds[i].append(n)
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,), daemon=True) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not errors, errors
+    assert not any(t.is_alive() for t in threads) and rounds == [list(range(10))] * 2
