@@ -14,7 +14,8 @@ using namespace i8;
 constexpr int kSegCols = 512;  // a wave's 16-byte loads: 8 columns a lane
 constexpr int kRegSegs = 8;     // of a wave's row at most
 
-// Rows that exist: all of them, or the routed ones.
+// Rows that exist: all of them, or the routed ones.  Every wave checks all ends:
+// up to 256 experts that costs nothing (65536 x 7168 in 250 us), 1024 of them 404.
 __device__ __forceinline__ bool routed_rows(const Routing& R, int64_t* rows) {
   if (R.d_offs) {
     if (!routing_ok(R)) return false;

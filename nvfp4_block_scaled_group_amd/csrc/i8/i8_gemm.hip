@@ -11,8 +11,8 @@
 // What bounds it: at large sizes power (8192 x 8192 x 8192 in 410 to 450 us, 2.4 to
 // 2.7 POP/s, matrix units 63% busy at a clock of 1.5 GHz; the same launch on
 // zeros runs at 3.4; gated block of 65536 rows of 32 experts, 7168 x 2 x 2048: 1.62
-// to 1.73 ms, 2.2 to 2.4), with few steps a tile its start and epilogue (32768 rows of
-// 64 experts, 2048 x 7168, fp32: 600 to 660 us, 1.5 to 1.6 POP/s), with few rows an
+// to 1.76 ms, 2.2 to 2.4), with few steps a tile its start and epilogue (32768 rows of
+// 64 experts, 2048 x 7168, fp32: 600 to 660 us, 682 with a row of them, 1.4 to 1.6 POP/s), with few rows an
 // expert the weights' way from memory (256 rows of each of 32, 7168 x 2 x 2048: 261 us,
 // 3.6 TB/s), with few tiles the copies' latency.
 #include "i8_choice.hpp"
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(S::kThreads, S::OCC) void product_kernel(Operands O
       if (inside && r0 + r + srow < T.rows) {
         u32x4* to = reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(out) + SIZE * at);
         const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
-        // results past the caches, which keep the operands (32768 rows, 2048 x 7168, fp32: 604 us and 614;
+        // results past the caches, which keep the operands (in turn, 32768 rows, 2048 x 7168, fp32: 604 us and 614;
         // 2048 x 2048 x 2048: 14.3 and 14.9); parts are read again at once
         if (EPI == kParts) *to = v;
         else __builtin_nontemporal_store(v, to);

@@ -17,9 +17,9 @@
 // by an atomic.  With many sequences a third launch adds them.
 //
 // What bounds it: reading the logits and, in the gradient, writing as much
-// (32768 x 256 fp32: 10.4 us forward, 3.3 TB/s of logits and choices; 5.3 for the
-// join, three quarters of it a launch and two dependent rounds of loads; 14.8 for
-// the gradient, 4.5 TB/s).  Small batches cost a launch (33 x 8: one work-group,
+// (32768 x 256 fp32: 10.4 to 11.0 us forward, 3.1 to 3.3 TB/s of logits and choices, of
+// which two to three dependent rounds of loads; 5.3 for the join, three quarters of it a
+// launch and two more such rounds; 14.7 to 15.1 for the gradient, 4.5 TB/s).  Small batches cost a launch (33 x 8: one work-group,
 // 4.0 us, and 2.9 for the gradient).
 #include <algorithm>
 

@@ -309,9 +309,11 @@ constexpr int kGroup = MOE_KEEP8_GROUP;  // columns of a scale: four lanes hold 
 static_assert(kGroup == 32, "the reductions below are over four lanes");
 
 // Codes of a lane's 8 values and the scale (bf16 bits) of its group.  Beside the
-// products they cost little: 16384 rows, 7168 x 2 x 2048: 799 us, 789 with g and u in
-// bf16, 774 with none kept; the backward pass 433 us and 429, 447 where it writes
-// act(g) u again; 8192 rows, 2048 x 2 x 1040: 87.5 us, 89.1, 85.6, and 58.8, 68.4, 59.8.
+// products they cost little: 16384 rows, 7168 x 2 x 2048: 801 to 810 us, 786 to 796 with
+// g and u in bf16, 775 to 802 with none kept; the backward pass 428 to 440 us and 425 to
+// 432, 441 to 447 where it writes act(g) u again; 8192 rows, 2048 x 2 x 1040: 93 to 95 us,
+// 93, 90, and 63.5, 73, 64.  (Sixteen of the large ones in a row pull the clock down to
+// 870 and 473 us.)
 __device__ __forceinline__ u32x2 keep8(const float (&v)[8], uint16_t* scale) {
   uint32_t m = 0;
 #pragma unroll
